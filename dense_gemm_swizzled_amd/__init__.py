@@ -11,11 +11,14 @@ Two layers:
   ``mx_scales_to_blocks``, ``mx_gemm_blocks_run``, ``gemm_layout_run``,
   ``gemm_layout128_run``, ``gemm_last_error``, ``gemm_version``,
   ``gemm_lds_layout``, ``gemm_lds_layout_mxfp6``, ``gemm_lds_layout_cblock``,
-  ``gemm_lds_image``: the C entry points under the same names, taking integer
-  device pointers.
+  ``gemm_lds_image``, ``i8_gemm_run``, ``i8_grouped_gemm_run``, ``i8_quant_run``,
+  ``moe_route_run``, ``moe_route_backward_run``, ``moe_plan_run``,
+  ``moe_plan_workspace_bytes``: the C entry points under the same names, taking
+  integer device pointers.
 * ``gemm``, ``gemm_strided``, ``grouped_gemm``, ``mx_gemm``, ``mxfp4_gemm``,
   ``mxfp6_gemm``, ``mx_scales_blocks``, ``mx_gemm_blocks``, ``gemm_layout``,
-  ``gemm_layout128``: the same calls on torch CUDA
+  ``gemm_layout128``, ``i8_gemm``, ``i8_grouped_gemm``, ``i8_quant``,
+  ``moe_route``, ``moe_route_backward``, ``moe_plan``: the same calls on torch CUDA
   tensors (shapes read from the tensors, output allocated by torch, launched
   on torch's current stream).
 """
@@ -41,6 +44,11 @@ __all__ = [
     "gemm", "gemm_plan", "gemm_strided", "grouped_gemm", "mx_gemm", "mxfp4_gemm", "mxfp6_gemm",
     "gemm_layout", "gemm_layout_io", "gemm_layout_io_run",
     "gemm_layout128", "SG_LAYOUT_PAD16",
+    "i8_gemm_run", "i8_grouped_gemm_run", "i8_quant_run", "moe_route_run",
+    "moe_route_backward_run", "moe_plan_run", "moe_plan_workspace_bytes",
+    "i8_gemm", "i8_grouped_gemm", "i8_quant", "moe_route", "moe_route_backward", "moe_plan",
+    "SG_SCORE_SOFTMAX", "SG_SCORE_SIGMOID", "SG_GROUP_MAX", "SG_GROUP_TOP2", "SG_MAX_TOP_K",
+    "SG_MAX_ROUTE_GROUPS",
     "library_path", "load",
 ]
 
@@ -51,6 +59,9 @@ SG_SF_ROWS, SG_SF_BLOCKS = 0, 1
 SG_K_MAJOR, SG_MN_MAJOR = 0, 1
 SG_MAX_GROUPS = 256
 SG_LAYOUT_PAD16 = -1
+SG_SCORE_SOFTMAX, SG_SCORE_SIGMOID = 0, 1
+SG_GROUP_MAX, SG_GROUP_TOP2 = 0, 1
+SG_MAX_TOP_K, SG_MAX_ROUTE_GROUPS = 32, 32
 ERRORS = {-1: "SG_ERR_NULL", -2: "SG_ERR_ALIGN", -3: "SG_ERR_SHAPE",
           -4: "SG_ERR_DTYPE", -5: "SG_ERR_MAJOR", -6: "SG_ERR_GROUPS",
           -7: "SG_ERR_HIP"}
@@ -106,7 +117,19 @@ def load():
     lib.mx_scales_blocks_bytes.restype = ctypes.c_int64
     lib.mx_scales_to_blocks.argtypes = [vp, i64, i64, vp, vp]
     lib.mx_gemm_blocks_run.argtypes = [i32, i64, i64, i64, vp, vp, vp, vp, vp, i32, vp]
-    for f in (lib.mx_scales_to_blocks, lib.mx_gemm_blocks_run, lib.gemm_run, lib.gemm_strided_run, lib.grouped_gemm_run, lib.mx_gemm_run,
+    lib.i8_gemm_run.argtypes = [i64, i64, i64, vp, i64, vp, vp, i64, vp, vp, i64, i32, vp]
+    lib.i8_grouped_gemm_run.argtypes = [i32, i64, i64, i64, vp, vp, i64, i64, vp, vp, vp, vp, vp,
+                                        i64, i32, vp]
+    lib.i8_quant_run.argtypes = [i64, i64, vp, i64, i32, vp, i64, vp, vp]
+    lib.moe_route_run.argtypes = [i64, i32, i32, vp, i64, i32, vp, i32, i32, i32, i32, i32, f32,
+                                  vp, vp, vp]
+    lib.moe_route_backward_run.argtypes = [i64, i32, i32, vp, vp, i64, i32, vp, i32, i32, f32, vp,
+                                           i64, vp]
+    lib.moe_plan_run.argtypes = [i64, i32, i32, vp, vp, vp, vp, vp, i64, vp]
+    lib.moe_plan_workspace_bytes.argtypes = [i64, i32]
+    lib.moe_plan_workspace_bytes.restype = ctypes.c_int64
+    for f in (lib.i8_gemm_run, lib.i8_grouped_gemm_run, lib.i8_quant_run, lib.moe_route_run,
+              lib.moe_route_backward_run, lib.moe_plan_run, lib.mx_scales_to_blocks, lib.mx_gemm_blocks_run, lib.gemm_run, lib.gemm_strided_run, lib.grouped_gemm_run, lib.mx_gemm_run,
               lib.mxfp4_gemm_run, lib.mxfp6_gemm_run,
               lib.gemm_layout_run, lib.gemm_layout128_run, lib.gemm_layout_io_run,
               lib.gemm_lds_layout, lib.gemm_lds_layout_mxfp6, lib.gemm_lds_layout_cblock,
@@ -183,6 +206,42 @@ def gemm_layout_io_run(operand_swz, output_swz, M, N, K, A, B, C, c_dtype, D, d_
 
 def gemm_layout128_run(layout, M, N, K, A, B, C, c_dtype, D, d_dtype, stream) -> int:
     return load().gemm_layout128_run(layout, M, N, K, A, B, C, c_dtype, D, d_dtype, stream)
+
+
+def i8_gemm_run(M, N, K, A, lda, SA, B, ldb, SB, D, ldd, d_dtype, stream) -> int:
+    return load().i8_gemm_run(M, N, K, A, lda, SA, B, ldb, SB, D, ldd, d_dtype, stream)
+
+
+def i8_grouped_gemm_run(G, R, N, K, offsets, A, lda, a_rows, rows, SA, B, SB, D, ldd, d_dtype,
+                        stream) -> int:
+    return load().i8_grouped_gemm_run(G, R, N, K, offsets, A, lda, a_rows, rows, SA, B, SB, D,
+                                      ldd, d_dtype, stream)
+
+
+def i8_quant_run(R, K, X, ldx, x_dtype, Q, ldq, S, stream) -> int:
+    return load().i8_quant_run(R, K, X, ldx, x_dtype, Q, ldq, S, stream)
+
+
+def moe_route_run(T, E, top_k, logits, ldl, dtype, bias, score, n_groups, top_groups,
+                  group_score, renorm, scale, weights, ids, stream) -> int:
+    return load().moe_route_run(T, E, top_k, logits, ldl, dtype, bias, score, n_groups,
+                                top_groups, group_score, renorm, scale, weights, ids, stream)
+
+
+def moe_route_backward_run(T, E, top_k, dweights, logits, ldl, dtype, ids, score, renorm, scale,
+                           dlogits, lddl, stream) -> int:
+    return load().moe_route_backward_run(T, E, top_k, dweights, logits, ldl, dtype, ids, score,
+                                         renorm, scale, dlogits, lddl, stream)
+
+
+def moe_plan_run(T, E, top_k, ids, offsets, rows, slots, workspace, workspace_bytes,
+                 stream) -> int:
+    return load().moe_plan_run(T, E, top_k, ids, offsets, rows, slots, workspace,
+                               workspace_bytes, stream)
+
+
+def moe_plan_workspace_bytes(P, E) -> int:
+    return load().moe_plan_workspace_bytes(P, E)
 
 
 def gemm_last_error() -> str:
@@ -648,3 +707,287 @@ def mxfp6_gemm(A, SFA, B, SFB, *, fmt: str = "e2m3", out_dtype=None, out=None):
     _check(mxfp6_gemm_run(code, M, N, K, A.data_ptr(), SFA.data_ptr(), B.data_ptr(),
                           SFB.data_ptr(), out.data_ptr(), _dt(out.dtype), _stream(A.device)))
     return out
+
+
+# ---------------------------------------------- 8-bit products, expert routing
+#
+# These calls launch on the tensors' device even when another is current.
+
+class _OnDevice:
+    """Makes `device` current for a launch (most calls find it current)."""
+    __slots__ = ("device", "guard")
+
+    def __init__(self, device):
+        self.device = device
+
+    def __enter__(self):
+        import torch
+        self.guard = None
+        if torch.cuda.current_device() != self.device.index:
+            self.guard = torch.cuda.device(self.device)
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _vector(name: str, t, n: int, dtypes) -> None:
+    """t is a packed vector of n elements."""
+    _need(t.dim() == 1 and t.shape[0] == n, -3,
+          f"{name} has shape {tuple(t.shape)}, expected ({n},)")
+    _dtype_is(name, t, dtypes)
+    _need(n <= 1 or t.stride(0) == 1, -2, f"{name} must be contiguous")
+
+
+def _rows2d(name: str, t) -> int:
+    """The row stride of a 2-D tensor with unit column stride."""
+    _need(t.dim() == 2, -3, f"{name} must be 2-D, got shape {tuple(t.shape)}")
+    rows, cols = t.shape
+    _need(cols <= 1 or t.stride(1) == 1, -2, f"{name} must have unit column stride; strides "
+                                             f"{tuple(t.stride())}")
+    if rows <= 1:  # the stride of a single row says nothing
+        return max(int(cols), 1)
+    _need(t.stride(0) >= cols, -2, f"{name} must have a row stride of at least its width; "
+                                   f"strides {tuple(t.stride())}")
+    return max(int(t.stride(0)), 1)
+
+
+def _out_rows(out, R: int, N: int, out_dtype, device):
+    """(out, ldd): `out` checked as [R][N] with padded rows, or a new tensor."""
+    import torch
+    if out is None:
+        return torch.empty((R, N), dtype=out_dtype or torch.bfloat16, device=device), N
+    _shape("out", out, (R, N))
+    _dtype_is("out", out, (torch.float32, torch.bfloat16, torch.float16))
+    return out, _rows2d("out", out)
+
+
+def _i8_pitch(name: str, t, K: int) -> int:
+    """The row pitch of codes: K rounded up to 16 where no second row tells it."""
+    import torch
+    _dtype_is(name, t, (torch.int8,))
+    ld = _rows2d(name, t)
+    return ld if t.shape[0] > 1 and K > 0 else -(-K // 16) * 16
+
+
+def i8_quant(X, *, out=None, out_scale=None):
+    """X [R][K] (float32, bfloat16 or float16, unit column stride) as 8-bit
+    codes with one scale per row: (codes int8 [R][Kp], scales float32 [R]), Kp
+    = K rounded up to 16, the columns behind K zero.  X is about codes *
+    scales[:, None]; scale = max|x| / 127.  A row with an infinity or a NaN has
+    the scale NaN.  out: int8 [R][Kp] whose row stride is a multiple of 16."""
+    import torch
+    ldx = _rows2d("X", X)
+    R, K = (int(n) for n in X.shape)
+    _dtype_is("X", X, (torch.float32, torch.bfloat16, torch.float16))
+    Kp = -(-K // 16) * 16
+    ldq = Kp
+    if out is not None:
+        _shape("out", out, (R, Kp))
+        ldq = _i8_pitch("out", out, K)
+    if out_scale is not None:
+        _vector("out_scale", out_scale, R, (torch.float32,))
+    _one_device(("X", X), ("out", out), ("out_scale", out_scale))
+    if out is None:
+        out = torch.empty((R, Kp), dtype=torch.int8, device=X.device)
+    if out_scale is None:
+        out_scale = torch.empty(R, dtype=torch.float32, device=X.device)
+    with _OnDevice(X.device):
+        _check(i8_quant_run(R, K, X.data_ptr(), ldx, _dt(X.dtype), out.data_ptr(), ldq,
+                            out_scale.data_ptr(), _stream(X.device)))
+    return out, out_scale
+
+
+def i8_gemm(A, SA, B, SB, *, out_dtype=None, out=None):
+    """D[m][n] = SA[m] * SB[n] * sum_k A[m][k] * B[n][k] for int8 A [M][K] and
+    B [N][K] and float32 scales SA [M], SB [N]; returns D [M][N] of out_dtype
+    (default torch.bfloat16), or writes `out`.  K is a multiple of 16 (i8_quant
+    pads); rows of A, B and out may be padded."""
+    import torch
+    _need(A.dim() == 2 and B.dim() == 2, -3, "A and B must be 2-D")
+    M, K = (int(n) for n in A.shape)
+    N = int(B.shape[0])
+    _need(B.shape[1] == K, -3, f"A and B disagree on K ({K} vs {B.shape[1]})")
+    lda, ldb = _i8_pitch("A", A, K), _i8_pitch("B", B, K)
+    _vector("SA", SA, M, (torch.float32,))
+    _vector("SB", SB, N, (torch.float32,))
+    if out is not None:
+        out, ldd = _out_rows(out, M, N, None, None)
+    _one_device(("A", A), ("SA", SA), ("B", B), ("SB", SB), ("out", out))
+    if out is None:
+        out, ldd = _out_rows(None, M, N, out_dtype, A.device)
+    with _OnDevice(A.device):
+        _check(i8_gemm_run(M, N, K, A.data_ptr(), lda, SA.data_ptr(), B.data_ptr(), ldb,
+                           SB.data_ptr(), out.data_ptr(), ldd, _dt(out.dtype),
+                           _stream(A.device)))
+    return out
+
+
+def i8_grouped_gemm(A, SA, B, SB, offsets, *, rows=None, out_dtype=None, out=None):
+    """i8_gemm for G experts whose row ranges are on the device: row r of D,
+    offsets[g] <= r < offsets[g+1], is A's row rows[r] (or r) times B[g].
+
+    A int8 [T][K], SA [T]; B int8 [G][N][K], SB [G][N]; offsets int32 [G+1] and
+    rows int32 [R] as moe_plan returns them (without rows, R = T).  Returns D
+    [R][N] of out_dtype (default torch.bfloat16), or writes `out`.  Rows at and
+    behind offsets[G] are not written: a new D holds anything there."""
+    import torch
+    _need(A.dim() == 2, -3, f"A must be 2-D, got shape {tuple(A.shape)}")
+    _dense("B", B, dims=3)
+    _dtype_is("B", B, (torch.int8,))
+    G, N, K = (int(n) for n in B.shape)
+    T = int(A.shape[0])
+    _need(A.shape[1] == K, -3, f"A and B disagree on K ({A.shape[1]} vs {K})")
+    lda = _i8_pitch("A", A, K)
+    _vector("SA", SA, T, (torch.float32,))
+    _dense("SB", SB)
+    _shape("SB", SB, (G, N))
+    _dtype_is("SB", SB, (torch.float32,))
+    _vector("offsets", offsets, G + 1, (torch.int32,))
+    R = T
+    if rows is not None:
+        _need(rows.dim() == 1, -3, f"rows must be 1-D, got shape {tuple(rows.shape)}")
+        R = int(rows.shape[0])
+        _vector("rows", rows, R, (torch.int32,))
+    if out is not None:
+        out, ldd = _out_rows(out, R, N, None, None)
+    _one_device(("A", A), ("SA", SA), ("B", B), ("SB", SB), ("offsets", offsets), ("rows", rows),
+                ("out", out))
+    if out is None:
+        out, ldd = _out_rows(None, R, N, out_dtype, A.device)
+    with _OnDevice(A.device):
+        _check(i8_grouped_gemm_run(G, R, N, K, offsets.data_ptr(), A.data_ptr(), lda, T,
+                                   None if rows is None else rows.data_ptr(), SA.data_ptr(),
+                                   B.data_ptr(), SB.data_ptr(), out.data_ptr(), ldd,
+                                   _dt(out.dtype), _stream(A.device)))
+    return out
+
+
+_SCORES = {"softmax": SG_SCORE_SOFTMAX, "sigmoid": SG_SCORE_SIGMOID}
+_GROUP_SCORES = {"max": SG_GROUP_MAX, "top2": SG_GROUP_TOP2}
+
+
+def _route_args(logits, score):
+    import torch
+    ldl = _rows2d("logits", logits)
+    _dtype_is("logits", logits, (torch.float32, torch.bfloat16, torch.float16))
+    _need(score in _SCORES, -4, f"score must be one of {sorted(_SCORES)}, got {score!r}")
+    return int(logits.shape[0]), int(logits.shape[1]), ldl
+
+
+def moe_route(logits, top_k: int, *, score: str = "softmax", bias=None, n_groups: int = 1,
+              top_groups: Optional[int] = None, group_score: str = "max", renorm: bool = True,
+              scale: float = 1.0, out=None):
+    """The top_k experts of each token and their weights, from router logits
+    [T][E]: (weights float32 [T][top_k], ids int32 [T][top_k]).
+
+    Experts are chosen by score + bias (bias float32 [E]; softmax or sigmoid
+    scores), within the top_groups best of n_groups equal groups; among equal
+    ones the lowest index.  Weights are the scores of the chosen ones (without
+    the bias), divided by their sum (renorm), times scale.  Logits of -inf or
+    NaN are masked; a token with no expert left has ids -1 and weights 0.
+    out: (weights, ids) to write."""
+    import torch
+    T, E, ldl = _route_args(logits, score)
+    top_k, n_groups = int(top_k), int(n_groups)
+    top_groups = n_groups if top_groups is None else int(top_groups)
+    _need(group_score in _GROUP_SCORES, -6,
+          f"group_score must be one of {sorted(_GROUP_SCORES)}, got {group_score!r}")
+    _need(1 <= top_k <= min(E, SG_MAX_TOP_K), -3, f"top_k={top_k} outside 1..min({E}, "
+                                                  f"{SG_MAX_TOP_K})")
+    if bias is not None:
+        _vector("bias", bias, E, (torch.float32,))
+    weights = ids = None
+    if out is not None:
+        weights, ids = out
+        for name, t, dt in (("weights", weights, torch.float32), ("ids", ids, torch.int32)):
+            _dense(name, t)
+            _shape(name, t, (T, top_k))
+            _dtype_is(name, t, (dt,))
+    _one_device(("logits", logits), ("bias", bias), ("weights", weights), ("ids", ids))
+    if out is None:
+        weights = torch.empty((T, top_k), dtype=torch.float32, device=logits.device)
+        ids = torch.empty((T, top_k), dtype=torch.int32, device=logits.device)
+    with _OnDevice(logits.device):
+        _check(moe_route_run(T, E, top_k, logits.data_ptr(), ldl, _dt(logits.dtype),
+                             None if bias is None else bias.data_ptr(), _SCORES[score], n_groups,
+                             top_groups, _GROUP_SCORES[group_score], int(bool(renorm)),
+                             float(scale), weights.data_ptr(), ids.data_ptr(),
+                             _stream(logits.device)))
+    return weights, ids
+
+
+def moe_route_backward(dweights, logits, ids, *, score: str = "softmax", renorm: bool = True,
+                       scale: float = 1.0, out=None):
+    """The gradient of the logits [T][E] (their type) from dweights float32
+    [T][top_k], the gradient of moe_route's weights, and its ids."""
+    import torch
+    T, E, ldl = _route_args(logits, score)
+    _dense("ids", ids)
+    top_k = int(ids.shape[1])
+    _shape("ids", ids, (T, top_k))
+    _dtype_is("ids", ids, (torch.int32,))
+    _dense("dweights", dweights)
+    _shape("dweights", dweights, (T, top_k))
+    _dtype_is("dweights", dweights, (torch.float32,))
+    lddl = E
+    if out is not None:
+        _shape("out", out, (T, E))
+        _dtype_is("out", out, (logits.dtype,))
+        lddl = _rows2d("out", out)
+    _one_device(("dweights", dweights), ("logits", logits), ("ids", ids), ("out", out))
+    if out is None:
+        out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    with _OnDevice(logits.device):
+        _check(moe_route_backward_run(T, E, top_k, dweights.data_ptr(), logits.data_ptr(), ldl,
+                                      _dt(logits.dtype), ids.data_ptr(), _SCORES[score],
+                                      int(bool(renorm)), float(scale), out.data_ptr(), lddl,
+                                      _stream(logits.device)))
+    return out
+
+
+def moe_plan(ids, n_experts: int, *, out=None, workspace=None):
+    """The (token, expert) pairs of ids int32 [T][top_k] sorted by expert,
+    stably: (offsets int32 [E+1], rows int32 [T*top_k], slots int32 [T][top_k]).
+    Expert e's sorted rows are offsets[e]:offsets[e+1], rows[r] is the token of
+    sorted row r (-1 behind offsets[E]) and slots[t][j] the sorted row of pair
+    (t, j), -1 where its id is outside [0, E).
+
+    out: (offsets, rows, slots) to write.  workspace: a uint8 tensor of at
+    least moe_plan_workspace_bytes(T * top_k, E) bytes; by default one is
+    allocated for the call."""
+    import torch
+    _dense("ids", ids)
+    _dtype_is("ids", ids, (torch.int32,))
+    T, top_k = (int(n) for n in ids.shape)
+    E, P = int(n_experts), T * top_k
+    need = int(moe_plan_workspace_bytes(P, E))
+    _check(need if need < 0 else 0)
+    offsets = rows = slots = None
+    if out is not None:
+        offsets, rows, slots = out
+        _vector("offsets", offsets, E + 1, (torch.int32,))
+        _vector("rows", rows, P, (torch.int32,))
+        _dense("slots", slots)
+        _shape("slots", slots, (T, top_k))
+        _dtype_is("slots", slots, (torch.int32,))
+    if workspace is not None:
+        _dense("workspace", workspace, 1)
+        _dtype_is("workspace", workspace, (torch.uint8,))
+        _need(workspace.shape[0] >= need, -3,
+              f"workspace has {workspace.shape[0]} bytes, {need} are needed")
+    _one_device(("ids", ids), ("offsets", offsets), ("rows", rows), ("slots", slots),
+                ("workspace", workspace))
+    dev = ids.device
+    if out is None:
+        offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
+        rows = torch.empty(P, dtype=torch.int32, device=dev)
+        slots = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+    if workspace is None and need > 0:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    with _OnDevice(dev):
+        _check(moe_plan_run(T, E, top_k, ids.data_ptr(), offsets.data_ptr(), rows.data_ptr(),
+                            slots.data_ptr(), None if need == 0 else workspace.data_ptr(), need,
+                            _stream(dev)))
+    return offsets, rows, slots

@@ -16,7 +16,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libswizzled_gemm.so")
-SOURCES = ["api.hip", "launch_dense.hip", "launch_mx.hip", "diag.hip"]
+SOURCES = ["api.hip", "launch_dense.hip", "launch_mx.hip", "launch_i8.hip", "moe.hip", "quant.hip",
+           "diag.hip"]
 ARCH = "gfx950"
 
 FLAGS = [

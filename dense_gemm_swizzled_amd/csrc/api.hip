@@ -10,8 +10,10 @@
 #include <string>
 
 #include "../../include/swizzled_gemm.h"
+#include "i8_params.h"
 #include "launch.h"
 #include "lds_layout.h"
+#include "moe.h"
 
 namespace {
 
@@ -473,6 +475,308 @@ int mx_scales_to_blocks(const void* SF, int64_t rows, int64_t K, void* out, void
     return fail(SG_ERR_SHAPE, "mx_scales_to_blocks: too many rows or K blocks");
   hipError_t e = sg::launch_sf_blocks(SF, rows, K, out, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail(e, "mx_scales_to_blocks launch");
+  return ok();
+}
+
+namespace {
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+constexpr int64_t kI8MaxK = 131056;  // 2^14 * K < 2^31, K a multiple of 16
+
+int64_t i8_tile_rows(sg::I8Tile t) {
+  switch (t) {
+    case sg::kI8Skinny16: return 16;
+    case sg::kI8Skinny32: return 32;
+    case sg::kI8Skinny64: return 64;
+    case sg::kI8Tile64: return 64;
+    case sg::kI8Tile128: return 128;
+    default: return 256;
+  }
+}
+
+bool i8_skinny(sg::I8Tile t) {
+  return t == sg::kI8Skinny16 || t == sg::kI8Skinny32 || t == sg::kI8Skinny64;
+}
+
+// The kernel of a dense 8-bit product.
+sg::I8Tile pick_i8_tile(int64_t M, int64_t N, bool fits256) {
+  if (M <= 16) return sg::kI8Skinny16;
+  if (M <= 32) return sg::kI8Skinny32;
+  if (M <= 64) return sg::kI8Skinny64;
+  if (fits256 && cdiv(M, 256) * cdiv(N, 256) >= kCUs) return sg::kI8Tile256;
+  if (cdiv(M, 128) * cdiv(N, 128) >= kCUs / 2) return sg::kI8Tile128;
+  return sg::kI8Tile64;
+}
+
+// The kernel of a grouped 8-bit product, from the groups' mean rows: the
+// offsets themselves are in device memory.
+sg::I8Tile pick_i8_grouped_tile(int64_t R, int64_t G, int64_t N, bool fits256) {
+  const int64_t mean = cdiv(R, G);
+  if (mean <= 12) return sg::kI8Skinny16;
+  if (mean <= 24) return sg::kI8Skinny32;
+  if (mean <= 64) return sg::kI8Skinny64;
+  if (fits256 && mean >= 192 && cdiv(R, 256) * cdiv(N, 256) >= kCUs) return sg::kI8Tile256;
+  return sg::kI8Tile128;
+}
+
+// The shared checks and launch of the 8-bit products; G = 0: dense.
+int i8_run(const char* who, int G, int64_t M, int64_t N, int64_t K, const int32_t* offsets,
+           const void* A, int64_t lda, const int32_t* rows, int64_t a_rows, const float* SA,
+           const void* B, int64_t ldb, const float* SB, void* D, int64_t ldd, int d_dtype,
+           void* stream) {
+  if (M < 0 || N < 0 || K < 0 || a_rows < 0)
+    return fail(SG_ERR_SHAPE, "%s: negative size M=%lld N=%lld K=%lld", who, (long long)M,
+                (long long)N, (long long)K);
+  if (!is_out_dtype(d_dtype))
+    return fail(SG_ERR_DTYPE, "%s: d_dtype %d is not SG_F32/SG_BF16/SG_F16", who, d_dtype);
+  if (K % 16 || K > kI8MaxK)
+    return fail(SG_ERR_SHAPE, "%s: K=%lld is not a multiple of 16 up to %lld", who, (long long)K,
+                (long long)kI8MaxK);
+  if (lda < K || ldb < K || ldd < N)
+    return fail(SG_ERR_SHAPE, "%s: a leading dimension is below its minimum (lda %lld, ldb %lld, "
+                              "ldd %lld)", who, (long long)lda, (long long)ldb, (long long)ldd);
+  if (M >= kMaxExtent || N >= kMaxExtent || a_rows >= kMaxExtent)
+    return fail(SG_ERR_SHAPE, "%s: 2^31 rows or columns or more", who);
+  if (M == 0 || N == 0) return ok();
+  if (!D || (G > 0 && !offsets)) return fail(SG_ERR_NULL, "%s: D or offsets is NULL", who);
+  const bool no_a = rows && a_rows == 0;  // no index names a row
+  if ((K > 0 && !no_a && !A) || (K > 0 && !B) || (!no_a && !SA) || !SB)
+    return fail(SG_ERR_NULL, "%s: A, B, SA or SB is NULL", who);
+  const int db = elem_bytes(d_dtype);
+  if ((K > 0 && (!aligned16(A) || !aligned16(B))) || !aligned4(SA) || !aligned4(SB) ||
+      !aligned4(offsets) || !aligned4(rows) || reinterpret_cast<uintptr_t>(D) % db)
+    return fail(SG_ERR_ALIGN, "%s: A and B must be 16-byte aligned, the other pointers to their "
+                              "elements", who);
+  if (lda % 16 || ldb % 16)
+    return fail(SG_ERR_ALIGN, "%s: the row pitches of A and B must be multiples of 16 bytes", who);
+  if (rows && a_rows > 0 && (a_rows - 1) * lda + K >= kMaxExtent)
+    return fail(SG_ERR_SHAPE, "%s: gathered A spans 2^31 bytes or more", who);
+  const bool fits256 = 256 * lda < kMaxExtent && 256 * ldb < kMaxExtent;
+  const sg::I8Tile tile = G == 0 ? pick_i8_tile(M, N, fits256)
+                                 : pick_i8_grouped_tile(M, G, N, fits256);
+  const int64_t T = i8_tile_rows(tile);
+  sg::I8Params p;
+  p.wk = 1;
+  int64_t tn = T;
+  if (i8_skinny(tile)) {
+    // Each wave takes a K range of 512 bytes or more.
+    p.wk = 8;
+    while (p.wk > 1 && K < 512 * p.wk) p.wk /= 2;
+    tn = (tile == sg::kI8Skinny64 ? 256 : 128) / p.wk;
+  }
+  if ((T > tn ? T : tn) * (lda > ldb ? lda : ldb) >= kMaxExtent)
+    return fail(SG_ERR_SHAPE, "%s: an operand panel spans 2^31 bytes or more", who);
+  const int64_t tiles_n = cdiv(N, tn);
+  // Row tiles: every group may end in a partial one.
+  const int64_t groups = G == 0 ? 1 : G < M ? G : M;
+  const int64_t tiles_m = G == 0 ? cdiv(M, T) : (M + groups * (T - 1)) / T;
+  if (tiles_m * tiles_n > 0x7fffffffLL) return fail(SG_ERR_SHAPE, "%s: too many tiles", who);
+  p.A = A;
+  p.B = B;
+  p.SA = SA;
+  p.SB = SB;
+  p.D = D;
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.lda = lda;
+  p.ldb = ldb;
+  p.ldd = ldd;
+  p.d_dtype = d_dtype;
+  p.vec = aligned16(D) && (ldd * db) % 16 == 0;
+  p.tiles_m = (int)tiles_m;
+  p.tiles_n = (int)tiles_n;
+  p.group_m = kGroupM;
+  p.clk = g_clk;
+  p.G = G;
+  p.offsets = offsets;
+  p.rows = rows;
+  p.a_total = (int)a_rows;
+  const hipError_t e = sg::launch_i8(tile, p, (int)(tiles_m * tiles_n),
+                                     static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, who);
+  return ok();
+}
+
+// The checks that the forward and backward routing share.
+int route_check(const char* who, int64_t T, int E, int top_k, const void* logits, int64_t ldl,
+                int dtype, int score) {
+  if (T < 0 || T >= kMaxExtent || E < 1 || E > SG_MAX_GROUPS || top_k < 1 || top_k > E ||
+      top_k > SG_MAX_TOP_K)
+    return fail(SG_ERR_SHAPE, "%s: T=%lld, E=%d (1..%d), top_k=%d (1..min(E, %d))", who,
+                (long long)T, E, SG_MAX_GROUPS, top_k, SG_MAX_TOP_K);
+  if (!is_out_dtype(dtype))
+    return fail(SG_ERR_DTYPE, "%s: dtype %d is not SG_F32/SG_BF16/SG_F16", who, dtype);
+  if (score != SG_SCORE_SOFTMAX && score != SG_SCORE_SIGMOID)
+    return fail(SG_ERR_DTYPE, "%s: score %d is not SG_SCORE_SOFTMAX/SG_SCORE_SIGMOID", who, score);
+  if (ldl < E) return fail(SG_ERR_SHAPE, "%s: ldl=%lld is below E=%d", who, (long long)ldl, E);
+  if (T == 0) return SG_OK;
+  if (!logits) return fail(SG_ERR_NULL, "%s: logits is NULL", who);
+  if (reinterpret_cast<uintptr_t>(logits) % elem_bytes(dtype))
+    return fail(SG_ERR_ALIGN, "%s: logits must be aligned to its elements", who);
+  return SG_OK;
+}
+
+// Pairs a workgroup of the plan sorts, and how many workgroups there are.
+int64_t plan_chunk(int64_t P) {
+  if (P <= 4096) return 4096;
+  const int64_t chunk = cdiv(cdiv(P, 256), 1024) * 1024;
+  return chunk;
+}
+
+}  // namespace
+
+int i8_gemm_run(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const float* SA,
+                const void* B, int64_t ldb, const float* SB, void* D, int64_t ldd, int d_dtype,
+                void* stream) {
+  return i8_run("i8_gemm_run", 0, M, N, K, nullptr, A, lda, nullptr, M, SA, B, ldb, SB, D, ldd,
+                d_dtype, stream);
+}
+
+int i8_grouped_gemm_run(int G, int64_t R, int64_t N, int64_t K, const int32_t* offsets,
+                        const void* A, int64_t lda, int64_t a_rows, const int32_t* rows,
+                        const float* SA, const void* B, const float* SB, void* D, int64_t ldd,
+                        int d_dtype, void* stream) {
+  const char* who = "i8_grouped_gemm_run";
+  if (G < 1 || G > SG_MAX_GROUPS)
+    return fail(SG_ERR_GROUPS, "%s: G=%d outside [1, %d]", who, G, SG_MAX_GROUPS);
+  if (!rows && a_rows < R)
+    return fail(SG_ERR_SHAPE, "%s: A has %lld rows, D %lld", who, (long long)a_rows,
+                (long long)R);
+  return i8_run(who, G, R, N, K, offsets, A, lda, rows, a_rows, SA, B, K, SB, D, ldd, d_dtype,
+                stream);
+}
+
+int i8_quant_run(int64_t R, int64_t K, const void* X, int64_t ldx, int x_dtype, void* Q,
+                 int64_t ldq, float* S, void* stream) {
+  const char* who = "i8_quant_run";
+  if (R < 0 || K < 0 || R >= kMaxExtent || K >= kMaxExtent)
+    return fail(SG_ERR_SHAPE, "%s: R=%lld K=%lld", who, (long long)R, (long long)K);
+  if (!is_out_dtype(x_dtype))
+    return fail(SG_ERR_DTYPE, "%s: x_dtype %d is not SG_F32/SG_BF16/SG_F16", who, x_dtype);
+  if (ldx < K || ldq < cdiv(K, 16) * 16)
+    return fail(SG_ERR_SHAPE, "%s: ldx=%lld is below K=%lld, or ldq=%lld below K rounded up to "
+                              "16", who, (long long)ldx, (long long)K, (long long)ldq);
+  if (R == 0) return ok();
+  if ((K > 0 && (!X || !Q)) || !S) return fail(SG_ERR_NULL, "%s: X, Q or S is NULL", who);
+  if (reinterpret_cast<uintptr_t>(X) % elem_bytes(x_dtype) || !aligned4(S) ||
+      (K > 0 && (!aligned16(Q) || ldq % 16)))
+    return fail(SG_ERR_ALIGN, "%s: Q and its row pitch must be 16-byte aligned, X and S to their "
+                              "elements", who);
+  hipError_t e = sg::launch_i8_quant(X, R, K, ldx, x_dtype, Q, ldq, S,
+                                     static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, who);
+  return ok();
+}
+
+int moe_route_run(int64_t T, int E, int top_k, const void* logits, int64_t ldl, int dtype,
+                  const float* bias, int score, int n_groups, int top_groups, int group_score,
+                  int renorm, float scale, float* weights, int32_t* ids, void* stream) {
+  const char* who = "moe_route_run";
+  if (const int rc = route_check(who, T, E, top_k, logits, ldl, dtype, score)) return rc;
+  if (n_groups < 1 || n_groups > SG_MAX_ROUTE_GROUPS || E % n_groups || top_groups < 1 ||
+      top_groups > n_groups)
+    return fail(SG_ERR_GROUPS, "%s: n_groups=%d (1..%d, dividing E=%d), top_groups=%d", who,
+                n_groups, SG_MAX_ROUTE_GROUPS, E, top_groups);
+  if (group_score != SG_GROUP_MAX && group_score != SG_GROUP_TOP2)
+    return fail(SG_ERR_GROUPS, "%s: group_score %d is not SG_GROUP_MAX/SG_GROUP_TOP2", who,
+                group_score);
+  if (top_k > top_groups * (E / n_groups))
+    return fail(SG_ERR_GROUPS, "%s: top_k=%d is more than the %d experts of %d groups", who, top_k,
+                top_groups * (E / n_groups), top_groups);
+  if (T == 0) return ok();
+  if (!weights || !ids) return fail(SG_ERR_NULL, "%s: weights or ids is NULL", who);
+  if (!aligned4(weights) || !aligned4(ids) || !aligned4(bias))
+    return fail(SG_ERR_ALIGN, "%s: weights, ids and bias must be 4-byte aligned", who);
+  sg::RouteParams p{};
+  p.T = T;
+  p.E = E;
+  p.top_k = top_k;
+  p.logits = logits;
+  p.ldl = ldl;
+  p.bias = bias;
+  p.score = score;
+  p.n_groups = top_groups == n_groups ? 1 : n_groups;  // every group kept: no choice
+  p.top_groups = top_groups;
+  p.group_score = group_score;
+  p.renorm = renorm;
+  p.scale = scale;
+  p.by_score = bias || (p.n_groups > 1 && group_score == SG_GROUP_TOP2);
+  p.weights = weights;
+  p.ids = ids;
+  hipError_t e = sg::launch_moe_route(dtype, p, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, who);
+  return ok();
+}
+
+int moe_route_backward_run(int64_t T, int E, int top_k, const float* dweights, const void* logits,
+                           int64_t ldl, int dtype, const int32_t* ids, int score, int renorm,
+                           float scale, void* dlogits, int64_t lddl, void* stream) {
+  const char* who = "moe_route_backward_run";
+  if (const int rc = route_check(who, T, E, top_k, logits, ldl, dtype, score)) return rc;
+  if (lddl < E) return fail(SG_ERR_SHAPE, "%s: lddl=%lld is below E=%d", who, (long long)lddl, E);
+  if (T == 0) return ok();
+  if (!dweights || !ids || !dlogits)
+    return fail(SG_ERR_NULL, "%s: dweights, ids or dlogits is NULL", who);
+  if (!aligned4(dweights) || !aligned4(ids) ||
+      reinterpret_cast<uintptr_t>(dlogits) % elem_bytes(dtype))
+    return fail(SG_ERR_ALIGN, "%s: every pointer must be aligned to its elements", who);
+  sg::RouteParams p{};
+  p.T = T;
+  p.E = E;
+  p.top_k = top_k;
+  p.logits = logits;
+  p.ldl = ldl;
+  p.score = score;
+  p.renorm = renorm;
+  p.scale = scale;
+  p.ids = const_cast<int32_t*>(ids);
+  p.dweights = dweights;
+  p.dlogits = dlogits;
+  p.lddl = lddl;
+  hipError_t e = sg::launch_moe_route_backward(dtype, p, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, who);
+  return ok();
+}
+
+int64_t moe_plan_workspace_bytes(int64_t P, int E) {
+  if (P < 0 || P >= kMaxExtent || E < 1 || E > SG_MAX_GROUPS)
+    return fail(SG_ERR_SHAPE, "moe_plan_workspace_bytes: P=%lld E=%d", (long long)P, E);
+  const int64_t blocks = cdiv(P, plan_chunk(P));
+  return blocks <= 1 ? 0 : blocks * (E + 1) * 4;
+}
+
+int moe_plan_run(int64_t T, int E, int top_k, const int32_t* ids, int32_t* offsets, int32_t* rows,
+                 int32_t* slots, void* workspace, int64_t workspace_bytes, void* stream) {
+  const char* who = "moe_plan_run";
+  if (T < 0 || T >= kMaxExtent || E < 1 || E > SG_MAX_GROUPS || top_k < 1 ||
+      top_k > SG_MAX_GROUPS || T * top_k >= kMaxExtent)
+    return fail(SG_ERR_SHAPE, "%s: T=%lld, E=%d (1..%d), top_k=%d (1..%d), T * top_k below 2^31",
+                who, (long long)T, E, SG_MAX_GROUPS, top_k, SG_MAX_GROUPS);
+  const int64_t P = T * top_k;
+  if (!offsets || (P > 0 && (!ids || !rows || !slots)))
+    return fail(SG_ERR_NULL, "%s: ids, offsets, rows or slots is NULL", who);
+  if (!aligned4(ids) || !aligned4(offsets) || !aligned4(rows) || !aligned4(slots) ||
+      !aligned4(workspace))
+    return fail(SG_ERR_ALIGN, "%s: every pointer must be 4-byte aligned", who);
+  const int64_t need = moe_plan_workspace_bytes(P, E);
+  if (workspace_bytes < need)
+    return fail(SG_ERR_SHAPE, "%s: the workspace has %lld bytes, %lld are needed", who,
+                (long long)workspace_bytes, (long long)need);
+  if (need > 0 && !workspace) return fail(SG_ERR_NULL, "%s: workspace is NULL", who);
+  sg::PlanParams p;
+  p.P = P;
+  p.E = E;
+  p.top_k = top_k;
+  p.chunk = plan_chunk(P);
+  p.ids = ids;
+  p.offsets = offsets;
+  p.rows = rows;
+  p.slots = slots;
+  p.counts = static_cast<int32_t*>(workspace);
+  hipError_t e = sg::launch_moe_plan(p, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, who);
   return ok();
 }
 

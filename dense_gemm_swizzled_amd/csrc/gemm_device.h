@@ -13,11 +13,20 @@ namespace sg {
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
+typedef int32_t i32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+// Element types of the tile templates (their `Elem` parameter; `true` and
+// `false` of the kernels' IsBF16 are the first two).  An operand tile is rows
+// of 128 bytes of K for all three, so the loaders, the LDS layout and the
+// fragment reads do not depend on the type; i8 has 128 k in those bytes and
+// its accumulators are 32-bit integers kept in the registers of the f32 ones.
+constexpr int kElemF16 = 0, kElemBF16 = 1, kElemI8 = 2;
 
 constexpr int kWaveSize = 64;
 constexpr int kThreads = 256;  // default workgroup: 4 waves
@@ -303,9 +312,14 @@ __device__ __forceinline__ void wait_vmem() {
 // the same K assignment, so the product is independent of how the hardware
 // orders K inside the instruction.
 // ---------------------------------------------------------------------------
-template <bool IsBF16>
+template <int Elem>
 __device__ __forceinline__ f32x16 mfma32x32x16(u32x4 a, u32x4 b, f32x16 c) {
-  if constexpr (IsBF16)
+  if constexpr (Elem == kElemI8)  // v_mfma_i32_32x32x32_i8: the same 16 bytes a lane
+    return __builtin_bit_cast(
+        f32x16, __builtin_amdgcn_mfma_i32_32x32x32_i8(
+                    __builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b),
+                    __builtin_bit_cast(i32x16, c), 0, 0, 0));
+  else if constexpr (Elem == kElemBF16)
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(
         __builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
   else
@@ -316,9 +330,14 @@ __device__ __forceinline__ f32x16 mfma32x32x16(u32x4 a, u32x4 b, f32x16 c) {
 // v_mfma_f32_16x16x32_{bf16,f16}: lane l supplies row l%16 of its operand and
 // the 16-byte K chunk l/16 of the 32-wide K step; lane l receives rows
 // 4(l/16) .. 4(l/16)+3 of column l%16 of the 16x16 result.
-template <bool IsBF16>
+template <int Elem>
 __device__ __forceinline__ f32x4 mfma16x16x32(u32x4 a, u32x4 b, f32x4 c) {
-  if constexpr (IsBF16)
+  if constexpr (Elem == kElemI8)  // v_mfma_i32_16x16x64_i8: the same 16 bytes a lane
+    return __builtin_bit_cast(
+        f32x4, __builtin_amdgcn_mfma_i32_16x16x64_i8(
+                   __builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b),
+                   __builtin_bit_cast(i32x4, c), 0, 0, 0));
+  else if constexpr (Elem == kElemBF16)
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(
         __builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
   else

@@ -93,6 +93,12 @@ struct TileJob {
   int64_t n0;           // first output column
   int64_t ldc;          // leading dimension of C in elements
   float alpha, beta;    // D = alpha * acc + beta * C
+  // The 8-bit products only: D = acc * sa[row] * sb[column].
+  const int32_t* rows;  // A row of each tile row, or NULL: the tile's own rows
+  const float* sa;      // row scales (of A's rows with `rows`, else of the tile's)
+  const float* sb;      // scales of the tile's columns
+  int a_total;          // rows of A (with `rows`)
+  bool vec;             // D's rows are 16-byte aligned
 };
 
 // Epilogue element work shared by every kernel.  One chunk is 4 consecutive
@@ -152,6 +158,68 @@ __device__ __forceinline__ void store_d_chunk(f32x4 v, const c_chunk_t<CD>& c, v
     *reinterpret_cast<f32x4*>(static_cast<float*>(D) + idx) = v;
   else
     *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(D) + idx) = pack_d16<DD>(v);
+}
+
+// 16 bytes of one D row (4 fp32 or 8 16-bit values) of which the first `cols`
+// values exist: one store where D's rows are 16-byte aligned (`vec`) and all
+// of them do, else a store for each value.
+template <class V>
+__device__ __forceinline__ void store_any(V* p, u32x4 d, int cols, bool vec) {
+  constexpr int kN = 16 / sizeof(V);
+  if (vec && cols >= kN) {
+    *reinterpret_cast<u32x4*>(p) = d;
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < kN; ++e) {
+    if (e >= cols) break;
+    // (a copy: __builtin_bit_cast of a vector element reads element 0)
+    const uint32_t w = d[sizeof(V) == 4 ? e : e / 2];
+    if constexpr (sizeof(V) == 4)
+      p[e] = __builtin_bit_cast(V, w);
+    else
+      p[e] = (V)(w >> (16 * (e & 1)));
+  }
+}
+
+// The scale of tile row ml (clamped into the tile) of an 8-bit product.  A
+// gathered row outside A, whose codes read as zero, has the scale zero.
+template <bool Rows>
+__device__ __forceinline__ float i8_row_scale(const TileJob& j, int ml) {
+  ml = min(ml, j.m_valid - 1);
+  if constexpr (!Rows) return j.sa[ml];
+  const int src = j.rows[ml];
+  return (uint32_t)src < (uint32_t)j.a_total ? j.sa[src] : 0.0f;
+}
+
+// Four integer sums of one row (in fp32 registers) scaled.
+__device__ __forceinline__ f32x4 i8_scale4(f32x4 acc, float sa, const float (&sb)[4]) {
+  const i32x4 s = __builtin_bit_cast(i32x4, acc);
+  f32x4 v;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = (float)s[e] * sa * sb[e];
+  return v;
+}
+
+// Four scaled values at element idx of D, of which the first `cols` exist,
+// rounded to D's type.
+__device__ __forceinline__ void store_i8_chunk(f32x4 v, void* D, int d_dtype, int64_t idx,
+                                               int cols, bool vec) {
+  if (d_dtype == SG_F32) {
+    store_any(static_cast<float*>(D) + idx, __builtin_bit_cast(u32x4, v), cols, vec);
+    return;
+  }
+  const u32x2 h = d_dtype == SG_BF16 ? pack_d16<SG_BF16>(v) : pack_d16<SG_F16>(v);
+  uint16_t* p = static_cast<uint16_t*>(D) + idx;
+  if (vec && cols >= 4) {
+    *reinterpret_cast<u32x2*>(p) = h;
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (e >= cols) break;
+    p[e] = (uint16_t)(h[e / 2] >> (16 * (e & 1)));
+  }
 }
 
 // Epilogue of a wave's NI x NJ blocks of 16x16 accumulators (v_mfma_f32_
@@ -240,7 +308,7 @@ __device__ __forceinline__ void epilogue16(const f32x4 (&acc)[NI][NJ], const Til
 // Waves = 4: one wave per SIMD, each wave owns a (BM/2) x (BN/2) block.
 // Waves = 8: two waves per SIMD (the hardware interleaves them, and twice as
 // many waves issue the direct-to-LDS loads), each owning (BM/2) x (BN/4).
-template <int BM, int BN, bool IsBF16, bool AMn, bool BMn, int Swz, int Waves = 4>
+template <int BM, int BN, int Elem, bool AMn, bool BMn, int Swz, int Waves = 4>
 struct GemmTile {
   static constexpr int kBK = 64;            // K elements per stage
   static constexpr int kRowBytes = 128;     // kBK * 2 bytes
@@ -302,7 +370,7 @@ struct GemmTile {
     for (int fm = 0; fm < kFM; ++fm)
 #pragma unroll
       for (int fn = 0; fn < kFN; ++fn)
-        acc[fm][fn] = mfma32x32x16<IsBF16>(f.b[fn], f.a[fm], acc[fm][fn]);
+        acc[fm][fn] = mfma32x32x16<Elem>(f.b[fn], f.a[fm], acc[fm][fn]);
   }
 
   // Instruction-scheduling hints (LLVM AMDGPU sched_group_barrier masks).

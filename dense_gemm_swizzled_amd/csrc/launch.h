@@ -13,6 +13,11 @@ namespace sg {
 
 // Tile shapes the planner chooses between.
 enum TileShape { kTile256 = 0, kTile128 = 1, kTile64 = 2 };
+// The 8-bit products: rows of a tile, and the kernel (see i8_kernels.h).
+enum I8Tile { kI8Skinny16, kI8Skinny32, kI8Skinny64, kI8Tile64, kI8Tile128, kI8Tile256 };
+struct I8Params;
+struct RouteParams;
+struct PlanParams;
 
 // Name of the kernel instantiation this thread launched last (set by every
 // launcher; read through gemm_last_kernel()).
@@ -53,6 +58,15 @@ hipError_t launch_mxfp6(bool e3m2, const MxParams& p, hipStream_t s);  // 256x25
 // e8m0 scales [rows][K/32] (K a multiple of 128) into the blocks layout of
 // SfMap (mx_kernels.h).
 hipError_t launch_sf_blocks(const void* sf, int64_t rows, int64_t K, void* out, hipStream_t s);
+// The 8-bit product, dense (p.G = 0) or grouped; `grid` workgroups.
+hipError_t launch_i8(I8Tile t, const I8Params& p, int grid, hipStream_t s);
+// Rows of floats (SG_F32, SG_BF16, SG_F16) to 8-bit codes and row scales.
+hipError_t launch_i8_quant(const void* X, int64_t R, int64_t K, int64_t ldx, int dtype, void* Q,
+                           int64_t ldq, float* S, hipStream_t s);
+// Expert routing (moe.hip); dtype is the logits'.
+hipError_t launch_moe_route(int dtype, const RouteParams& p, hipStream_t s);
+hipError_t launch_moe_route_backward(int dtype, const RouteParams& p, hipStream_t s);
+hipError_t launch_moe_plan(const PlanParams& p, hipStream_t s);
 // The MFMA clock probe (diag.hip): one wave per SIMD of 256 CUs.
 int clock_probe_waves();
 hipError_t launch_clock_probe(int64_t iters, void* out, hipStream_t s);

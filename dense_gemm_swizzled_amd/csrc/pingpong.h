@@ -153,6 +153,45 @@ struct HalfLoader {
   }
 };
 
+// HalfLoader for a gathered operand: row r of the half is row rows[r] of the
+// source (a source row outside [0, src_rows) reads as zero).  The four rows a
+// lane loads are looked up once per tile job; the loads then cost what
+// HalfLoader's do, since a lane's offset is a register either way.
+template <int Swz>
+struct RowsHalfLoader {
+  uint32_t voff[4];  // row * pitch + chunk byte, or out of range
+  uint32_t chunk;    // byte of K inside the tile (0, 16, ..., 112)
+
+  // `rows`: the half's first entry; rows_valid: entries that exist.
+  __device__ __forceinline__ void init(int w4, int lane, uint32_t row_pitch,
+                                       const int32_t* rows, int rows_valid, int src_rows) {
+    const uint32_t logical = swz_bytes<Swz>((uint32_t)w4 * 1024u + 16u * (uint32_t)lane);
+    const int row = (int)(logical >> 7);
+    chunk = logical & 127u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int src = row + 32 * i < rows_valid ? rows[row + 32 * i] : -1;
+      voff[i] = (uint32_t)src < (uint32_t)src_rows ? (uint32_t)src * row_pitch + chunk
+                                                   : kOutOfRange;
+    }
+  }
+  __device__ __forceinline__ uint32_t offset(int i, uint32_t kbyte0,
+                                             uint32_t kbytes_total) const {
+    return kbyte0 + chunk < kbytes_total ? voff[i] + kbyte0 : kOutOfRange;
+  }
+  __device__ __forceinline__ void issue(u32x4 rsrc, uint32_t half, int w4, int i, int,
+                                        uint32_t kbyte0, uint32_t kbytes_total) const {
+    dma16(rsrc, offset(i, kbyte0, kbytes_total), half + (uint32_t)(4 * i + w4) * 1024u);
+  }
+  __device__ __forceinline__ void prep(uint32_t half, int w4, int i) const {
+    set_m0<0>(half + (uint32_t)(4 * i + w4) * 1024u);
+  }
+  __device__ __forceinline__ void go(u32x4 rsrc, int i, int, uint32_t kbyte0,
+                                     uint32_t kbytes_total) const {
+    dma16_so_m0(rsrc, offset(i, kbyte0, kbytes_total), 0u);
+  }
+};
+
 // The half-tile loader for K a multiple of 64: each lane's four row offsets
 // (out of range for rows past the operand) are fixed per tile job, and the K
 // position of a load travels in the instruction's SGPR offset; a K tile past
@@ -166,6 +205,10 @@ struct KExactHalfLoader {
     for (int i = 0; i < 4; ++i)
       voff[i] = h.row + 32 * i < rows_valid ? h.base + (uint32_t)(32 * i) * h.pitch
                                             : kOutOfRange;
+  }
+  __device__ __forceinline__ void init(const RowsHalfLoader<Swz>& h, int) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) voff[i] = h.voff[i];
   }
 
   template <int I>
@@ -215,8 +258,9 @@ __device__ __forceinline__ uint32_t dstage_offset(uint32_t w4, uint32_t r, uint3
 // Stores wave w4's staged 128 x 64 block of a 16-bit D: lane l takes 16-byte
 // chunk l%8 of row 8s + l/8 (one contiguous KiB per read), so 8 lanes store
 // one 128-byte row segment (16 stores per wave).  N is a multiple of 4: a
-// chunk with 4 valid columns stores its first 8 bytes.
-template <bool OutSwz = true>
+// chunk with 4 valid columns stores its first 8 bytes.  AnyD: any number of
+// columns and any row pitch (store_any).
+template <bool OutSwz = true, bool AnyD = false>
 __device__ __forceinline__ void store_d16_block(char* const (&cq)[4], const TileJob& j, void* D,
                                                 int64_t ldd, int lane, int g, int w4) {
   const int cc = lane & 7;
@@ -228,6 +272,10 @@ __device__ __forceinline__ void store_d16_block(char* const (&cq)[4], const Tile
     const int ml = 128 * g + (int)r;
     if (ml >= j.m_valid || nl >= j.n_valid) continue;
     uint16_t* p = static_cast<uint16_t*>(D) + (j.d_row0 + ml) * ldd + j.n0 + nl;
+    if constexpr (AnyD) {
+      store_any(p, d, j.n_valid - nl, j.vec);
+      continue;
+    }
     if (j.n_valid - nl >= 8)
       *reinterpret_cast<u32x4*>(p) = d;
     else
@@ -235,9 +283,9 @@ __device__ __forceinline__ void store_d16_block(char* const (&cq)[4], const Tile
   }
 }
 
-template <bool IsBF16, int Swz>
+template <int Elem, int Swz>
 struct PingPongTile {
-  using Base = GemmTile<256, 256, IsBF16, false, false, Swz, 8>;
+  using Base = GemmTile<256, 256, Elem, false, false, Swz, 8>;
   static constexpr int kHalfBytes = 16384;             // 128 rows x 128 B
   static constexpr int kTileBytes = 2 * kHalfBytes;    // one operand, one K tile
   static constexpr int kBK = 64;
@@ -297,7 +345,7 @@ struct PingPongTile {
       for (int m = 0; m < 4; ++m) {
         const int fm = ((q & 1) << 1) | (m >> 1), fn = m & 1;
         if constexpr (Active)
-          acc[fm][fn] = mfma32x32x16<IsBF16>(f.b[kk][fn], f.a[kk][fm], acc[fm][fn]);
+          acc[fm][fn] = mfma32x32x16<Elem>(f.b[kk][fn], f.a[kk][fm], acc[fm][fn]);
       }
       __builtin_amdgcn_sched_barrier(0);
       ld.issue(rsrc, half, w4, q, rows_valid, kbyte0, kbytes);

@@ -36,10 +36,15 @@ namespace sg {
 // come from transposing reads.  Only for K a multiple of 64 with at least
 // two K tiles.  OutSwz: whether the epilogue's C and D staging in LDS use
 // their XOR keys (the library) or the logical chunk order (the output half
-// of the layout ablation); Swz is the operands' layout.
-template <bool IsBF16, int Swz, bool AMn = false, bool BMn = false, bool OutSwz = true>
+// of the layout ablation); Swz is the operands' layout.  Elem: the element
+// type; for kElemI8 K and the offsets along it count pairs of elements, so
+// that a K tile is the same 128 bytes.  Rows: A's rows are gathered (TileJob
+// `rows`).
+template <int Elem, int Swz, bool AMn = false, bool BMn = false, bool OutSwz = true,
+          bool Rows = false>
 struct PingPong16Tile {
-  using PP = PingPongTile<IsBF16, Swz>;
+  using PP = PingPongTile<Elem, Swz>;
+  using ALoader = typename std::conditional<Rows, RowsHalfLoader<Swz>, HalfLoader<Swz>>::type;
   static constexpr int kHalfBytes = PP::kHalfBytes;
   static constexpr int kTileBytes = PP::kTileBytes;
   static constexpr int kBK = PP::kBK;
@@ -147,9 +152,9 @@ struct PingPong16Tile {
   // of blocks left to right, row i+1 right to left), so consecutive MFMAs
   // always share an operand: measured 1.5-2% more clock at the power limit
   // than restarting each row at block 0.
-  template <bool Active>
+  template <bool Active, class Loader>
   __device__ __forceinline__ static void compute(f32x4 (&acc)[kI][kJ], const Frags& f,
-                                                 const HalfLoader<Swz>& ld, u32x4 rsrc,
+                                                 const Loader& ld, u32x4 rsrc,
                                                  uint32_t half, int w4, int rows_valid,
                                                  uint32_t kbyte0, uint32_t kbytes) {
 #pragma unroll
@@ -162,7 +167,7 @@ struct PingPong16Tile {
           ld.prep(half, w4, q);
           __builtin_amdgcn_sched_barrier(0);
         }
-        if constexpr (Active) acc[i][j] = mfma16x16x32<IsBF16>(f.b[j], f.a[i], acc[i][j]);
+        if constexpr (Active) acc[i][j] = mfma16x16x32<Elem>(f.b[j], f.a[i], acc[i][j]);
       }
       __builtin_amdgcn_sched_barrier(0);
       if constexpr (Active)
@@ -192,7 +197,7 @@ struct PingPong16Tile {
           if (q == 3) ld.template prep<3>(half, w4);
           __builtin_amdgcn_sched_barrier(0);
         }
-        if constexpr (Active) acc[i][j] = mfma16x16x32<IsBF16>(f.b[j], f.a[i], acc[i][j]);
+        if constexpr (Active) acc[i][j] = mfma16x16x32<Elem>(f.b[j], f.a[i], acc[i][j]);
       }
       __builtin_amdgcn_sched_barrier(0);
       if constexpr (Active) {
@@ -218,7 +223,7 @@ struct PingPong16Tile {
 #pragma unroll
       for (int mm = 0; mm < 32; ++mm) {
         const int i = mm >> 2, j = (i & 1) ? 3 - (mm & 3) : (mm & 3);
-        acc[i][j] = mfma16x16x32<IsBF16>(f.b[j], f.a[i], acc[i][j]);
+        acc[i][j] = mfma16x16x32<Elem>(f.b[j], f.a[i], acc[i][j]);
       }
     }
   }
@@ -433,7 +438,7 @@ struct PingPong16Tile {
           lds_write16(cq[i >> 1], dstage_offset<OutSwz>((uint32_t)w4, r, ch),
                       u32x4{a[0], b[0], a[1], b[1]});
         }
-      store_d16_block<OutSwz>(cq, j, D, ldd, lane, g, w4);
+      store_d16_block<OutSwz, Elem == kElemI8>(cq, j, D, ldd, lane, g, w4);
     }
   }
 
@@ -458,9 +463,57 @@ struct PingPong16Tile {
 #undef SG_EPI
   }
 
+  // The epilogue of the 8-bit product: the integer accumulators become
+  // acc * sa[row] * sb[column] in fp32 (the conversion rounds sums of 2^24
+  // and more, by half a unit in the last place; then one rounding for each
+  // product and one to D's type).  A 16-bit D is staged in LDS as in
+  // epilogue_lds_t; D may have any number of columns and any row pitch.
+  __device__ __forceinline__ static void epilogue_i8(f32x4 (&acc)[kI][kJ], const TileJob& j,
+                                                     char* smem, int T, void* D, int d_dtype,
+                                                     int64_t ldd, int lane, int g, int w4,
+                                                     bool active) {
+    if (active) {
+      float sb[kJ][4];
+#pragma unroll
+      for (int jn = 0; jn < kJ; ++jn)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          sb[jn][e] = j.sb[min(64 * w4 + 16 * jn + 4 * (lane >> 4) + e, j.n_valid - 1)];
+#pragma unroll
+      for (int i = 0; i < kI; ++i) {
+        const float sa = i8_row_scale<Rows>(j, 128 * g + 16 * i + (lane & 15));
+#pragma unroll
+        for (int jn = 0; jn < kJ; ++jn) acc[i][jn] = i8_scale4(acc[i][jn], sa, sb[jn]);
+      }
+    }
+    if (d_dtype == SG_F32) {
+      if (!active) return;
+#pragma unroll
+      for (int i = 0; i < kI; ++i) {
+        const int ml = 128 * g + 16 * i + (lane & 15);
+        if (ml >= j.m_valid) continue;
+        float* row = static_cast<float*>(D) + (j.d_row0 + ml) * ldd + j.n0;
+#pragma unroll
+        for (int jn = 0; jn < kJ; ++jn) {
+          const int nl = 64 * w4 + 16 * jn + 4 * (lane >> 4);
+          store_any(row + nl, __builtin_bit_cast(u32x4, acc[i][jn]), j.n_valid - nl, j.vec);
+        }
+      }
+      return;
+    }
+    PP::barrier();  // every fragment read is done: the ring becomes the staging area
+    if (!active) return;
+    char* cq[4];
+    cblock_quarters(cq, smem, T, g, kTileBytes, kHalfBytes);
+    if (d_dtype == SG_BF16)
+      epilogue_lds_t<SG_NONE, SG_BF16>(acc, j, cq, D, ldd, lane, g, w4);
+    else
+      epilogue_lds_t<SG_NONE, SG_F16>(acc, j, cq, D, ldd, lane, g, w4);
+  }
+
   template <bool Active>
   __device__ __forceinline__ static void mainloop(f32x4 (&acc)[kI][kJ],
-                                                  const HalfLoader<Swz>& la,
+                                                  const ALoader& la,
                                                   const HalfLoader<Swz>& lb, u32x4 ra, u32x4 rb,
                                                   int a_rows, int b_rows, uint32_t a_ring,
                                                   uint32_t b_ring, const char* a_rd,
@@ -498,10 +551,15 @@ struct PingPong16Tile {
     // Group g loads rows [128g, 128g+128) of both operands.
     const u32x4 ra = rsrc_words(j.a, j.a_bytes), rb = rsrc_words(j.b, j.b_bytes);
     const int a_rows = j.m_valid - 128 * g, b_rows = j.n_valid - 128 * g;
-    HalfLoader<Swz> la, lb;
-    la.init(w4, lane, j.a_pitch);
+    ALoader la;
+    HalfLoader<Swz> lb;
+    if constexpr (Rows) {
+      la.init(w4, lane, j.a_pitch, j.rows + 128 * g, a_rows, j.a_total);
+    } else {
+      la.init(w4, lane, j.a_pitch);
+      la.base += (uint32_t)(128 * g) * j.a_pitch;
+    }
     lb.init(w4, lane, j.b_pitch);
-    la.base += (uint32_t)(128 * g) * j.a_pitch;
     lb.base += (uint32_t)(128 * g) * j.b_pitch;
 
     const uint32_t s0 = lds_addr(smem);
@@ -595,6 +653,11 @@ struct PingPong16Tile {
                       w4, T, kbytes);
     }
     wait_vmem();  // the C block, or the zero-filled loads past K
+
+    if constexpr (Elem == kElemI8) {
+      epilogue_i8(acc, j, smem, T, D, d_dtype, ldd, lane, g, w4, a_rows > 0);
+      return;
+    }
 
     // Through LDS: a 16-bit C that came in with the last loads, and a 16-bit
     // D.  Every fragment read is done once all waves pass the barrier, and

@@ -306,6 +306,145 @@ int gemm_layout128_run(int layout, int64_t M, int64_t N, int64_t K, const void* 
                        const void* B, const void* C, int c_dtype, void* D, int d_dtype,
                        void* stream);
 
+/*
+ * i8_gemm_run -- the product of 8-bit integer matrices with one scale per row
+ * of A (token) and per row of B (output channel):
+ *   D[m][n] = SA[m] * SB[n] * sum_k A[m][k] * B[n][k].
+ * The sum is exact (32-bit integers); it is converted to fp32 and multiplied
+ * by SA[m], then by SB[n], one rounding each, then rounded to d_dtype.
+ *   A   int8 [M][lda], K codes a row;  SA  fp32 [M].
+ *   B   int8 [N][ldb], K codes a row;  SB  fp32 [N].
+ *   D   [M][ldd] of d_dtype (SG_F32, SG_BF16, SG_F16), N values a row.  N and
+ *       ldd may be any; D is aligned to its elements (rows that are 16-byte
+ *       aligned are written fastest).
+ *   K   a multiple of 16 (i8_quant_run pads with zeros), at most 131056, for
+ *       which the sum cannot overflow.  K = 0 gives D = 0.
+ *   lda, ldb are multiples of 16, A and B 16-byte aligned.
+ * Codes are any of -128 .. 127.  A NaN scale makes its row or column NaN.
+ * Errors: SG_ERR_NULL, SG_ERR_ALIGN, SG_ERR_SHAPE (also a leading dimension
+ * below its minimum, or a tile's panel of 2^31 bytes or more), SG_ERR_DTYPE,
+ * SG_ERR_HIP.
+ */
+int i8_gemm_run(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const float* SA,
+                const void* B, int64_t ldb, const float* SB, void* D, int64_t ldd, int d_dtype,
+                void* stream);
+
+/*
+ * i8_grouped_gemm_run -- i8_gemm_run for G experts, whose row ranges are in
+ * DEVICE memory (moe_plan_run writes them), so that no copy to the host stands
+ * between routing and the product:
+ *   D[r] = the 8-bit product of A's row a(r) with B_g, for offsets[g] <= r <
+ *   offsets[g+1], a(r) = rows[r], or r without `rows`.
+ *   R        rows of D.  Rows at and behind offsets[G] are left as they were.
+ *   offsets  DEVICE int32 [G+1], not decreasing, within [0, R].  The device
+ *            clamps them: offsets that break this rule give undefined values
+ *            in D, and no access outside the buffers.
+ *   rows     DEVICE int32 [R], or NULL.  An index outside [0, a_rows) makes
+ *            its row of D zero.
+ *   A        int8 [a_rows][lda] (a_rows >= R without `rows`);  SA [a_rows].
+ *   B        int8, G blocks [N][K], packed;  SB  fp32 [G][N].
+ * G is 1..SG_MAX_GROUPS.  The kernel is chosen from R / G, not from the
+ * offsets.  Everything else is i8_gemm_run's.  Errors: its, SG_ERR_GROUPS (G),
+ * and SG_ERR_SHAPE for a gathered A of 2^31 bytes or more.
+ */
+int i8_grouped_gemm_run(int G, int64_t R, int64_t N, int64_t K, const int32_t* offsets,
+                        const void* A, int64_t lda, int64_t a_rows, const int32_t* rows,
+                        const float* SA, const void* B, const float* SB, void* D, int64_t ldd,
+                        int d_dtype, void* stream);
+
+/*
+ * i8_quant_run -- rows of X to 8-bit codes with one scale per row, for the
+ * operands of the 8-bit products (activations at every call, weights once):
+ *   a = max_k |X[r][k]|,  S[r] = max(a, 2^-100) / 127,
+ *   Q[r][k] = round(X[r][k] * (127 / max(a, 2^-100))),
+ * each step rounded once to fp32 and the codes to nearest even: |Q| <= 127.  A
+ * row that holds an infinity or a NaN has S[r] = NaN and codes 0, so that a
+ * product with it is NaN.
+ *   X   [R][ldx] of x_dtype (SG_F32, SG_BF16, SG_F16), K values a row; any
+ *       ldx >= K and any alignment of its elements (16-byte aligned rows of a
+ *       multiple of 8 values are read fastest).
+ *   Q   int8 [R][ldq], 16-byte aligned, ldq a multiple of 16.  Columns K up to
+ *       the next multiple of 16 are written as zero; those behind are left.
+ *   S   fp32 [R].
+ * K = 0 writes S only.  Errors: SG_ERR_NULL, SG_ERR_ALIGN, SG_ERR_SHAPE,
+ * SG_ERR_DTYPE, SG_ERR_HIP.
+ */
+int i8_quant_run(int64_t R, int64_t K, const void* X, int64_t ldx, int x_dtype, void* Q,
+                 int64_t ldq, float* S, void* stream);
+
+/* Expert routing. */
+#define SG_SCORE_SOFTMAX 0
+#define SG_SCORE_SIGMOID 1
+#define SG_GROUP_MAX 0  /* a group scores its largest key */
+#define SG_GROUP_TOP2 1 /* the sum of its two largest keys */
+#define SG_MAX_TOP_K 32
+#define SG_MAX_ROUTE_GROUPS 32
+
+/*
+ * moe_route_run -- chooses top_k of E experts for each of T tokens and their
+ * weights.
+ *   scores   s[e] = softmax over the token's logits, or sigmoid of each.  A
+ *            logit of -inf or NaN is masked: it scores 0, takes no part in the
+ *            softmax and is never chosen.
+ *   keys     s[e] + bias[e] evaluated in 64 bits.  Without a bias (and without
+ *            SG_GROUP_TOP2 groups) the experts are ordered by their logits,
+ *            which is the exact order of their scores.  A key of -inf or NaN
+ *            masks the expert too.
+ *   groups   with n_groups > 1 (dividing E) the experts form n_groups equal
+ *            runs; only those of the top_groups best groups can be chosen.
+ *   ids      int32 [T][top_k]: the experts by falling key; among equal keys
+ *            (and equal groups) the lowest index comes first.  -1 where no
+ *            expert is left (a fully masked token has -1 throughout).
+ *   weights  fp32 [T][top_k]: s[id] (without the bias), with renorm divided by
+ *            their sum (by 2^-126 where the sum is smaller), times scale; 0
+ *            where the id is -1.
+ *   logits   [T][ldl] of dtype (SG_F32, SG_BF16, SG_F16), any ldl >= E;
+ *   bias     fp32 [E] or NULL.
+ * E is 1..SG_MAX_GROUPS, top_k 1..SG_MAX_TOP_K and at most the experts that
+ * can be chosen, n_groups at most SG_MAX_ROUTE_GROUPS.  Errors: SG_ERR_NULL,
+ * SG_ERR_ALIGN, SG_ERR_SHAPE, SG_ERR_DTYPE, SG_ERR_GROUPS, SG_ERR_HIP.
+ */
+int moe_route_run(int64_t T, int E, int top_k, const void* logits, int64_t ldl, int dtype,
+                  const float* bias, int score, int n_groups, int top_groups, int group_score,
+                  int renorm, float scale, float* weights, int32_t* ids, void* stream);
+
+/*
+ * moe_route_backward_run -- the gradient of the logits from the gradient of
+ * moe_route_run's weights, the choice of experts held fixed.
+ *   dweights  fp32 [T][top_k];  ids  int32 [T][top_k] as moe_route_run wrote
+ *             them (ids outside [0, E) carry no gradient; an id that appears
+ *             twice counts twice).
+ *   dlogits   [T][lddl] of the logits' type, E values a row: all written, zero
+ *             for masked logits.
+ * score, renorm and scale are the forward call's.  Errors as there.
+ */
+int moe_route_backward_run(int64_t T, int E, int top_k, const float* dweights, const void* logits,
+                           int64_t ldl, int dtype, const int32_t* ids, int score, int renorm,
+                           float scale, void* dlogits, int64_t lddl, void* stream);
+
+/*
+ * moe_plan_run -- sorts the T * top_k (token, expert) pairs by expert, stably
+ * and without a copy to the host:
+ *   offsets  int32 [E+1]: expert e's pairs are the sorted rows [offsets[e],
+ *            offsets[e+1]); offsets[E] is the number of valid pairs.
+ *   rows     int32 [T*top_k]: the token of each sorted row (the row index that
+ *            i8_grouped_gemm_run gathers by); -1 behind offsets[E].
+ *   slots    int32 [T][top_k]: the sorted row of each pair, -1 where its id is
+ *            outside [0, E).
+ *   ids      int32 [T][top_k].
+ *   workspace  DEVICE, moe_plan_workspace_bytes(T * top_k, E) bytes, 4-byte
+ *            aligned (0 bytes up to 4096 pairs: may be NULL).  It holds nothing
+ *            between calls; calls that may run at the same time need their own.
+ * T = 0 writes offsets only.  Errors: SG_ERR_NULL, SG_ERR_ALIGN, SG_ERR_SHAPE,
+ * SG_ERR_HIP.
+ */
+int moe_plan_run(int64_t T, int E, int top_k, const int32_t* ids, int32_t* offsets, int32_t* rows,
+                 int32_t* slots, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that moe_plan_run needs for P pairs (host only), or
+ * SG_ERR_SHAPE (negative). */
+int64_t moe_plan_workspace_bytes(int64_t P, int E);
+
 /* Thread-local text of the last failing call ("" if none).  Never NULL. */
 const char* gemm_last_error(void);
 
