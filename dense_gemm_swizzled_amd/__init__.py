@@ -711,64 +711,111 @@ def mxfp6_gemm(A, SFA, B, SFB, *, fmt: str = "e2m3", out_dtype=None, out=None):
 
 # ---------------------------------------------- 8-bit products, expert routing
 #
-# These calls launch on the tensors' device even when another is current.
+# Small calls of these take less time on the GPU than a wrapper of the kind
+# above takes to check them (13 to 19 us), so the checks build their messages
+# only when they fail and the C functions are called directly (6 to 9 us a
+# call).  The launches go to the tensors' device even when another is current.
 
-class _OnDevice:
-    """Makes `device` current for a launch (most calls find it current)."""
-    __slots__ = ("device", "guard")
+_torch = None
 
-    def __init__(self, device):
-        self.device = device
 
-    def __enter__(self):
+def _lib_torch():
+    """(the loaded library, torch), imported once."""
+    global _torch
+    if _torch is None:
         import torch
-        self.guard = None
-        if torch.cuda.current_device() != self.device.index:
-            self.guard = torch.cuda.device(self.device)
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+        load()
+        _torch = torch
+    return _lib, _torch
 
 
-def _vector(name: str, t, n: int, dtypes) -> None:
-    """t is a packed vector of n elements."""
-    _need(t.dim() == 1 and t.shape[0] == n, -3,
-          f"{name} has shape {tuple(t.shape)}, expected ({n},)")
-    _dtype_is(name, t, dtypes)
-    _need(n <= 1 or t.stride(0) == 1, -2, f"{name} must be contiguous")
+def _launch(f, device, *args) -> None:
+    """Calls the C function f(*args, stream) with `device` current."""
+    index = device.index
+    if _torch.cuda.current_device() == index:
+        rc = f(*args, _torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with _torch.cuda.device(index):
+            rc = f(*args, _torch._C._cuda_getCurrentRawStream(index))
+    if rc:
+        raise GemmError(rc, gemm_last_error())
 
 
-def _rows2d(name: str, t) -> int:
-    """The row stride of a 2-D tensor with unit column stride."""
-    _need(t.dim() == 2, -3, f"{name} must be 2-D, got shape {tuple(t.shape)}")
+def _fail(code: int, msg: str):
+    raise GemmError(code, msg)
+
+
+def _on_one_device(first, *others) -> None:
+    """Every tensor (None passes) is on `first`'s CUDA device."""
+    device = first.device
+    if not first.is_cuda:
+        _fail(-1, f"a tensor is on {device}, not a CUDA device")
+    for t in others:
+        if t is not None and t.device != device:
+            _fail(-1, f"tensors are on {t.device} and {device}")
+
+
+def _vector(name: str, t, n: int, dtype) -> None:
+    """t is a packed vector of n elements of dtype."""
+    if t.shape != (n,):
+        _fail(-3, f"{name} has shape {tuple(t.shape)}, expected ({n},)")
+    if t.dtype is not dtype:
+        _fail(-4, f"{name} has dtype {t.dtype}, expected {dtype}")
+    if not t.is_contiguous():
+        _fail(-2, f"{name} must be contiguous; strides {t.stride()}")
+
+
+def _packed(name: str, t, shape, dtype) -> None:
+    """t is a packed row-major tensor of `shape` and dtype."""
+    if not t.is_contiguous():
+        _fail(-2, f"{name} must be contiguous (row-major); strides {t.stride()}")
+    if t.shape != shape:
+        _fail(-3, f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype is not dtype:
+        _fail(-4, f"{name} has dtype {t.dtype}, expected {dtype}")
+
+
+def _pitch(name: str, t) -> int:
+    """The row stride of a 2-D tensor with unit column stride: at least its
+    width, which stands in where no second row tells the stride."""
+    if t.dim() != 2:
+        _fail(-3, f"{name} must be 2-D, got shape {tuple(t.shape)}")
     rows, cols = t.shape
-    _need(cols <= 1 or t.stride(1) == 1, -2, f"{name} must have unit column stride; strides "
-                                             f"{tuple(t.stride())}")
-    if rows <= 1:  # the stride of a single row says nothing
-        return max(int(cols), 1)
-    _need(t.stride(0) >= cols, -2, f"{name} must have a row stride of at least its width; "
-                                   f"strides {tuple(t.stride())}")
-    return max(int(t.stride(0)), 1)
+    s0, s1 = t.stride()
+    if cols > 1 and s1 != 1:
+        _fail(-2, f"{name} must have unit column stride; strides {t.stride()}")
+    if rows <= 1 or cols == 0:
+        return cols
+    if s0 < cols:
+        _fail(-2, f"{name} must have a row stride of at least its width; strides {t.stride()}")
+    return s0
 
 
-def _out_rows(out, R: int, N: int, out_dtype, device):
-    """(out, ldd): `out` checked as [R][N] with padded rows, or a new tensor."""
-    import torch
-    if out is None:
-        return torch.empty((R, N), dtype=out_dtype or torch.bfloat16, device=device), N
-    _shape("out", out, (R, N))
-    _dtype_is("out", out, (torch.float32, torch.bfloat16, torch.float16))
-    return out, _rows2d("out", out)
+def _code_pitch(name: str, t) -> int:
+    """_pitch of int8 codes; a single row's is its width rounded up to 16."""
+    if t.dtype is not _torch.int8:
+        _fail(-4, f"{name} has dtype {t.dtype}, expected torch.int8")
+    ld = _pitch(name, t)
+    return ld if t.shape[0] > 1 else -(-ld // 16) * 16
 
 
-def _i8_pitch(name: str, t, K: int) -> int:
-    """The row pitch of codes: K rounded up to 16 where no second row tells it."""
-    import torch
-    _dtype_is(name, t, (torch.int8,))
-    ld = _rows2d(name, t)
-    return ld if t.shape[0] > 1 and K > 0 else -(-K // 16) * 16
+def _float_code(name: str, dtype) -> int:
+    """The SG_* code of a float type."""
+    T = _torch
+    if dtype is T.bfloat16:
+        return SG_BF16
+    if dtype is T.float32:
+        return SG_F32
+    if dtype is T.float16:
+        return SG_F16
+    _fail(-4, f"{name} has dtype {dtype}, expected float32, bfloat16 or float16")
+
+
+def _out_pitch(out, R: int, N: int) -> int:
+    if out.shape != (R, N):
+        _fail(-3, f"out has shape {tuple(out.shape)}, expected ({R}, {N})")
+    _float_code("out", out.dtype)
+    return _pitch("out", out)
 
 
 def i8_quant(X, *, out=None, out_scale=None):
@@ -777,25 +824,25 @@ def i8_quant(X, *, out=None, out_scale=None):
     = K rounded up to 16, the columns behind K zero.  X is about codes *
     scales[:, None]; scale = max|x| / 127.  A row with an infinity or a NaN has
     the scale NaN.  out: int8 [R][Kp] whose row stride is a multiple of 16."""
-    import torch
-    ldx = _rows2d("X", X)
-    R, K = (int(n) for n in X.shape)
-    _dtype_is("X", X, (torch.float32, torch.bfloat16, torch.float16))
-    Kp = -(-K // 16) * 16
-    ldq = Kp
+    lib, T = _lib_torch()
+    ldx = _pitch("X", X)
+    R, K = X.shape
+    dt = _float_code("X", X.dtype)
+    ldq = Kp = -(-K // 16) * 16
     if out is not None:
-        _shape("out", out, (R, Kp))
-        ldq = _i8_pitch("out", out, K)
+        if out.shape != (R, Kp):
+            _fail(-3, f"out has shape {tuple(out.shape)}, expected ({R}, {Kp})")
+        ldq = _code_pitch("out", out)
     if out_scale is not None:
-        _vector("out_scale", out_scale, R, (torch.float32,))
-    _one_device(("X", X), ("out", out), ("out_scale", out_scale))
+        _vector("out_scale", out_scale, R, T.float32)
+    _on_one_device(X, out, out_scale)
+    dev = X.device
     if out is None:
-        out = torch.empty((R, Kp), dtype=torch.int8, device=X.device)
+        out = T.empty((R, Kp), dtype=T.int8, device=dev)
     if out_scale is None:
-        out_scale = torch.empty(R, dtype=torch.float32, device=X.device)
-    with _OnDevice(X.device):
-        _check(i8_quant_run(R, K, X.data_ptr(), ldx, _dt(X.dtype), out.data_ptr(), ldq,
-                            out_scale.data_ptr(), _stream(X.device)))
+        out_scale = T.empty(R, dtype=T.float32, device=dev)
+    _launch(lib.i8_quant_run, dev, R, K, X.data_ptr(), ldx, dt, out.data_ptr(), ldq,
+            out_scale.data_ptr())
     return out, out_scale
 
 
@@ -804,23 +851,21 @@ def i8_gemm(A, SA, B, SB, *, out_dtype=None, out=None):
     B [N][K] and float32 scales SA [M], SB [N]; returns D [M][N] of out_dtype
     (default torch.bfloat16), or writes `out`.  K is a multiple of 16 (i8_quant
     pads); rows of A, B and out may be padded."""
-    import torch
-    _need(A.dim() == 2 and B.dim() == 2, -3, "A and B must be 2-D")
-    M, K = (int(n) for n in A.shape)
-    N = int(B.shape[0])
-    _need(B.shape[1] == K, -3, f"A and B disagree on K ({K} vs {B.shape[1]})")
-    lda, ldb = _i8_pitch("A", A, K), _i8_pitch("B", B, K)
-    _vector("SA", SA, M, (torch.float32,))
-    _vector("SB", SB, N, (torch.float32,))
-    if out is not None:
-        out, ldd = _out_rows(out, M, N, None, None)
-    _one_device(("A", A), ("SA", SA), ("B", B), ("SB", SB), ("out", out))
+    lib, T = _lib_torch()
+    lda, ldb = _code_pitch("A", A), _code_pitch("B", B)
+    M, K = A.shape
+    N, Kb = B.shape
+    if Kb != K:
+        _fail(-3, f"A and B disagree on K ({K} vs {Kb})")
+    _vector("SA", SA, M, T.float32)
+    _vector("SB", SB, N, T.float32)
+    ldd = N if out is None else _out_pitch(out, M, N)
+    _on_one_device(A, SA, B, SB, out)
+    dev = A.device
     if out is None:
-        out, ldd = _out_rows(None, M, N, out_dtype, A.device)
-    with _OnDevice(A.device):
-        _check(i8_gemm_run(M, N, K, A.data_ptr(), lda, SA.data_ptr(), B.data_ptr(), ldb,
-                           SB.data_ptr(), out.data_ptr(), ldd, _dt(out.dtype),
-                           _stream(A.device)))
+        out = T.empty((M, N), dtype=out_dtype or T.bfloat16, device=dev)
+    _launch(lib.i8_gemm_run, dev, M, N, K, A.data_ptr(), lda, SA.data_ptr(), B.data_ptr(), ldb,
+            SB.data_ptr(), out.data_ptr(), ldd, _float_code("out", out.dtype))
     return out
 
 
@@ -832,35 +877,30 @@ def i8_grouped_gemm(A, SA, B, SB, offsets, *, rows=None, out_dtype=None, out=Non
     rows int32 [R] as moe_plan returns them (without rows, R = T).  Returns D
     [R][N] of out_dtype (default torch.bfloat16), or writes `out`.  Rows at and
     behind offsets[G] are not written: a new D holds anything there."""
-    import torch
-    _need(A.dim() == 2, -3, f"A must be 2-D, got shape {tuple(A.shape)}")
-    _dense("B", B, dims=3)
-    _dtype_is("B", B, (torch.int8,))
-    G, N, K = (int(n) for n in B.shape)
-    T = int(A.shape[0])
-    _need(A.shape[1] == K, -3, f"A and B disagree on K ({A.shape[1]} vs {K})")
-    lda = _i8_pitch("A", A, K)
-    _vector("SA", SA, T, (torch.float32,))
-    _dense("SB", SB)
-    _shape("SB", SB, (G, N))
-    _dtype_is("SB", SB, (torch.float32,))
-    _vector("offsets", offsets, G + 1, (torch.int32,))
-    R = T
+    lib, T = _lib_torch()
+    lda = _code_pitch("A", A)
+    R, K = A.shape
+    if B.dim() != 3:
+        _fail(-3, f"B must be [G][N][K], got shape {tuple(B.shape)}")
+    G, N, Kb = B.shape
+    _packed("B", B, B.shape, T.int8)
+    if Kb != K:
+        _fail(-3, f"A and B disagree on K ({K} vs {Kb})")
+    _vector("SA", SA, R, T.float32)
+    _packed("SB", SB, (G, N), T.float32)
+    _vector("offsets", offsets, G + 1, T.int32)
+    a_rows = R
     if rows is not None:
-        _need(rows.dim() == 1, -3, f"rows must be 1-D, got shape {tuple(rows.shape)}")
-        R = int(rows.shape[0])
-        _vector("rows", rows, R, (torch.int32,))
-    if out is not None:
-        out, ldd = _out_rows(out, R, N, None, None)
-    _one_device(("A", A), ("SA", SA), ("B", B), ("SB", SB), ("offsets", offsets), ("rows", rows),
-                ("out", out))
+        R = rows.numel()
+        _vector("rows", rows, R, T.int32)
+    ldd = N if out is None else _out_pitch(out, R, N)
+    _on_one_device(A, SA, B, SB, offsets, rows, out)
+    dev = A.device
     if out is None:
-        out, ldd = _out_rows(None, R, N, out_dtype, A.device)
-    with _OnDevice(A.device):
-        _check(i8_grouped_gemm_run(G, R, N, K, offsets.data_ptr(), A.data_ptr(), lda, T,
-                                   None if rows is None else rows.data_ptr(), SA.data_ptr(),
-                                   B.data_ptr(), SB.data_ptr(), out.data_ptr(), ldd,
-                                   _dt(out.dtype), _stream(A.device)))
+        out = T.empty((R, N), dtype=out_dtype or T.bfloat16, device=dev)
+    _launch(lib.i8_grouped_gemm_run, dev, G, R, N, K, offsets.data_ptr(), A.data_ptr(), lda,
+            a_rows, None if rows is None else rows.data_ptr(), SA.data_ptr(), B.data_ptr(),
+            SB.data_ptr(), out.data_ptr(), ldd, _float_code("out", out.dtype))
     return out
 
 
@@ -868,12 +908,11 @@ _SCORES = {"softmax": SG_SCORE_SOFTMAX, "sigmoid": SG_SCORE_SIGMOID}
 _GROUP_SCORES = {"max": SG_GROUP_MAX, "top2": SG_GROUP_TOP2}
 
 
-def _route_args(logits, score):
-    import torch
-    ldl = _rows2d("logits", logits)
-    _dtype_is("logits", logits, (torch.float32, torch.bfloat16, torch.float16))
-    _need(score in _SCORES, -4, f"score must be one of {sorted(_SCORES)}, got {score!r}")
-    return int(logits.shape[0]), int(logits.shape[1]), ldl
+def _score_code(score) -> int:
+    code = _SCORES.get(score)
+    if code is None:
+        _fail(-4, f"score must be one of {sorted(_SCORES)}, got {score!r}")
+    return code
 
 
 def moe_route(logits, top_k: int, *, score: str = "softmax", bias=None, n_groups: int = 1,
@@ -888,33 +927,30 @@ def moe_route(logits, top_k: int, *, score: str = "softmax", bias=None, n_groups
     the bias), divided by their sum (renorm), times scale.  Logits of -inf or
     NaN are masked; a token with no expert left has ids -1 and weights 0.
     out: (weights, ids) to write."""
-    import torch
-    T, E, ldl = _route_args(logits, score)
-    top_k, n_groups = int(top_k), int(n_groups)
-    top_groups = n_groups if top_groups is None else int(top_groups)
-    _need(group_score in _GROUP_SCORES, -6,
-          f"group_score must be one of {sorted(_GROUP_SCORES)}, got {group_score!r}")
-    _need(1 <= top_k <= min(E, SG_MAX_TOP_K), -3, f"top_k={top_k} outside 1..min({E}, "
-                                                  f"{SG_MAX_TOP_K})")
+    lib, T = _lib_torch()
+    ldl = _pitch("logits", logits)
+    n, E = logits.shape
+    dt, code = _float_code("logits", logits.dtype), _score_code(score)
+    groups = _GROUP_SCORES.get(group_score)
+    if groups is None:
+        _fail(-6, f"group_score must be one of {sorted(_GROUP_SCORES)}, got {group_score!r}")
+    if not 1 <= top_k <= min(E, SG_MAX_TOP_K):
+        _fail(-3, f"top_k={top_k} outside 1..min({E}, {SG_MAX_TOP_K})")
     if bias is not None:
-        _vector("bias", bias, E, (torch.float32,))
-    weights = ids = None
-    if out is not None:
-        weights, ids = out
-        for name, t, dt in (("weights", weights, torch.float32), ("ids", ids, torch.int32)):
-            _dense(name, t)
-            _shape(name, t, (T, top_k))
-            _dtype_is(name, t, (dt,))
-    _one_device(("logits", logits), ("bias", bias), ("weights", weights), ("ids", ids))
+        _vector("bias", bias, E, T.float32)
     if out is None:
-        weights = torch.empty((T, top_k), dtype=torch.float32, device=logits.device)
-        ids = torch.empty((T, top_k), dtype=torch.int32, device=logits.device)
-    with _OnDevice(logits.device):
-        _check(moe_route_run(T, E, top_k, logits.data_ptr(), ldl, _dt(logits.dtype),
-                             None if bias is None else bias.data_ptr(), _SCORES[score], n_groups,
-                             top_groups, _GROUP_SCORES[group_score], int(bool(renorm)),
-                             float(scale), weights.data_ptr(), ids.data_ptr(),
-                             _stream(logits.device)))
+        _on_one_device(logits, bias)
+        weights = T.empty((n, top_k), dtype=T.float32, device=logits.device)
+        ids = T.empty((n, top_k), dtype=T.int32, device=logits.device)
+    else:
+        weights, ids = out
+        _packed("weights", weights, (n, top_k), T.float32)
+        _packed("ids", ids, (n, top_k), T.int32)
+        _on_one_device(logits, bias, weights, ids)
+    _launch(lib.moe_route_run, logits.device, n, E, top_k, logits.data_ptr(), ldl, dt,
+            None if bias is None else bias.data_ptr(), code, n_groups,
+            n_groups if top_groups is None else top_groups, groups, 1 if renorm else 0, scale,
+            weights.data_ptr(), ids.data_ptr())
     return weights, ids
 
 
@@ -922,28 +958,29 @@ def moe_route_backward(dweights, logits, ids, *, score: str = "softmax", renorm:
                        scale: float = 1.0, out=None):
     """The gradient of the logits [T][E] (their type) from dweights float32
     [T][top_k], the gradient of moe_route's weights, and its ids."""
-    import torch
-    T, E, ldl = _route_args(logits, score)
-    _dense("ids", ids)
-    top_k = int(ids.shape[1])
-    _shape("ids", ids, (T, top_k))
-    _dtype_is("ids", ids, (torch.int32,))
-    _dense("dweights", dweights)
-    _shape("dweights", dweights, (T, top_k))
-    _dtype_is("dweights", dweights, (torch.float32,))
+    lib, T = _lib_torch()
+    ldl = _pitch("logits", logits)
+    n, E = logits.shape
+    dt, code = _float_code("logits", logits.dtype), _score_code(score)
+    if ids.dim() != 2:
+        _fail(-3, f"ids must be 2-D, got shape {tuple(ids.shape)}")
+    top_k = ids.shape[1]
+    _packed("ids", ids, (n, top_k), T.int32)
+    _packed("dweights", dweights, (n, top_k), T.float32)
     lddl = E
     if out is not None:
-        _shape("out", out, (T, E))
-        _dtype_is("out", out, (logits.dtype,))
-        lddl = _rows2d("out", out)
-    _one_device(("dweights", dweights), ("logits", logits), ("ids", ids), ("out", out))
+        if out.shape != (n, E):
+            _fail(-3, f"out has shape {tuple(out.shape)}, expected ({n}, {E})")
+        if out.dtype is not logits.dtype:
+            _fail(-4, f"out has dtype {out.dtype}, expected {logits.dtype}")
+        lddl = _pitch("out", out)
+    _on_one_device(logits, dweights, ids, out)
+    dev = logits.device
     if out is None:
-        out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
-    with _OnDevice(logits.device):
-        _check(moe_route_backward_run(T, E, top_k, dweights.data_ptr(), logits.data_ptr(), ldl,
-                                      _dt(logits.dtype), ids.data_ptr(), _SCORES[score],
-                                      int(bool(renorm)), float(scale), out.data_ptr(), lddl,
-                                      _stream(logits.device)))
+        out = T.empty((n, E), dtype=logits.dtype, device=dev)
+    _launch(lib.moe_route_backward_run, dev, n, E, top_k, dweights.data_ptr(),
+            logits.data_ptr(), ldl, dt, ids.data_ptr(), code, 1 if renorm else 0, scale,
+            out.data_ptr(), lddl)
     return out
 
 
@@ -957,37 +994,34 @@ def moe_plan(ids, n_experts: int, *, out=None, workspace=None):
     out: (offsets, rows, slots) to write.  workspace: a uint8 tensor of at
     least moe_plan_workspace_bytes(T * top_k, E) bytes; by default one is
     allocated for the call."""
-    import torch
-    _dense("ids", ids)
-    _dtype_is("ids", ids, (torch.int32,))
-    T, top_k = (int(n) for n in ids.shape)
-    E, P = int(n_experts), T * top_k
-    need = int(moe_plan_workspace_bytes(P, E))
-    _check(need if need < 0 else 0)
-    offsets = rows = slots = None
+    lib, T = _lib_torch()
+    if ids.dim() != 2:
+        _fail(-3, f"ids must be 2-D, got shape {tuple(ids.shape)}")
+    n, top_k = ids.shape
+    _packed("ids", ids, (n, top_k), T.int32)
+    P = n * top_k
+    need = lib.moe_plan_workspace_bytes(P, n_experts)
+    if need < 0:
+        _fail(need, gemm_last_error())
+    dev = ids.device
+    if workspace is not None:
+        size = workspace.numel()
+        _vector("workspace", workspace, size, T.uint8)
+        if size < need:
+            _fail(-3, f"workspace has {size} bytes, {need} are needed")
     if out is not None:
         offsets, rows, slots = out
-        _vector("offsets", offsets, E + 1, (torch.int32,))
-        _vector("rows", rows, P, (torch.int32,))
-        _dense("slots", slots)
-        _shape("slots", slots, (T, top_k))
-        _dtype_is("slots", slots, (torch.int32,))
-    if workspace is not None:
-        _dense("workspace", workspace, 1)
-        _dtype_is("workspace", workspace, (torch.uint8,))
-        _need(workspace.shape[0] >= need, -3,
-              f"workspace has {workspace.shape[0]} bytes, {need} are needed")
-    _one_device(("ids", ids), ("offsets", offsets), ("rows", rows), ("slots", slots),
-                ("workspace", workspace))
-    dev = ids.device
-    if out is None:
-        offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
-        rows = torch.empty(P, dtype=torch.int32, device=dev)
-        slots = torch.empty((T, top_k), dtype=torch.int32, device=dev)
-    if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    with _OnDevice(dev):
-        _check(moe_plan_run(T, E, top_k, ids.data_ptr(), offsets.data_ptr(), rows.data_ptr(),
-                            slots.data_ptr(), None if need == 0 else workspace.data_ptr(), need,
-                            _stream(dev)))
+        _vector("offsets", offsets, n_experts + 1, T.int32)
+        _vector("rows", rows, P, T.int32)
+        _packed("slots", slots, (n, top_k), T.int32)
+        _on_one_device(ids, offsets, rows, slots, workspace)
+    else:
+        _on_one_device(ids, workspace)
+        offsets = T.empty(n_experts + 1, dtype=T.int32, device=dev)
+        rows = T.empty(P, dtype=T.int32, device=dev)
+        slots = T.empty((n, top_k), dtype=T.int32, device=dev)
+    if workspace is None and need:
+        workspace = T.empty(need, dtype=T.uint8, device=dev)
+    _launch(lib.moe_plan_run, dev, n, n_experts, top_k, ids.data_ptr(), offsets.data_ptr(),
+            rows.data_ptr(), slots.data_ptr(), workspace.data_ptr() if need else None, need)
     return offsets, rows, slots
