@@ -618,6 +618,11 @@ int route_check(const char* who, int64_t T, int E, int top_k, const void* logits
   return SG_OK;
 }
 
+// Whether four values at any multiple of four of any row are one aligned access.
+bool rows_of_four(const void* p, int64_t ld, int dtype) {
+  return ld % 4 == 0 && reinterpret_cast<uintptr_t>(p) % (4 * elem_bytes(dtype)) == 0;
+}
+
 // Pairs a workgroup of the plan sorts, and how many workgroups there are.
 int64_t plan_chunk(int64_t P) {
   if (P <= 4096) return 4096;
@@ -703,6 +708,7 @@ int moe_route_run(int64_t T, int E, int top_k, const void* logits, int64_t ldl, 
   p.renorm = renorm;
   p.scale = scale;
   p.by_score = bias || (p.n_groups > 1 && group_score == SG_GROUP_TOP2);
+  p.vec = rows_of_four(logits, ldl, dtype);
   p.weights = weights;
   p.ids = ids;
   hipError_t e = sg::launch_moe_route(dtype, p, static_cast<hipStream_t>(stream));
@@ -735,6 +741,8 @@ int moe_route_backward_run(int64_t T, int E, int top_k, const float* dweights, c
   p.dweights = dweights;
   p.dlogits = dlogits;
   p.lddl = lddl;
+  p.vec = rows_of_four(logits, ldl, dtype);
+  p.vec_d = rows_of_four(dlogits, lddl, dtype);
   hipError_t e = sg::launch_moe_route_backward(dtype, p, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail(e, who);
   return ok();

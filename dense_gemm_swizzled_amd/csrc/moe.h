@@ -17,6 +17,7 @@ struct RouteParams {
   int renorm;
   float scale;
   bool by_score;            // order by score + bias (64 bits), not by logit
+  bool vec, vec_d;          // four logits / gradients at a multiple of four: one access
   float* weights;           // [T][top_k] (forward)
   int32_t* ids;             // [T][top_k]; read by the backward pass
   const float* dweights;    // [T][top_k] (backward)

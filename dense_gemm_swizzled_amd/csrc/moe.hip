@@ -4,8 +4,9 @@
 #include <hip/hip_runtime.h>
 
 #include <cfloat>
+#include <type_traits>
 
-#include "gemm_device.h"
+#include "gemm_kernels.h"
 #include "lane_ops.h"
 #include "launch.h"
 #include "moe.h"
@@ -14,7 +15,7 @@ namespace sg {
 
 namespace {
 
-constexpr int kHeld = 4;             // experts a lane holds: e = i * Lanes + lane
+constexpr int kHeld = 4;             // experts a lane holds: 4 * lane .. 4 * lane + 3
 constexpr float kTiny = 0x1p-126f;   // smallest sum that weights are divided by
 constexpr int kBlockThreads = 256;
 
@@ -31,6 +32,33 @@ __device__ __forceinline__ float clean(float x) {
   return x > -__builtin_inff() ? __builtin_fminf(x, FLT_MAX) : -__builtin_inff();
 }
 
+// The logits of experts e0 .. e0+3 of row t, masked past E.  vec: four logits
+// from any multiple of four are one aligned load.
+template <int DT>
+__device__ __forceinline__ void load_row4(const RouteParams& p, int64_t t, int e0, bool live,
+                                          float (&x)[kHeld]) {
+  if (live && p.vec && e0 + kHeld <= p.E) {
+    const int64_t at = t * p.ldl + e0;
+    if constexpr (DT == SG_F32) {
+      const f32x4 v = *reinterpret_cast<const f32x4*>(static_cast<const float*>(p.logits) + at);
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) x[i] = clean(v[i]);
+    } else {
+      const u32x2 v = *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(p.logits) + at);
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) {
+        const uint32_t h = (i & 1) ? v[i / 2] >> 16 : v[i / 2] & 0xffffu;
+        x[i] = clean(DT == SG_BF16 ? bf16_to_f32(h) : f16_to_f32(h));
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i)
+    x[i] = live && e0 + i < p.E ? clean(load_logit<DT>(p.logits, t * p.ldl + e0 + i))
+                                : -__builtin_inff();
+}
+
 __device__ __forceinline__ float exp_of(float x) { return expf(x); }
 __device__ __forceinline__ double exp_of(double x) { return exp(x); }
 
@@ -41,19 +69,26 @@ __device__ __forceinline__ F sigmoid_of(F x) {
   return (x < 0 ? z : F(1)) / (F(1) + z);
 }
 
-// The scores of a token's experts in type F; x masked (-inf) scores zero.
+template <int Lanes>
+__device__ __forceinline__ float row_top(const float (&x)[kHeld]) {
+  float m = x[0];
+#pragma unroll
+  for (int i = 1; i < kHeld; ++i) m = OpMax{}(m, x[i]);
+  return lane_reduce<Lanes>(m, OpMax{});
+}
+
+// The scores of a token's experts in type F, up to a common divisor, which is
+// returned: the chosen ones alone are divided by it.  x masked (-inf) scores
+// zero.
 template <int Lanes, class F>
-__device__ __forceinline__ void scores_of(const float (&x)[kHeld], int score, F (&s)[kHeld]) {
+__device__ __forceinline__ F scores_of(const float (&x)[kHeld], int score, F (&s)[kHeld]) {
   if (score == SG_SCORE_SIGMOID) {
 #pragma unroll
     for (int i = 0; i < kHeld; ++i)
       s[i] = x[i] > -__builtin_inff() ? sigmoid_of((F)x[i]) : F(0);
-    return;
+    return F(1);
   }
-  float m = x[0];
-#pragma unroll
-  for (int i = 1; i < kHeld; ++i) m = OpMax{}(m, x[i]);
-  m = lane_reduce<Lanes>(m, OpMax{});
+  const float m = row_top<Lanes>(x);
   F sum = 0;
 #pragma unroll
   for (int i = 0; i < kHeld; ++i) {
@@ -61,136 +96,273 @@ __device__ __forceinline__ void scores_of(const float (&x)[kHeld], int score, F 
     sum += s[i];
   }
   sum = lane_reduce<Lanes>(sum, OpSum{});
-  sum = sum > F(kTiny) ? sum : F(kTiny);
-#pragma unroll
-  for (int i = 0; i < kHeld; ++i) s[i] /= sum;
+  return sum > F(kTiny) ? sum : F(kTiny);
 }
 
-// One group of Lanes lanes a token.  Key: what the experts are ordered by --
-// the logits themselves (float: score is increasing in the logit, so without
-// a bias they give the exact order of the scores), or score + bias in 64 bits.
-template <int DT, int Lanes, class Key>
-__global__ void __launch_bounds__(kBlockThreads) moe_route_kernel(const RouteParams p) {
-  constexpr int kTokens = kBlockThreads / Lanes;
-  constexpr bool kScores = sizeof(Key) == 8;
-  const Key kNone = -(Key)__builtin_inff();
-  const int lane = threadIdx.x % Lanes, slot = threadIdx.x / Lanes;
-  const int64_t t = (int64_t)blockIdx.x * kTokens + slot;
-  const bool live = t < p.T;  // a token past the end goes along for the barriers
+// A token's lanes are in one wave, whose LDS accesses complete in order: what
+// one lane wrote another may read after this.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
 
-  float x[kHeld], s[kHeld];
-  Key key[kHeld];
+// LDS of one token.
+template <int Lanes, class Key>
+struct RouteScratch {
+  Key keys[Lanes * kHeld];
+  Key best[SG_MAX_ROUTE_GROUPS];
+  int keep[SG_MAX_ROUTE_GROUPS];
+};
+
+// Masks (kNone) the experts outside the top_groups best groups.  2^j lanes
+// share a group's members and merge their two largest.  Returns the gap
+// between the last kept and the first dropped group.
+template <int Lanes, class Key>
+__device__ __forceinline__ Key keep_groups(const RouteParams& p, RouteScratch<Lanes, Key>& sc,
+                                           int lane, Key (&key)[kHeld]) {
+  const Key kNone = -(Key)__builtin_inff();
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) sc.keys[kHeld * lane + i] = key[i];
+  wave_sync();
+  const int G = p.n_groups, size = p.E / G;
+  int share = 1;
+  while (2 * share * G <= Lanes) share *= 2;
+  const int part = lane & (share - 1);
+  for (int g0 = 0; g0 < G; g0 += Lanes / share) {
+    const int g = g0 + lane / share;
+    Key b0 = kNone, b1 = kNone;
+    if (g < G)
+      for (int m = part; m < size; m += share) {
+        const Key k = sc.keys[g * size + m];
+        b1 = OpMax{}(b1, k < b0 ? k : b0);
+        b0 = OpMax{}(b0, k);
+      }
+    for (int d = 1; d < share; d *= 2) {
+      const Key o0 = __shfl_xor(b0, d), o1 = __shfl_xor(b1, d);
+      b1 = OpMax{}(OpMax{}(b1, o1), b0 < o0 ? b0 : o0);
+      b0 = OpMax{}(b0, o0);
+    }
+    if (g < G && part == 0)
+      sc.best[g] = p.group_score == SG_GROUP_TOP2 && b1 > kNone ? b0 + b1 : b0;
+  }
+  wave_sync();
+  Key kept = (Key)__builtin_inff(), dropped = kNone;
+  for (int g = lane; g < G; g += Lanes) {
+    const Key mine = sc.best[g];
+    int above = 0;  // groups before this one; ties go to the lowest
+    for (int h = 0; h < G; ++h) {
+      const Key o = sc.best[h];
+      above += o > mine || (o == mine && h < g);
+    }
+    const bool keep = above < p.top_groups;
+    sc.keep[g] = keep;
+    kept = keep && mine < kept ? mine : kept;
+    dropped = keep ? dropped : OpMax{}(dropped, mine);
+  }
+  wave_sync();
+  const int inv = (65536 + size - 1) / size;  // e / size for e < 256
 #pragma unroll
   for (int i = 0; i < kHeld; ++i) {
-    const int e = i * Lanes + lane;
-    x[i] = live && e < p.E ? clean(load_logit<DT>(p.logits, t * p.ldl + e)) : -__builtin_inff();
+    const int e = kHeld * lane + i;
+    if (e < p.E && !sc.keep[(e * inv) >> 16]) key[i] = kNone;
   }
-  if constexpr (kScores) {
-    double wide[kHeld];
-    scores_of<Lanes>(x, p.score, wide);
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-      const int e = i * Lanes + lane;
-      s[i] = (float)wide[i];
-      const double b = p.bias && e < p.E ? (double)p.bias[e] : 0.0;
-      const double k = wide[i] + b;
-      key[i] = x[i] > -__builtin_inff() && k > kNone ? k : kNone;
-    }
-  } else {
-    scores_of<Lanes>(x, p.score, s);
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) key[i] = x[i];
-  }
+  kept = -lane_reduce<Lanes>(-kept, OpMax{});
+  dropped = lane_reduce<Lanes>(dropped, OpMax{});
+  // (a dropped group without a key leaves no doubt, nor do two infinite ones
+  // beyond their order by index)
+  return dropped > kNone && kept < (Key)__builtin_inff() ? kept - dropped
+                                                         : (Key)__builtin_inff();
+}
 
-  if (p.n_groups > 1) {  // keep the top_groups best groups
-    __shared__ Key keys[kBlockThreads * kHeld];
-    __shared__ Key best[kTokens * SG_MAX_ROUTE_GROUPS];
-    Key* const kt = keys + slot * Lanes * kHeld;
-    Key* const bt = best + slot * SG_MAX_ROUTE_GROUPS;
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) kt[i * Lanes + lane] = key[i];
-    __syncthreads();
-    const int size = p.E / p.n_groups;
-    for (int g = lane; g < p.n_groups; g += Lanes) {
-      Key b0 = kNone, b1 = kNone;
-      for (int m = 0; m < size; ++m) {
-        const Key k = kt[g * size + m];
-        if (k > b0) {
-          b1 = b0;
-          b0 = k;
-        } else if (k > b1) {
-          b1 = k;
-        }
-      }
-      bt[g] = p.group_score == SG_GROUP_TOP2 && b1 > kNone ? b0 + b1 : b0;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-      const int e = i * Lanes + lane;
-      if (e >= p.E) continue;
-      const int g = e / size;
-      const Key mine = bt[g];
-      int above = 0;  // groups before this expert's; ties go to the lowest
-      for (int h = 0; h < p.n_groups; ++h) above += bt[h] > mine || (bt[h] == mine && h < g);
-      if (above >= p.top_groups) key[i] = kNone;
-    }
-  }
+// What keys are compared as: doubles as they are, floats as integers of the
+// same order (one instruction a step of a maximum, where a float's maximum
+// first quiets its operands).  -0 and 0 are one key.
+__device__ __forceinline__ double order_of(double k) { return k; }
+__device__ __forceinline__ int order_of(float k) {
+  const int u = __builtin_bit_cast(int, k + 0.0f);
+  return u ^ (int)((uint32_t)(u >> 31) >> 1);
+}
+__device__ __forceinline__ double key_at(double o) { return o; }
+__device__ __forceinline__ float key_at(int o) {
+  return __builtin_bit_cast(float, o ^ (int)((uint32_t)(o >> 31) >> 1));
+}
 
-  // top_k times the largest key, the lowest expert among equal ones.
-  int rank[kHeld];
+// top_k times the largest key, the lowest expert among equal ones: chosen[k]
+// receives (expert, s).  Each lane keeps its four keys sorted, so a round
+// compares the lanes' heads, finds the lowest lane that holds the largest and
+// pops it.  Returns how many experts were found; with Gaps, `gap` is the
+// smallest distance between one choice and the next, the first expert not
+// chosen included.
+struct Chosen {
+  int id;
+  float s;
+};
+template <int Lanes, bool Gaps, class Key>
+__device__ __forceinline__ int choose(const RouteParams& p, int lane, const Key (&key)[kHeld],
+                                      const float (&s)[kHeld], Chosen* chosen, Key& gap) {
+  typedef decltype(order_of(key[0])) Ord;
+  const Ord kNone = order_of(-(Key)__builtin_inff());
+  Ord h[kHeld];
+  int at[kHeld];
 #pragma unroll
-  for (int i = 0; i < kHeld; ++i) rank[i] = -1;
-  const int base = (threadIdx.x & 63) / Lanes * Lanes;
+  for (int i = 0; i < kHeld; ++i) {
+    h[i] = order_of(key[i]);
+    at[i] = i;
+  }
+  // Neighbours change places only when out of order, so equal keys keep theirs.
+  auto order = [&](int i) {
+    const bool swap = h[i] < h[i + 1];
+    const Ord a = h[i], b = h[i + 1];
+    const int m = at[i], n = at[i + 1];
+    h[i] = swap ? b : a;
+    h[i + 1] = swap ? a : b;
+    at[i] = swap ? n : m;
+    at[i + 1] = swap ? m : n;
+  };
+  order(0), order(2), order(1), order(0), order(2), order(1);
+  static_assert(kHeld == 4, "the sorting network");
+  const int self = threadIdx.x & 63, base = self / Lanes * Lanes;
   const uint64_t mask = Lanes == 64 ? ~0ull : ((1ull << (Lanes & 63)) - 1) << base;
   int found = 0;
+  Key last = (Key)__builtin_inff();
+  gap = (Key)__builtin_inff();
   for (int k = 0; k < p.top_k; ++k) {
-    Key m = key[0];
+    const Ord m = lane_reduce<Lanes>(h[0], OpMax{});
+    const bool any = m > kNone;
+    if constexpr (Gaps) {
+      const Key v = key_at(m), d = last - v;
+      gap = any && d < gap ? d : gap;
+      last = v;
+    }
+    const uint64_t eq = __ballot(h[0] == m) & mask;
+    found += any;
+    if (any && (int)__builtin_ctzll(eq) == self) {
+      const int i = at[0];
+      chosen[k] = {kHeld * lane + i, i == 0 ? s[0] : i == 1 ? s[1] : i == 2 ? s[2] : s[3]};
 #pragma unroll
-    for (int i = 1; i < kHeld; ++i) m = OpMax{}(m, key[i]);
-    m = lane_reduce<Lanes>(m, OpMax{});
-    if (!(m > kNone)) break;  // (this lane group; the others may go on)
-    bool open = true;
+      for (int q = 0; q + 1 < kHeld; ++q) {
+        h[q] = h[q + 1];
+        at[q] = at[q + 1];
+      }
+      h[kHeld - 1] = kNone;
+    }
+  }
+  if constexpr (Gaps) {
+    const Ord m = lane_reduce<Lanes>(h[0], OpMax{});
+    const Key d = last - key_at(m);
+    gap = m > kNone && d < gap ? d : gap;
+  }
+  return found;
+}
+
+// One group of Lanes lanes a token.  Scores: experts are ordered by score +
+// bias, else by the logits themselves (the score increases with the logit, so
+// this is the exact order of the scores).
+//
+// Score keys are defined in 64 bits.  They are first made in 32.  In units of
+// 2^-24 of the row's largest score, a sigmoid is off by at most 8 (expf 4, the
+// sum and the quotient 1 each, twice), a softmax score by 40 (the rounded
+// difference in the exponent and expf 24, the sum over the experts 10, the
+// divisor's reciprocal and product 3), and the sum with the bias by half a
+// unit of the key.  If two keys whose order matters lie closer than twice that
+// -- four times for sums of two -- the wave decides again in 64 bits: with 256
+// experts about one token in a thousand does (sigmoid; softmax fewer).
+template <int DT, int Lanes, bool Scores>
+__global__ void __launch_bounds__(kBlockThreads) moe_route_kernel(const RouteParams p) {
+  constexpr int kTokens = kBlockThreads / Lanes;
+  typedef typename std::conditional<Scores, double, float>::type Wide;
+  __shared__ RouteScratch<Lanes, Wide> scratch[kTokens];
+  __shared__ Chosen chosen_all[kTokens * SG_MAX_TOP_K];
+  const int lane = threadIdx.x % Lanes, slot = threadIdx.x / Lanes;
+  const int64_t t = (int64_t)blockIdx.x * kTokens + slot;
+  const bool live = t < p.T;  // lanes past the last token go along for the wave
+  Chosen* const chosen = chosen_all + slot * SG_MAX_TOP_K;
+  const float kNone = -__builtin_inff();
+
+  float x[kHeld], s[kHeld], key[kHeld], b[kHeld];
+  load_row4<DT>(p, t, kHeld * lane, live, x);
+  if constexpr (Scores) {
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {
-      const uint64_t eq = __ballot(key[i] == m) & mask;
-      if (open && eq) {
-        open = false;
-        if ((int)__builtin_ctzll(eq) == (int)(threadIdx.x & 63)) {
-          rank[i] = k;
-          key[i] = kNone;
-        }
-      }
+      const int e = kHeld * lane + i;
+      b[i] = p.bias && e < p.E ? p.bias[e] : 0.0f;
     }
-    ++found;
   }
+  const float over = scores_of<Lanes>(x, p.score, s);
+  float group_gap = __builtin_inff(), gap;
+  float off = 0.0f;  // the largest error of a key
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) key[i] = x[i];
+  if constexpr (Scores) {
+    const float inv = 1.0f / over;
+    float top = 0.0f, far = 0.0f;  // the largest score and finite |key|
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      const float v = s[i] * inv, k = v + b[i], a = __builtin_fabsf(k);
+      key[i] = x[i] > kNone && k > kNone ? k : kNone;
+      top = OpMax{}(top, v);
+      far = a < __builtin_inff() ? OpMax{}(far, a) : far;
+    }
+    const float units = p.score == SG_SCORE_SIGMOID ? 8.0f : 40.0f;
+    off = 0x1p-24f * lane_reduce<Lanes>(units * top + far, OpMax{});
+  }
+  if (p.n_groups > 1)
+    group_gap = keep_groups<Lanes>(
+        p, reinterpret_cast<RouteScratch<Lanes, float>&>(scratch[slot]), lane, key);
+  int found = choose<Lanes, Scores>(p, lane, key, s, chosen, gap);
+  if constexpr (Scores) {
+    if (__any(!(gap > 2 * off) || !(group_gap > 4 * off))) {
+      double wide[kHeld];
+      const double div = scores_of<Lanes>(x, p.score, wide);
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) {
+        const double k = wide[i] / div + (double)b[i];
+        wide[i] = x[i] > kNone && k > (double)kNone ? k : (double)kNone;
+      }
+      wave_sync();
+      if (p.n_groups > 1) keep_groups<Lanes>(p, scratch[slot], lane, wide);
+      double ignored;
+      found = choose<Lanes, false>(p, lane, wide, s, chosen, ignored);
+    }
+  }
+  wave_sync();
 
   float sum = 0.0f;
-#pragma unroll
-  for (int i = 0; i < kHeld; ++i) sum += rank[i] >= 0 ? s[i] : 0.0f;
+  for (int k = lane; k < found; k += Lanes) {
+    const float v = chosen[k].s / over;
+    chosen[k].s = v;
+    sum += v;
+  }
   sum = lane_reduce<Lanes>(sum, OpSum{});
   const float div = p.renorm ? __builtin_fmaxf(sum, kTiny) : 1.0f;
   if (!live) return;
-#pragma unroll
-  for (int i = 0; i < kHeld; ++i)
-    if (rank[i] >= 0) {
-      p.ids[t * p.top_k + rank[i]] = i * Lanes + lane;
-      p.weights[t * p.top_k + rank[i]] = s[i] / div * p.scale;
-    }
-  for (int k = found + lane; k < p.top_k; k += Lanes) {
-    p.ids[t * p.top_k + k] = -1;
-    p.weights[t * p.top_k + k] = 0.0f;
+  for (int k = lane; k < p.top_k; k += Lanes) {
+    const Chosen c = chosen[k];
+    p.ids[t * p.top_k + k] = k < found ? c.id : -1;
+    p.weights[t * p.top_k + k] = k < found ? c.s / div * p.scale : 0.0f;
   }
 }
 
 template <int DT>
-__device__ __forceinline__ void store_logit(void* D, int64_t i, float v) {
-  if constexpr (DT == SG_F32)
-    static_cast<float*>(D)[i] = v;
-  else if constexpr (DT == SG_BF16)
-    static_cast<__bf16*>(D)[i] = (__bf16)v;
-  else
-    static_cast<_Float16*>(D)[i] = (_Float16)v;
+__device__ __forceinline__ void store_row4(const RouteParams& p, int64_t t, int e0, f32x4 v) {
+  const int64_t at = t * p.lddl + e0;
+  if (p.vec_d && e0 + kHeld <= p.E) {
+    if constexpr (DT == SG_F32)
+      *reinterpret_cast<f32x4*>(static_cast<float*>(p.dlogits) + at) = v;
+    else
+      *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(p.dlogits) + at) = pack_d16<DT>(v);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    if (e0 + i >= p.E) break;
+    if constexpr (DT == SG_F32)
+      static_cast<float*>(p.dlogits)[at + i] = v[i];
+    else if constexpr (DT == SG_BF16)
+      static_cast<__bf16*>(p.dlogits)[at + i] = (__bf16)(float)v[i];
+    else
+      static_cast<_Float16*>(p.dlogits)[at + i] = (_Float16)(float)v[i];
+  }
 }
 
 // With r_j = s_j / S (S = max(sum s, 2^-126) with renorm, else 1) and g_j the
@@ -200,72 +372,84 @@ __device__ __forceinline__ void store_logit(void* D, int64_t i, float v) {
 // and of the logits, summing u_j over the j that name the expert,
 //   sigmoid  dx_e = u_e (1 - s_e),
 //   softmax  dx_e = u_e - s_e sum_j u_j   (the sum is zero with renorm).
-// Only ratios of scores appear, so small scores lose nothing.
+// Only ratios of scores appear, so small scores lose nothing.  Bound by
+// memory: the gradient's rows are written whole; softmax reads the logits'
+// rows, sigmoid only the chosen logits.  Lane j of a token's lanes handles its
+// j-th expert and puts the result into the token's row in LDS.
 template <int DT, int Lanes>
 __global__ void __launch_bounds__(kBlockThreads) moe_route_backward_kernel(
     const RouteParams p) {
   constexpr int kTokens = kBlockThreads / Lanes;
-  __shared__ float us[kTokens * SG_MAX_TOP_K];
-  __shared__ int is[kTokens * SG_MAX_TOP_K];
+  __shared__ __attribute__((aligned(16))) float rows[kTokens][Lanes * kHeld];
+  __shared__ Chosen us_all[kTokens * SG_MAX_TOP_K];
   const int lane = threadIdx.x % Lanes, slot = threadIdx.x / Lanes;
   const int64_t t = (int64_t)blockIdx.x * kTokens + slot;
   const bool live = t < p.T;
-  float x[kHeld], s[kHeld];
-#pragma unroll
-  for (int i = 0; i < kHeld; ++i) {
-    const int e = i * Lanes + lane;
-    x[i] = live && e < p.E ? clean(load_logit<DT>(p.logits, t * p.ldl + e)) : -__builtin_inff();
-  }
-  scores_of<Lanes>(x, p.score, s);
+  const int e0 = kHeld * lane;
+  float* const row = rows[slot];
+  Chosen* const us = us_all + slot * SG_MAX_TOP_K;
+  const bool soft = p.score == SG_SCORE_SOFTMAX;
 
-  // The chosen experts' scores travel through LDS to the lanes of their j.
-  __shared__ float sc[kBlockThreads * kHeld];
-  float* const st = sc + slot * Lanes * kHeld;
+  // Softmax: the row's largest logit and sum of exponentials.
+  float x[kHeld], s[kHeld] = {}, top = 0.0f, total = 1.0f;
+  if (soft) {
+    load_row4<DT>(p, t, e0, live, x);
+    top = row_top<Lanes>(x);
+    total = 0.0f;
 #pragma unroll
-  for (int i = 0; i < kHeld; ++i) st[i * Lanes + lane] = s[i];
-  __syncthreads();
+    for (int i = 0; i < kHeld; ++i) {
+      s[i] = x[i] > -__builtin_inff() ? expf(x[i] - top) : 0.0f;
+      total += s[i];
+    }
+    total = __builtin_fmaxf(lane_reduce<Lanes>(total, OpSum{}), kTiny);
+  }
+  *reinterpret_cast<f32x4*>(row + e0) = f32x4{};
+
+  // The chosen experts' scores, then their sum and mean gradient.
   float sum = 0.0f;
   for (int k = lane; k < p.top_k; k += Lanes) {
     const int id = live ? p.ids[t * p.top_k + k] : -1;
-    is[slot * SG_MAX_TOP_K + k] = id;
-    sum += (uint32_t)id < (uint32_t)p.E ? st[id] : 0.0f;
+    float sk = 0.0f;
+    if ((uint32_t)id < (uint32_t)p.E) {
+      const float xk = clean(load_logit<DT>(p.logits, t * p.ldl + id));
+      if (xk > -__builtin_inff()) sk = soft ? expf(xk - top) / total : sigmoid_of(xk);
+    }
+    us[k] = {id, sk};
+    sum += sk;
   }
   sum = lane_reduce<Lanes>(sum, OpSum{});
   const bool floor = !(sum >= kTiny);
   const float div = !p.renorm ? 1.0f : floor ? kTiny : sum;
   float dot = 0.0f;
-  for (int k = lane; k < p.top_k; k += Lanes) {
-    const int id = is[slot * SG_MAX_TOP_K + k];
-    const bool in = (uint32_t)id < (uint32_t)p.E;
-    const float g = in ? p.dweights[t * p.top_k + k] * p.scale : 0.0f;
-    const float r = in ? st[id] / div : 0.0f;
-    dot += g * r;
-  }
+  for (int k = lane; k < p.top_k; k += Lanes)
+    dot += us[k].s > 0.0f ? p.dweights[t * p.top_k + k] * p.scale * (us[k].s / div) : 0.0f;
   dot = lane_reduce<Lanes>(dot, OpSum{});
   const float mean = p.renorm && !floor ? dot : 0.0f;
   for (int k = lane; k < p.top_k; k += Lanes) {
-    const int id = is[slot * SG_MAX_TOP_K + k];
-    const bool in = (uint32_t)id < (uint32_t)p.E;
-    const float g = in ? p.dweights[t * p.top_k + k] * p.scale : 0.0f;
-    us[slot * SG_MAX_TOP_K + k] = in ? st[id] / div * (g - mean) : 0.0f;
+    const float sk = us[k].s;
+    float u = 0.0f;
+    if (sk > 0.0f) {
+      u = sk / div * (p.dweights[t * p.top_k + k] * p.scale - mean);
+      if (!soft) u *= 1.0f - sk;
+    }
+    us[k].s = u;
   }
-  const float total = p.renorm && !floor ? 0.0f : dot;
-  __syncthreads();
-  float u[kHeld] = {};
-  for (int k = 0; k < p.top_k; ++k) {
-    const int id = is[slot * SG_MAX_TOP_K + k];
-    const float v = us[slot * SG_MAX_TOP_K + k];
+  wave_sync();
+  // An expert named more than once takes the sum, in the order of its names.
+  for (int k = lane; k < p.top_k; k += Lanes) {
+    const int id = us[k].id;
+    float u = 0.0f;
+    for (int q = 0; q < p.top_k; ++q) u += us[q].id == id ? us[q].s : 0.0f;
+    if ((uint32_t)id < (uint32_t)p.E) row[id] = u;
+  }
+  wave_sync();
+  if (!live || e0 >= p.E) return;
+  f32x4 d = *reinterpret_cast<const f32x4*>(row + e0);
+  const float all = p.renorm && !floor ? 0.0f : dot / total;
+  if (soft)
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) u[i] += id == i * Lanes + lane ? v : 0.0f;
-  }
-  if (!live) return;
-#pragma unroll
-  for (int i = 0; i < kHeld; ++i) {
-    const int e = i * Lanes + lane;
-    if (e >= p.E) continue;
-    const float d = p.score == SG_SCORE_SIGMOID ? u[i] * (1.0f - s[i]) : u[i] - s[i] * total;
-    store_logit<DT>(p.dlogits, t * p.lddl + e, x[i] > -__builtin_inff() ? d : 0.0f);
-  }
+    for (int i = 0; i < kHeld; ++i) d[i] -= s[i] * all;
+  store_row4<DT>(p, t, e0, d);
 }
 
 // ------------------------------------------------------------------ the plan
@@ -333,19 +517,31 @@ __global__ void __launch_bounds__(kPlanThreads) moe_plan_place_kernel(const Plan
   }
   __syncthreads();
 
-  // Totals of the buckets, and how many of each come before this block.
-  int total = 0, before = 0, own = 0;
-  if (tid < n) {
-    for (int w = 0; w < kPlanWaves; ++w) own += bins[w][tid];
-    if constexpr (Multi) {
-      for (int b = 0; b < (int)gridDim.x; ++b) {
-        const int v = p.counts[(int64_t)b * n + tid];
-        total += v;
-        before += b < (int)blockIdx.x ? v : 0;
+  // Totals of the buckets, and how many of each come before this block: the
+  // waves share the blocks' counts, lane l taking buckets l, l + 64 ... (one
+  // thread a bucket going through 128 blocks took 25 us of latency).
+  int total = 0, before = 0;
+  if constexpr (Multi) {
+    __shared__ int sums[kPlanWaves][kPlanBins], firsts[kPlanWaves][kPlanBins];
+    for (int e = lane; e < n; e += 64) {
+      int sum = 0, first = 0;
+#pragma unroll 8
+      for (int b = wave; b < (int)gridDim.x; b += kPlanWaves) {
+        const int v = p.counts[(int64_t)b * n + e];
+        sum += v;
+        first += b < (int)blockIdx.x ? v : 0;
       }
-    } else {
-      total = own;
+      sums[wave][e] = sum;
+      firsts[wave][e] = first;
     }
+    __syncthreads();
+    if (tid < n)
+      for (int w = 0; w < kPlanWaves; ++w) {
+        total += sums[w][tid];
+        before += firsts[w][tid];
+      }
+  } else if (tid < n) {
+    for (int w = 0; w < kPlanWaves; ++w) total += bins[w][tid];
   }
   // Exclusive scan of the totals (the first n <= 257 threads: waves 0 .. 4).
   int upto = total;
@@ -384,12 +580,10 @@ __global__ void __launch_bounds__(kPlanThreads) moe_plan_place_kernel(const Plan
       p.slots[i] = key < p.E ? place : -1;
       if (place < p.P) p.rows[place] = key < p.E ? (int)(i / p.top_k) : -1;
     }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+    wave_sync();
     if (in && (same >> lane) == 1)  // the last lane of its id moves the place on
       bins[wave][key] += __builtin_popcountll(same);
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+    wave_sync();
   }
 }
 
@@ -412,11 +606,9 @@ hipError_t go_route(const RouteParams& p, hipStream_t s) {
         kernel_label("moe_route_kernel", dt_label(DT), kL, "scores")};
     last_kernel() = names[p.by_score ? 1 : 0];
     if (p.by_score)
-      hipLaunchKernelGGL((moe_route_kernel<DT, Lanes, double>), grid, dim3(kBlockThreads), 0, s,
-                         p);
+      hipLaunchKernelGGL((moe_route_kernel<DT, Lanes, true>), grid, dim3(kBlockThreads), 0, s, p);
     else
-      hipLaunchKernelGGL((moe_route_kernel<DT, Lanes, float>), grid, dim3(kBlockThreads), 0, s,
-                         p);
+      hipLaunchKernelGGL((moe_route_kernel<DT, Lanes, false>), grid, dim3(kBlockThreads), 0, s, p);
   }
   return hipGetLastError();
 }
