@@ -484,40 +484,103 @@ bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 
 constexpr int64_t kI8MaxK = 131056;  // 2^14 * K < 2^31, K a multiple of 16
 
-int64_t i8_tile_rows(sg::I8Tile t) {
+struct I8Shape {
+  int64_t rows, cols;
+};
+I8Shape i8_shape(sg::I8Tile t) {
   switch (t) {
-    case sg::kI8Skinny16: return 16;
-    case sg::kI8Skinny32: return 32;
-    case sg::kI8Skinny64: return 64;
-    case sg::kI8Tile64: return 64;
-    case sg::kI8Tile128: return 128;
-    default: return 256;
+    case sg::kI8Stream16x16: return {16, 16};
+    case sg::kI8Stream16x32: return {16, 32};
+    case sg::kI8Stream16x64: return {16, 64};
+    case sg::kI8Stream32x16: return {32, 16};
+    case sg::kI8Stream32x32:
+    case sg::kI8Stream32x32x2: return {32, 32};
+    case sg::kI8Stream64x32: return {64, 32};
+    case sg::kI8Mid64x64: return {64, 64};
+    case sg::kI8Mid64x128: return {64, 128};
+    case sg::kI8Mid128x128: return {128, 128};
+    default: return {256, 256};
   }
 }
 
-bool i8_skinny(sg::I8Tile t) {
-  return t == sg::kI8Skinny16 || t == sg::kI8Skinny32 || t == sg::kI8Skinny64;
+// The streaming kernel for up to 64 rows (16 when grouped) and `cols` columns
+// of B in all.  Narrow tiles while 16 columns a workgroup are no more
+// workgroups than CUs, then 32 (MI355X, us, 16 / 32 / 64 columns: 1 x 4096 x
+// 4096 5.5 / 6.0 / 7.0; 1 x 8192 x 8192 15.4 / 15.0 / 16.6); 64 where there
+// are many workgroups of few stages each (1 x 65536 x 2048 38 / 30 / 28; 64
+// experts of 2048 x 2048 79 / 53 / 47, but 128 of 1024 x 4096 106 / 86 / 91).
+// 17 to 32 rows: five stages for one workgroup a CU, two stages for more (32 x
+// 8192 x 8192 16.5 / 20.0, 32 x 28672 x 8192 55 / 49).
+sg::I8Tile pick_i8_stream(int64_t M, int64_t cols, int64_t K) {
+  const bool narrow = cols <= 16 * kCUs;
+  if (M <= 16)
+    return narrow ? sg::kI8Stream16x16
+                  : cols > 128 * kCUs && K <= 2048 ? sg::kI8Stream16x64 : sg::kI8Stream16x32;
+  if (M <= 32)
+    return narrow ? sg::kI8Stream32x16
+                  : cols <= 32 * kCUs ? sg::kI8Stream32x32 : sg::kI8Stream32x32x2;
+  return sg::kI8Stream64x32;
 }
 
-// The kernel of a dense 8-bit product.
-sg::I8Tile pick_i8_tile(int64_t M, int64_t N, bool fits256) {
-  if (M <= 16) return sg::kI8Skinny16;
-  if (M <= 32) return sg::kI8Skinny32;
-  if (M <= 64) return sg::kI8Skinny64;
-  if (fits256 && cdiv(M, 256) * cdiv(N, 256) >= kCUs) return sg::kI8Tile256;
-  if (cdiv(M, 128) * cdiv(N, 128) >= kCUs / 2) return sg::kI8Tile128;
-  return sg::kI8Tile64;
+// The tile of a larger product: the least of a model of the time, in ns.  A
+// round of workgroups costs `start` (tile lookup, first loads, epilogue) and,
+// for each 128 bytes of K, `step` alone and `full` with every CU busy (the
+// smaller the tile, the sooner the L2's rate limits it, about 17 TB/s in all).
+// The rows are fitted to MI355X times of 64 to 4096 rows by 4096 and 8192
+// columns (us, model / measured / the best other tile): 128 x 4096 x 4096
+// 64x64 10.0 / 9.6 / 12.7; 333 x 4104 x 4112 64x128 16.5 / 18.0 / 21.3; 768 x
+// 4096 x 4096 128x128 22.3 / 21.2 / 27.7; 2048 x 4096 x 4096 256x256 44 / 42.8
+// / 47.6; 1024 x 8192 x 8192 256x256 81 / 77.8 / 83.8.
+struct I8Cost {
+  sg::I8Tile tile;
+  double start, step, full;
+};
+constexpr I8Cost kI8Costs[] = {{sg::kI8Mid64x64, 2500, 140, 210},
+                               {sg::kI8Mid64x128, 3500, 210, 350},
+                               {sg::kI8Mid128x128, 5000, 300, 550},
+                               {sg::kI8PingPong256, 6500, 950, 1300}};
+sg::I8Tile pick_i8_tile(int64_t M, int64_t groups, int64_t N, int64_t K, bool fits256) {
+  sg::I8Tile best = sg::kI8Mid64x64;
+  double least = 0;
+  for (const I8Cost& c : kI8Costs) {
+    if (c.tile == sg::kI8PingPong256 && !fits256) continue;
+    const I8Shape s = i8_shape(c.tile);
+    // Row tiles: every group's last one is half empty on average.
+    const double rows = groups == 1 ? (double)cdiv(M, s.rows)
+                                    : (double)M / s.rows + 0.5 * (double)groups;
+    const double wgs = (rows > (double)groups ? rows : (double)groups) * (double)cdiv(N, s.cols);
+    const double rounds = (double)(int64_t)(wgs / kCUs), left = wgs / kCUs - rounds;
+    const double k = (double)cdiv(K, 128);
+    double ns = rounds * (c.start + k * c.full);
+    if (left > 0) ns += c.start + k * (c.step + (c.full - c.step) * left);
+    if (least == 0 || ns < least) {
+      least = ns;
+      best = c.tile;
+    }
+  }
+  return best;
 }
 
-// The kernel of a grouped 8-bit product, from the groups' mean rows: the
-// offsets themselves are in device memory.
-sg::I8Tile pick_i8_grouped_tile(int64_t R, int64_t G, int64_t N, bool fits256) {
-  const int64_t mean = cdiv(R, G);
-  if (mean <= 12) return sg::kI8Skinny16;
-  if (mean <= 24) return sg::kI8Skinny32;
-  if (mean <= 64) return sg::kI8Skinny64;
-  if (fits256 && mean >= 192 && cdiv(R, 256) * cdiv(N, 256) >= kCUs) return sg::kI8Tile256;
-  return sg::kI8Tile128;
+// Dense: streaming up to 64 rows (for 33 to 64 only while its workgroups fit
+// the CUs: 64 x 8192 x 8192 19.4 us against 64x64 tiles' 25.8, 64 x 16384 x
+// 2048 13.1 against 9.9).
+sg::I8Tile pick_i8_dense(int64_t M, int64_t N, int64_t K, bool fits256) {
+  if (M <= 32 || (M <= 64 && N <= 32 * kCUs)) return pick_i8_stream(M, N, K);
+  return pick_i8_tile(M, 1, N, K, fits256);
+}
+
+// Grouped, from the groups' mean rows (the offsets are in device memory).  Up
+// to 8 rows a group on average stream (64 experts of 2048 x 2048, us, 64x128
+// tiles / streaming: 4 rows 60 / 47, 16 rows 60 / 68).  Beyond, each group's B
+// comes from memory whatever the tile, so 256x256 tiles win as soon as they
+// fill the CUs (64 experts of 2048 x 2048 with 64 rows each 64x128 / 128x128 /
+// 256x256: 70 / 79 / 64 us; 256 rows 203 / 160 / 91).
+sg::I8Tile pick_i8_grouped(int64_t R, int64_t G, int64_t N, int64_t K, bool fits256) {
+  const int64_t groups = G < R ? G : R;
+  if (cdiv(R, G) <= 8) return pick_i8_stream(1, groups * N, K);
+  if (fits256 && (groups > R / 256 ? groups : R / 256) * cdiv(N, 256) >= kCUs)
+    return sg::kI8PingPong256;
+  return pick_i8_tile(R, groups, N, K, fits256);
 }
 
 // The shared checks and launch of the 8-bit products; G = 0: dense.
@@ -553,18 +616,9 @@ int i8_run(const char* who, int G, int64_t M, int64_t N, int64_t K, const int32_
   if (rows && a_rows > 0 && (a_rows - 1) * lda + K >= kMaxExtent)
     return fail(SG_ERR_SHAPE, "%s: gathered A spans 2^31 bytes or more", who);
   const bool fits256 = 256 * lda < kMaxExtent && 256 * ldb < kMaxExtent;
-  const sg::I8Tile tile = G == 0 ? pick_i8_tile(M, N, fits256)
-                                 : pick_i8_grouped_tile(M, G, N, fits256);
-  const int64_t T = i8_tile_rows(tile);
-  sg::I8Params p;
-  p.wk = 1;
-  int64_t tn = T;
-  if (i8_skinny(tile)) {
-    // Each wave takes a K range of 512 bytes or more.
-    p.wk = 8;
-    while (p.wk > 1 && K < 512 * p.wk) p.wk /= 2;
-    tn = (tile == sg::kI8Skinny64 ? 256 : 128) / p.wk;
-  }
+  const sg::I8Tile tile = G == 0 ? pick_i8_dense(M, N, K, fits256)
+                                 : pick_i8_grouped(M, G, N, K, fits256);
+  const int64_t T = i8_shape(tile).rows, tn = i8_shape(tile).cols;
   if ((T > tn ? T : tn) * (lda > ldb ? lda : ldb) >= kMaxExtent)
     return fail(SG_ERR_SHAPE, "%s: an operand panel spans 2^31 bytes or more", who);
   const int64_t tiles_n = cdiv(N, tn);
@@ -572,6 +626,7 @@ int i8_run(const char* who, int G, int64_t M, int64_t N, int64_t K, const int32_
   const int64_t groups = G == 0 ? 1 : G < M ? G : M;
   const int64_t tiles_m = G == 0 ? cdiv(M, T) : (M + groups * (T - 1)) / T;
   if (tiles_m * tiles_n > 0x7fffffffLL) return fail(SG_ERR_SHAPE, "%s: too many tiles", who);
+  sg::I8Params p;
   p.A = A;
   p.B = B;
   p.SA = SA;

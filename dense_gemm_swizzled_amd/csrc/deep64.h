@@ -33,12 +33,10 @@
 
 namespace sg {
 
-template <int BM, int Elem, bool AMn, bool BMn, bool Rows = false>
+template <int BM, bool IsBF16, bool AMn, bool BMn>
 struct DeepTile {
   static_assert(BM == 64 || BM == 128, "64x64 or 128x128 tiles");
-  using Base = GemmTile<BM, BM, Elem, AMn, BMn, kSwzDefault, 4>;
-  using ALoader = typename std::conditional<Rows, RowsHalfLoader<kSwzDefault>,
-                                            HalfLoader<kSwzDefault>>::type;
+  using Base = GemmTile<BM, BM, IsBF16, AMn, BMn, kSwzDefault, 4>;
   static constexpr int kFM = Base::kFM, kFN = Base::kFN;   // 32x32 blocks per wave
   static constexpr int kStages = BM == 64 ? 8 : 5;
   static constexpr int kBK = 64;
@@ -75,12 +73,8 @@ struct DeepTile {
     const u32x4 ra = rsrc_words(j.a, j.a_bytes), rb = rsrc_words(j.b, j.b_bytes);
     const uint32_t kbytes = (uint32_t)K * 2u;
     const int T = (int)((K + kBK - 1) / kBK);
-    ALoader la;
-    HalfLoader<kSwzDefault> lb;
-    if constexpr (Rows)
-      la.init(wave, lane, j.a_pitch, j.rows, j.m_valid, j.a_total);
-    else
-      la.init(wave, lane, j.a_pitch);
+    HalfLoader<kSwzDefault> la, lb;
+    la.init(wave, lane, j.a_pitch);
     lb.init(wave, lane, j.b_pitch);
     const uint32_t s0 = lds_addr(smem);
 
@@ -88,7 +82,7 @@ struct DeepTile {
     // out of range (zero fill).  Regions 4i + wave (1 KiB each).  MN-major:
     // lane l of region r fills k-row 8r + l/8, physical chunk l%8, which
     // holds logical chunk (l%8 + 4 * bit 1 of the row) mod 8.
-    auto issue_op = [&](auto mn, const auto& ld, u32x4 rsrc, uint32_t pitch,
+    auto issue_op = [&](auto mn, const HalfLoader<kSwzDefault>& ld, u32x4 rsrc, uint32_t pitch,
                         int rows_valid, uint32_t dst, int t) {
       if constexpr (!decltype(mn)::value) {
 #pragma unroll
@@ -192,7 +186,7 @@ struct DeepTile {
     // t + kStages - 1.
     Frags f0, f1;
     asm volatile("s_waitcnt vmcnt(24)" ::: "memory");
-    PingPongTile<Elem, kSwzDefault>::barrier();
+    PingPongTile<IsBF16, kSwzDefault>::barrier();
     read(f0, 0);
     // The reads of K step kk of tile t.
     auto read_kk = [&](Frags& f, int t, int kk) {
@@ -226,7 +220,7 @@ struct DeepTile {
         asm volatile("s_waitcnt vmcnt(20) lgkmcnt(0)" ::: "memory");
       else
         asm volatile("s_waitcnt vmcnt(16) lgkmcnt(0)" ::: "memory");
-      PingPongTile<Elem, kSwzDefault>::barrier();
+      PingPongTile<IsBF16, kSwzDefault>::barrier();
       if constexpr (BM != 64) {
         issue(t + kStages - 1);
         read(nxt, t + 1);  // past the last tile: stale LDS, never used
@@ -236,7 +230,7 @@ struct DeepTile {
 #pragma unroll
           for (int m = 0; m < kFM * kFN; ++m) {
             const int fm = m / kFN, fn = (fm & 1) ? kFN - 1 - m % kFN : m % kFN;
-            acc[fm][fn] = mfma32x32x16<Elem>(cur.b[kk][fn], cur.a[kk][fm], acc[fm][fn]);
+            acc[fm][fn] = mfma32x32x16<IsBF16>(cur.b[kk][fn], cur.a[kk][fm], acc[fm][fn]);
           }
         }
         return;
@@ -248,7 +242,7 @@ struct DeepTile {
           for (int m = 0; m < kFM * kFN; ++m) {
             // snake order: consecutive MFMAs share an operand
             const int fm = m / kFN, fn = (fm & 1) ? kFN - 1 - m % kFN : m % kFN;
-            acc[fm][fn] = mfma32x32x16<Elem>(cur.b[kk][fn], cur.a[kk][fm], acc[fm][fn]);
+            acc[fm][fn] = mfma32x32x16<IsBF16>(cur.b[kk][fn], cur.a[kk][fm], acc[fm][fn]);
           }
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -272,13 +266,8 @@ struct DeepTile {
     }
     wait_vmem();  // the loads past K
 
-    if constexpr (Elem == kElemI8) {
-      PingPongTile<Elem, kSwzDefault>::barrier();  // every wave's reads are done
-      store_i8_via_lds(acc, j, smem + wave * kWaveBytes, D, d_dtype, ldd, lane, wm, wn);
-      return;
-    }
     if (d_dtype == SG_F32 && C == nullptr) {
-      PingPongTile<Elem, kSwzDefault>::barrier();  // every wave's reads are done
+      PingPongTile<IsBF16, kSwzDefault>::barrier();  // every wave's reads are done
       store_f32_via_lds(acc, j, smem + wave * kWaveBytes, D, ldd, lane, wm, wn);
     } else {
       Base::epilogue(acc, j, C, c_dtype, D, d_dtype, ldd, lane, wm, wn);
@@ -327,42 +316,6 @@ struct DeepTile {
       const int ml = wm * Base::kWM + (int)r;
       if (ml >= j.m_valid || nl >= j.n_valid) continue;
       *reinterpret_cast<u32x4*>(static_cast<float*>(D) + (j.d_row0 + ml) * ldd + j.n0 + nl) = d;
-    }
-  }
-
-  // The 8-bit product's epilogue over the same staging: the integer sums go
-  // through LDS as they are, and each lane scales the four columns of a row
-  // that it stores (its column scales are the same for every row).
-  __device__ __forceinline__ static void store_i8_via_lds(const f32x16 (&acc)[kFM][kFN],
-                                                          const TileJob& j, char* area, void* D,
-                                                          int d_dtype, int64_t ldd, int lane,
-                                                          int wm, int wn) {
-#pragma unroll
-    for (int fm = 0; fm < kFM; ++fm)
-#pragma unroll
-      for (int fn = 0; fn < kFN; ++fn)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const f32x4 v = {acc[fm][fn][4 * q], acc[fm][fn][4 * q + 1], acc[fm][fn][4 * q + 2],
-                           acc[fm][fn][4 * q + 3]};
-          const uint32_t r = (uint32_t)(32 * fm + (lane & 31));
-          const uint32_t c = (uint32_t)(8 * fn + 2 * q + (lane >> 5));
-          lds_write16(area, r * kRowBytes + 16u * (c ^ row_key(r)), __builtin_bit_cast(u32x4, v));
-        }
-    constexpr int kLanesPerRow = kRowBytes / 16, kRowsPerStep = 64 / kLanesPerRow;
-    const uint32_t cc = (uint32_t)(lane % kLanesPerRow);
-    const int nl = wn * Base::kWN + 4 * (int)cc, cols = j.n_valid - nl;
-    float sb[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) sb[e] = j.sb[min(nl + e, j.n_valid - 1)];
-#pragma unroll
-    for (int s = 0; s < kWaveBytes / 1024; ++s) {
-      const uint32_t r = (uint32_t)(kRowsPerStep * s + lane / kLanesPerRow);
-      const u32x4 d = lds_read16(area, r * kRowBytes + 16u * (cc ^ row_key(r)));
-      const int ml = wm * Base::kWM + (int)r;
-      if (ml >= j.m_valid || cols <= 0) continue;
-      const f32x4 v = i8_scale4(__builtin_bit_cast(f32x4, d), i8_row_scale<Rows>(j, ml), sb);
-      store_i8_chunk(v, D, d_dtype, (j.d_row0 + ml) * ldd + j.n0 + nl, cols, j.vec);
     }
   }
 };

@@ -10,13 +10,12 @@
 // split of K changes the result.  A K tile of the 16-bit kernels is 128 bytes
 // of a row whatever the element, and v_mfma_i32_16x16x64_i8 and
 // v_mfma_i32_32x32x32_i8 take the same 16 bytes a lane as their 16-bit
-// counterparts in the same cycles, so large products run the mainloops of
-// pingpong16.h and deep64.h (Elem = kElemI8) at twice the operations per
-// byte.  Products of few rows are bound by reading B once and run
-// i8_skinny_kernel below.
+// counterparts in the same cycles, so large products run the mainloop of
+// pingpong16.h (Elem = kElemI8) at twice the operations per byte.  Middle
+// sizes run i8_mid_kernel, products of few rows, bound by reading B once,
+// i8_stream_kernel.
 #pragma once
 
-#include "deep64.h"
 #include "i8_params.h"
 #include "pingpong16.h"
 
@@ -140,103 +139,344 @@ __global__ void __launch_bounds__(512, 1) i8_pingpong_kernel(const I8Params p) {
   clock_end(p.clk, cs);
 }
 
-template <int BM, bool Grouped, bool Rows>
-__global__ void __launch_bounds__(256, 1) i8_deep_kernel(const I8Params p) {
-  using Tile = DeepTile<BM, kElemI8, false, false, Rows>;
+// Middle sizes, fewer 256x256 tiles than CUs: BM x BN tiles of eight waves in
+// two groups of four, one wave of each group per SIMD.  Group g multiplies K
+// tiles 2i + g, and the groups work one phase apart: in phase t one group
+// reads K tile t from LDS into registers while the other runs its MFMAs over
+// tile t - 1, so the LDS, the matrix cores and the loads are all busy in every
+// phase.  (With both groups in the same phase, or with one group of four, the
+// units wait for each other: a 128x128x128-byte step took 0.53 us instead of
+// the 0.33 us its LDS traffic needs.)  The groups' integer sums are added in
+// the epilogue, exactly.
+//
+// One ring of kStages K tiles serves both groups.  Every wave loads an eighth
+// of tile t + kStages - 1 in phase t, into the stage whose tile t - 1 was read
+// in the phase before; a phase ends when the wave's part of tile t + 1 has
+// landed, and its barrier makes that tile whole.
+template <int BM, int BN, bool Rows>
+struct I8MidTile {
+  static constexpr int kWM = BM / 2, kWN = BN / 2;        // a wave's block
+  static constexpr int kFM = kWM / 32, kFN = kWN / 32;    // 32x32 blocks of it
+  // K tiles are kSub times 128 bytes wide: 64x64 tiles take two at a time,
+  // which halves the barriers of their short phases.
+  static constexpr int kSub = BM * BN <= 64 * 64 ? 2 : 1;
+  static constexpr int kABytes = BM * 128, kSubBytes = (BM + BN) * 128;
+  static constexpr int kStageBytes = kSub * kSubBytes;
+  static constexpr int kStages = 163840 / kStageBytes;    // 5 or 6
+  static constexpr int kLdsBytes = kStages * kStageBytes;
+  static constexpr int kSubLoads = (BM + BN) / 64;
+  static constexpr int kLoads = kSub * kSubLoads;         // a wave's loads per K tile
+  static constexpr int kSteps = 4 * kSub;                 // 32-byte K steps of a tile
+  static_assert(kStages >= 3 && (kStages - 2) * kLoads < 64, "the ring");
+  using ALoader = typename std::conditional<Rows, RowsHalfLoader<kSwzDefault>,
+                                            HalfLoader<kSwzDefault>>::type;
+
+  struct Frags {
+    u32x4 a[kSteps][kFM], b[kSteps][kFN];
+  };
+
+  // The end of a phase.
+  __device__ __forceinline__ static void end_phase() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"i"((kStages - 2) * kLoads) : "memory");
+    PingPongTile<kElemI8, kSwzDefault>::barrier();
+  }
+
+  __device__ __forceinline__ static void run(char* smem, const TileJob& j, const I8Params& p) {
+    const int tid = threadIdx.x;
+    const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int g = wave >> 2, w4 = wave & 3, wm = w4 >> 1, wn = w4 & 1;
+    const int lrow = lane & 31, lhalf = lane >> 5;
+    const u32x4 ra = rsrc_words(j.a, j.a_bytes), rb = rsrc_words(j.b, j.b_bytes);
+    const uint32_t kbytes = (uint32_t)p.K;
+    const int T = (int)((p.K + 128 * kSub - 1) / (128 * kSub)), Tg = (T + 1) / 2;
+    // The half-tile loaders with eight waves: wave w fills regions 8q + w, the
+    // loaders' load 2q of "wave" w.
+    ALoader la;
+    HalfLoader<kSwzDefault> lb;
+    if constexpr (Rows)
+      la.init(wave, lane, j.a_pitch, j.rows, j.m_valid, j.a_total);
+    else
+      la.init(wave, lane, j.a_pitch);
+    lb.init(wave, lane, j.b_pitch);
+    const uint32_t ring = lds_addr(smem);
+    const Scales sc = load_scales(j, lane, g, wm, wn);
+
+    // Load q of the wave's part of K tile t; past K every chunk reads as zero.
+    auto issue1 = [&](int t, int q) {
+      const int sub = q / kSubLoads, l = q % kSubLoads;
+      const uint32_t stage = ring + (uint32_t)((t % kStages) * kStageBytes + sub * kSubBytes);
+      const uint32_t k0 = (uint32_t)(kSub * t + sub) * 128u;
+      if (l < BM / 64)
+        la.issue(ra, stage, wave, 2 * l, j.m_valid, k0, kbytes);
+      else
+        lb.issue(rb, stage + kABytes, wave, 2 * (l - BM / 64), j.n_valid, k0, kbytes);
+    };
+    auto issue = [&](int t) {
+#pragma unroll
+      for (int q = 0; q < kLoads; ++q) issue1(t, q);
+    };
+    uint32_t oa[4], ob[4];  // fragment 0 of each step of 128 bytes; the next ones 4 KiB on
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      oa[s] = lds_offset<128, kSwzDefault>(wm * kWM + lrow, 2 * s + lhalf);
+      ob[s] = kABytes + lds_offset<128, kSwzDefault>(wn * kWN + lrow, 2 * s + lhalf);
+    }
+    f32x16 acc[kFM][kFN];
+#pragma unroll
+    for (int m = 0; m < kFM; ++m)
+#pragma unroll
+      for (int n = 0; n < kFN; ++n) acc[m][n] = f32x16{};
+
+#pragma unroll
+    for (int t = 0; t < kStages - 1; ++t) issue(t);
+    end_phase();  // tile 0 has landed (its newer loads are those of a phase's end)
+    if (g) {      // group 1 is one phase behind
+      issue(kStages - 1);
+      end_phase();
+    }
+    for (int i = 0; i < Tg; ++i) {
+      const int t = 2 * i + g;  // the phase, and the tile it reads
+      Frags f;
+      const char* st = smem + (t % kStages) * kStageBytes;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+#pragma unroll
+        for (int m = 0; m < kFM; ++m)
+          f.a[s][m] = lds_read16(st, oa[s & 3] + (s >> 2) * kSubBytes + m * 4096);
+#pragma unroll
+        for (int n = 0; n < kFN; ++n)
+          f.b[s][n] = lds_read16(st, ob[s & 3] + (s >> 2) * kSubBytes + n * 4096);
+      }
+      issue(t + kStages - 1);
+      end_phase();
+      constexpr int kMfma = kSteps * kFM * kFN, kEvery = kMfma / kLoads;
+#pragma unroll
+      for (int q = 0; q < kMfma; ++q) {
+        const int s = q / (kFM * kFN), b = q % (kFM * kFN);
+        const int m = b / kFN, n = (m & 1) ? kFN - 1 - b % kFN : b % kFN;
+        acc[m][n] = mfma32x32x16<kElemI8>(f.b[s][n], f.a[s][m], acc[m][n]);
+        if (q % kEvery == kEvery - 1 && q / kEvery < kLoads) {
+          __builtin_amdgcn_sched_barrier(0);
+          issue1(t + kStages, q / kEvery);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      end_phase();
+    }
+    wait_vmem();  // the loads past K
+    PingPongTile<kElemI8, kSwzDefault>::barrier();
+    if (!g) PingPongTile<kElemI8, kSwzDefault>::barrier();
+    store(acc, smem, j, p, sc, lane, g, w4, wm, wn);
+  }
+
+  // The scales of the outputs that a lane stores, loaded before the mainloop:
+  // after it, their latency (with gathered rows twice) added 3 us to a tile.
+  static constexpr int kRowBytes = 128 * kFN, kWaveBytes = 32 * kFM * kRowBytes;
+  static constexpr int kLanesPerRow = kRowBytes / 16, kRowsPerStep = 64 / kLanesPerRow;
+  struct Scales {
+    float a[kWaveBytes / 2048], b[4];
+  };
+  __device__ __forceinline__ static int out_row(int h, int lane, int g) {
+    return kRowsPerStep * (2 * h + g) + lane / kLanesPerRow;
+  }
+  __device__ __forceinline__ static Scales load_scales(const TileJob& j, int lane, int g, int wm,
+                                                       int wn) {
+    Scales sc;
+    const int nl = wn * kWN + 4 * (lane % kLanesPerRow);
+#pragma unroll
+    for (int h = 0; h < kWaveBytes / 2048; ++h)
+      sc.a[h] = i8_row_scale<Rows>(j, wm * kWM + out_row(h, lane, g));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sc.b[e] = j.sb[min(nl + e, j.n_valid - 1)];
+    return sc;
+  }
+
+  // Lane l of accumulator block (m, n) holds row 32m + l%32 of the wave's
+  // block, columns 32n + 8q + 4(l/32) .. +3 in registers 4q .. 4q+3.  Every
+  // wave puts its sums into LDS as rows of kRowBytes, chunk c of row r at c
+  // XOR (r mod 8) (the 8 rows of a ds_write_b128 phase then fill a bank line);
+  // the two waves of a block take alternate KiB of both groups' rows, add them,
+  // scale them and store whole rows.
+  static_assert(8 * kWaveBytes <= kLdsBytes, "staging fits the ring");
+  __device__ __forceinline__ static void store(const f32x16 (&acc)[kFM][kFN], char* smem,
+                                               const TileJob& j, const I8Params& p,
+                                               const Scales& sc, int lane, int g, int w4, int wm,
+                                               int wn) {
+    char* const mine = smem + (4 * g + w4) * kWaveBytes;
+#pragma unroll
+    for (int m = 0; m < kFM; ++m)
+#pragma unroll
+      for (int n = 0; n < kFN; ++n)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const f32x4 v = {acc[m][n][4 * q], acc[m][n][4 * q + 1], acc[m][n][4 * q + 2],
+                           acc[m][n][4 * q + 3]};
+          const uint32_t r = (uint32_t)(32 * m + (lane & 31));
+          const uint32_t c = (uint32_t)(8 * n + 2 * q + (lane >> 5));
+          lds_write16(mine, r * kRowBytes + 16u * (c ^ (r & 7u)), __builtin_bit_cast(u32x4, v));
+        }
+    __syncthreads();
+    const uint32_t cc = (uint32_t)(lane % kLanesPerRow);
+    const int nl = wn * kWN + 4 * (int)cc, cols = j.n_valid - nl;
+    if (cols <= 0) return;
+#pragma unroll
+    for (int h = 0; h < kWaveBytes / 2048; ++h) {
+      const uint32_t r = (uint32_t)out_row(h, lane, g);
+      const uint32_t off = r * kRowBytes + 16u * (cc ^ (r & 7u));
+      const int ml = wm * kWM + (int)r;
+      if (ml >= j.m_valid) continue;
+      const i32x4 s = __builtin_bit_cast(i32x4, lds_read16(smem + w4 * kWaveBytes, off)) +
+                      __builtin_bit_cast(i32x4, lds_read16(smem + (4 + w4) * kWaveBytes, off));
+      const f32x4 v = i8_scale4(__builtin_bit_cast(f32x4, s), sc.a[h], sc.b);
+      store_i8_chunk(v, p.D, p.d_dtype, (j.d_row0 + ml) * p.ldd + j.n0 + nl, cols, j.vec);
+    }
+  }
+};
+
+template <int BM, int BN, bool Grouped, bool Rows>
+__global__ void __launch_bounds__(512, 1) i8_mid_kernel(const I8Params p) {
+  using Tile = I8MidTile<BM, BN, Rows>;
   __shared__ __attribute__((aligned(4096))) char smem[Tile::kLdsBytes];
   const ClockStamp cs = clock_begin(p.clk);
   TileJob j;
   if constexpr (Grouped) {
-    if (!i8_grouped_job<BM, Rows>(p, blockIdx.x, j, BM)) return;
+    if (!i8_grouped_job<BM, Rows>(p, blockIdx.x, j, BN)) return;
   } else {
-    j = i8_dense_job<BM>(p, blockIdx.x, BM);
+    j = i8_dense_job<BM>(p, blockIdx.x, BN);
   }
-  Tile::run(smem, j, p.K / 2, nullptr, SG_NONE, p.D, p.d_dtype, p.ldd);
+  Tile::run(smem, j, p);
   clock_end(p.clk, cs);
 }
 
 // ---- few rows
 
-// 16*MT rows by 16*NT*(8/wk) columns.  Bound by the bytes of B, which every
-// row tile reads once and no two waves share, so B goes from memory to the
-// MFMA operands through registers (lane l: row l%16, 16 bytes at 16(l/16) of
-// a 64-byte K step) with two stages of U steps in flight per wave.  wk of the
-// eight waves split K among them and add their integer sums through LDS.
-template <int MT, int NT>
-struct SkinnyTile {
-  static constexpr int kU = MT * NT == 1 ? 4 : MT * NT <= 4 ? 2 : 1;
-  struct Stage {
-    u32x4 a[kU][MT], b[kU][NT];
-  };
+// 16*MT rows by BN = 16*NT*WN columns, for products that are bound by reading
+// B.  Eight waves: WN along N, the other WK = 8 / WN split K.  A stage is 512
+// bytes of K of both operands, loaded straight to LDS an eighth by each wave
+// and kStages deep, so the loads in flight take no registers and every wave
+// waits once per 512 bytes; wave (wn, wk) multiplies its 64*WN bytes of the
+// stage.  The integer sums of the WK waves are added through LDS at the end.
+// (Reading both operands into registers instead kept too few loads in flight:
+// 16 x 8192 x 8192 took 20 us against 12 for the bytes.)
+template <int MT, int NT, int WN, int Stages>
+struct I8StreamTile {
+  static constexpr int kBM = 16 * MT, kBN = 16 * NT * WN, kWK = 8 / WN;
+  static constexpr int kSubBytes = (kBM + kBN) * 128;  // 128 bytes of K: A, then B
+  static constexpr int kStageBytes = 4 * kSubBytes;
+  static constexpr int kStages = Stages;
+  static constexpr int kLoadsA = MT, kLoadsB = NT * WN, kLoads = kLoadsA + kLoadsB;
   static constexpr int kBlocks = MT * NT;
-  static constexpr int kLdsBytes = 8 * kBlocks * 1024;
+  static constexpr int kSumBytes = kWK > 1 ? 8 * kBlocks * 1024 : 0;
+  static constexpr int kRingBytes = kStages * kStageBytes;
+  static constexpr int kLdsBytes = kRingBytes > kSumBytes ? kRingBytes : kSumBytes;
+  static_assert(kStages >= 2 && (kStages - 1) * kLoads < 64 && kLdsBytes <= 163840, "the ring");
+
+  // One wave's loads of one operand: load i fills 1 KiB region r = wave + 8i
+  // of the stage's four 128-byte wide sub-tiles (Regions each, 8 rows).
+  template <int Loads, int Regions>
+  struct Loader {
+    uint32_t voff[Loads], koff[Loads];  // byte of the operand; byte of K in the stage
+
+    // source(row): the row of the operand, or -1.
+    template <class Source>
+    __device__ __forceinline__ void init(int wave, int lane, uint32_t pitch, Source source) {
+#pragma unroll
+      for (int i = 0; i < Loads; ++i) {
+        const int idx = wave + 8 * i, sub = idx / Regions, r = idx % Regions;
+        const uint32_t at = swz_bytes<kSwzDefault>((uint32_t)r * 1024u + 16u * (uint32_t)lane);
+        const int src = source((int)(at >> 7));
+        koff[i] = (uint32_t)sub * 128u + (at & 127u);
+        voff[i] = src >= 0 ? (uint32_t)src * pitch + koff[i] : kOutOfRange;
+      }
+    }
+    __device__ __forceinline__ void issue(u32x4 rsrc, uint32_t stage, int wave, uint32_t k0,
+                                          uint32_t kbytes) const {
+#pragma unroll
+      for (int i = 0; i < Loads; ++i) {
+        const int idx = wave + 8 * i, sub = idx / Regions, r = idx % Regions;
+        dma16(rsrc, k0 + koff[i] < kbytes ? voff[i] + k0 : kOutOfRange,
+              stage + (uint32_t)(sub * kSubBytes + r * 1024));
+      }
+    }
+  };
 
   template <bool Rows>
   __device__ __forceinline__ static void run(char* smem, const TileJob& j, const I8Params& p) {
     const int tid = threadIdx.x;
     const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r = lane & 15, c = lane >> 4;
-    const int wk = p.wk, part = wave & (wk - 1), nb = wave / wk * (16 * NT);
-    const __amdgpu_buffer_rsrc_t ra = make_rsrc(j.a, j.a_bytes), rb = make_rsrc(j.b, j.b_bytes);
-    uint32_t ao[MT], bo[NT];
+    const int wk = wave % kWK, wn = wave / kWK;
+    const u32x4 ra = rsrc_words(j.a, j.a_bytes), rb = rsrc_words(j.b, j.b_bytes);
+    Loader<kLoadsB, kBN / 8> lb;
+    Loader<kLoadsA, kBM / 8> la;
+    lb.init(wave, lane, j.b_pitch, [&](int n) { return n < j.n_valid ? n : -1; });
+    la.init(wave, lane, j.a_pitch, [&](int m) {
+      if (m >= j.m_valid) return -1;
+      if (!Rows) return m;
+      const int src = j.rows[m];
+      return (uint32_t)src < (uint32_t)j.a_total ? src : -1;
+    });
+    const uint32_t kbytes = (uint32_t)p.K, ring = lds_addr(smem);
+    const int T = (int)((p.K + 511) >> 9);
+    auto issue = [&](int t) {
+      const uint32_t stage = ring + (uint32_t)((t % kStages) * kStageBytes);
+      lb.issue(rb, stage + kBM * 128, wave, (uint32_t)t * 512u, kbytes);
+      la.issue(ra, stage, wave, (uint32_t)t * 512u, kbytes);
+    };
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      const int m = 16 * mt + r;
-      ao[mt] = kOutOfRange;
-      if (m < j.m_valid) {
-        const int src = Rows ? j.rows[m] : m;
-        if (!Rows || (uint32_t)src < (uint32_t)j.a_total)
-          ao[mt] = (uint32_t)src * j.a_pitch + 16u * (uint32_t)c;
-      }
-    }
+    for (int t = 0; t < kStages - 1; ++t) issue(t);
+
+    float sa[MT], sb[NT][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int n = nb + 16 * nt + r;
-      bo[nt] = n < j.n_valid ? (uint32_t)n * j.b_pitch + 16u * (uint32_t)c : kOutOfRange;
-    }
+    for (int mt = 0; mt < MT; ++mt) sa[mt] = i8_row_scale<Rows>(j, 16 * mt + r);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        sb[nt][e] = j.sb[min(16 * (NT * wn + nt) + 4 * c + e, j.n_valid - 1)];
     f32x4 acc[MT][NT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) acc[mt][nt] = f32x4{};
+    uint32_t oa[WN], ob[WN];  // the wave's K steps: row block 0; the next 2 KiB on
+#pragma unroll
+    for (int s = 0; s < WN; ++s) {
+      const int step = wk * WN + s;
+      const uint32_t at = (uint32_t)((step >> 1) * kSubBytes);
+      oa[s] = at + lds_offset<128, kSwzDefault>(r, 4 * (step & 1) + c);
+      ob[s] = at + kBM * 128 + lds_offset<128, kSwzDefault>(16 * NT * wn + r, 4 * (step & 1) + c);
+    }
 
-    const int steps = (int)((p.K + 63) >> 6);
-    const int s0 = steps * part / wk, s1 = steps * (part + 1) / wk;
-    const uint32_t kend = (uint32_t)p.K - 16u * (uint32_t)c;  // K is a multiple of 16
-    auto load = [&](Stage& f, int s) {
+    for (int t = 0; t < T; ++t) {
+      // This wave's part of stage t has landed and its reads of stage t - 1
+      // are done; after the barrier both hold for every wave.
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"i"((kStages - 2) * kLoads) : "memory");
+      PingPongTile<kElemI8, kSwzDefault>::barrier();
+      const char* st = smem + (t % kStages) * kStageBytes;
+      u32x4 fa[WN][MT], fb[WN][NT];
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const uint32_t k = 64u * (uint32_t)(s + u);
-        const bool ok = s + u < s1 && (int)k < (int)kend;
+      for (int s = 0; s < WN; ++s) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          f.b[u][nt] = buffer_load16(rb, ok ? bo[nt] + k : kOutOfRange);
+        for (int mt = 0; mt < MT; ++mt) fa[s][mt] = lds_read16(st, block_at(oa[s], mt));
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-          f.a[u][mt] = buffer_load16(ra, ok ? ao[mt] + k : kOutOfRange);
+        for (int nt = 0; nt < NT; ++nt) fb[s][nt] = lds_read16(st, block_at(ob[s], nt));
       }
-    };
-    auto mma = [&](const Stage& f) {
+      issue(t + kStages - 1);
 #pragma unroll
-      for (int u = 0; u < kU; ++u)
+      for (int s = 0; s < WN; ++s)
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
-            acc[mt][nt] = mfma16x16x32<kElemI8>(f.b[u][nt], f.a[u][mt], acc[mt][nt]);
-    };
-    Stage f0, f1;
-    load(f0, s0);
-    for (int s = s0; s < s1; s += 2 * kU) {
-      load(f1, s + kU);
-      mma(f0);
-      load(f0, s + 2 * kU);
-      mma(f1);
+            acc[mt][nt] = mfma16x16x32<kElemI8>(fb[s][nt], fa[s][mt], acc[mt][nt]);
     }
 
     // Lane l of a block holds columns 4c .. 4c+3 of row l%16.  Block b's sums
-    // over the wk waves are finished by wave b mod wk of them.
-    if (wk > 1) {
+    // over the WK waves are finished by wave b mod WK of them.
+    wait_vmem();  // the loads past K
+    if constexpr (kWK > 1) {
+      __syncthreads();
 #pragma unroll
       for (int b = 0; b < kBlocks; ++b)
         lds_write16(smem, (uint32_t)((wave * kBlocks + b) * 1024 + 16 * lane),
@@ -245,39 +485,41 @@ struct SkinnyTile {
     }
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b) {
-      if (b % wk != part) continue;
+      if (b % kWK != wk) continue;
       i32x4 v = __builtin_bit_cast(i32x4, acc[b / NT][b % NT]);
-      if (wk > 1) {
+      if constexpr (kWK > 1) {
         v = i32x4{};
-        for (int w = 0; w < wk; ++w) {
-          const u32x4 o = lds_read16(
-              smem, (uint32_t)(((wave - part + w) * kBlocks + b) * 1024 + 16 * lane));
-          v += __builtin_bit_cast(i32x4, o);
-        }
-      }
-      const int ml = 16 * (b / NT) + r, nl = nb + 16 * (b % NT) + 4 * c;
-      if (ml >= j.m_valid || nl >= j.n_valid) continue;
-      float sb[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sb[e] = j.sb[min(nl + e, j.n_valid - 1)];
-      const f32x4 d = i8_scale4(__builtin_bit_cast(f32x4, v), i8_row_scale<Rows>(j, ml), sb);
+        for (int w = 0; w < kWK; ++w)
+          v += __builtin_bit_cast(
+              i32x4, lds_read16(smem, (uint32_t)(((kWK * wn + w) * kBlocks + b) * 1024 +
+                                                 16 * lane)));
+      }
+      const int ml = 16 * (b / NT) + r, nl = 16 * (NT * wn + b % NT) + 4 * c;
+      if (ml >= j.m_valid || nl >= j.n_valid) continue;
+      const f32x4 d = i8_scale4(__builtin_bit_cast(f32x4, v), sa[b / NT], sb[b % NT]);
       store_i8_chunk(d, p.D, p.d_dtype, (j.d_row0 + ml) * p.ldd + j.n0 + nl, j.n_valid - nl,
                      j.vec);
     }
   }
+
+  // The place of 16-row block b, from block 0's: rows 16 apart differ in bit 3
+  // of the XOR key (the line index), rows 32 apart in none of it.
+  __device__ __forceinline__ static uint32_t block_at(uint32_t first, int b) {
+    return (first ^ ((uint32_t)(b & 1) << 7)) + (uint32_t)b * 2048u;
+  }
 };
 
-template <int MT, int NT, bool Grouped, bool Rows>
-__global__ void __launch_bounds__(512, 1) i8_skinny_kernel(const I8Params p) {
-  using Tile = SkinnyTile<MT, NT>;
-  __shared__ __attribute__((aligned(16))) char smem[Tile::kLdsBytes];
+template <int MT, int NT, int WN, int Stages, bool Grouped, bool Rows>
+__global__ void __launch_bounds__(512, 1) i8_stream_kernel(const I8Params p) {
+  using Tile = I8StreamTile<MT, NT, WN, Stages>;
+  __shared__ __attribute__((aligned(4096))) char smem[Tile::kLdsBytes];
   const ClockStamp cs = clock_begin(p.clk);
-  const int bn = 16 * NT * 8 / p.wk;
   TileJob j;
   if constexpr (Grouped) {
-    if (!i8_grouped_job<16 * MT, Rows>(p, blockIdx.x, j, bn)) return;
+    if (!i8_grouped_job<Tile::kBM, Rows>(p, blockIdx.x, j, Tile::kBN)) return;
   } else {
-    j = i8_dense_job<16 * MT>(p, blockIdx.x, bn);
+    j = i8_dense_job<Tile::kBM>(p, blockIdx.x, Tile::kBN);
   }
   Tile::template run<Rows>(smem, j, p);
   clock_end(p.clk, cs);

@@ -19,7 +19,6 @@ struct I8Params {
   bool vec;                  // D and its row pitch are 16-byte aligned
   int tiles_m, tiles_n;      // dense only: tiles_m
   int group_m;
-  int wk;                    // skinny only: waves that share one K range
   ClockTrace clk;
   // Grouped: group g owns rows [offsets[g], offsets[g+1]) of D and the matrix
   // B + g * N * ldb; row r of D takes row rows[r] (or r) of A.

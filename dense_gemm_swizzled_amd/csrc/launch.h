@@ -13,8 +13,13 @@ namespace sg {
 
 // Tile shapes the planner chooses between.
 enum TileShape { kTile256 = 0, kTile128 = 1, kTile64 = 2 };
-// The 8-bit products: rows of a tile, and the kernel (see i8_kernels.h).
-enum I8Tile { kI8Skinny16, kI8Skinny32, kI8Skinny64, kI8Tile64, kI8Tile128, kI8Tile256 };
+// The kernels of the 8-bit products (i8_kernels.h), named by rows x columns of
+// a tile.  kI8Stream32x32: one workgroup a CU with five stages;
+// kI8Stream32x32x2: two with two.
+enum I8Tile {
+  kI8Stream16x16, kI8Stream16x32, kI8Stream16x64, kI8Stream32x16, kI8Stream32x32,
+  kI8Stream32x32x2, kI8Stream64x32, kI8Mid64x64, kI8Mid64x128, kI8Mid128x128, kI8PingPong256
+};
 struct I8Params;
 struct RouteParams;
 struct PlanParams;

@@ -463,6 +463,23 @@ struct PingPong16Tile {
 #undef SG_EPI
   }
 
+  // The scales of the wave's outputs (8-bit products), loaded before the
+  // mainloop so that their latency is not the tile's last.
+  struct Scales {
+    float a[kI], b[kJ][4];
+  };
+  __device__ __forceinline__ static void load_scales(Scales& sc, const TileJob& j, int lane,
+                                                     int g, int w4) {
+#pragma unroll
+    for (int i = 0; i < kI; ++i)
+      sc.a[i] = i8_row_scale<Rows>(j, 128 * g + 16 * i + (lane & 15));
+#pragma unroll
+    for (int jn = 0; jn < kJ; ++jn)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        sc.b[jn][e] = j.sb[min(64 * w4 + 16 * jn + 4 * (lane >> 4) + e, j.n_valid - 1)];
+  }
+
   // The epilogue of the 8-bit product: the integer accumulators become
   // acc * sa[row] * sb[column] in fp32 (the conversion rounds sums of 2^24
   // and more, by half a unit in the last place; then one rounding for each
@@ -471,20 +488,12 @@ struct PingPong16Tile {
   __device__ __forceinline__ static void epilogue_i8(f32x4 (&acc)[kI][kJ], const TileJob& j,
                                                      char* smem, int T, void* D, int d_dtype,
                                                      int64_t ldd, int lane, int g, int w4,
-                                                     bool active) {
+                                                     bool active, const Scales& sc) {
     if (active) {
-      float sb[kJ][4];
 #pragma unroll
-      for (int jn = 0; jn < kJ; ++jn)
+      for (int i = 0; i < kI; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          sb[jn][e] = j.sb[min(64 * w4 + 16 * jn + 4 * (lane >> 4) + e, j.n_valid - 1)];
-#pragma unroll
-      for (int i = 0; i < kI; ++i) {
-        const float sa = i8_row_scale<Rows>(j, 128 * g + 16 * i + (lane & 15));
-#pragma unroll
-        for (int jn = 0; jn < kJ; ++jn) acc[i][jn] = i8_scale4(acc[i][jn], sa, sb[jn]);
-      }
+        for (int jn = 0; jn < kJ; ++jn) acc[i][jn] = i8_scale4(acc[i][jn], sc.a[i], sc.b[jn]);
     }
     if (d_dtype == SG_F32) {
       if (!active) return;
@@ -578,6 +587,9 @@ struct PingPong16Tile {
     if constexpr (AMn) init_bmn(xam, g, w4, lane, j.a_pitch, a_rows);
     if constexpr (BMn) init_bmn(xbm, g, w4, lane, j.b_pitch, b_rows);
 
+    [[maybe_unused]] Scales sc;
+    if constexpr (Elem == kElemI8) load_scales(sc, j, lane, g, w4);
+
     // Tiles 0 and 1 (B before A, the order the mainloop keeps); the K-exact
     // mainloop loads A of tile 1 itself.
     const bool kexact = AMn || BMn || (K & (kBK - 1)) == 0;
@@ -655,7 +667,7 @@ struct PingPong16Tile {
     wait_vmem();  // the C block, or the zero-filled loads past K
 
     if constexpr (Elem == kElemI8) {
-      epilogue_i8(acc, j, smem, T, D, d_dtype, ldd, lane, g, w4, a_rows > 0);
+      epilogue_i8(acc, j, smem, T, D, d_dtype, ldd, lane, g, w4, a_rows > 0, sc);
       return;
     }
 

@@ -7,6 +7,6 @@ namespace sg {
 template __global__ void i8_pingpong_kernel<false, false>(const I8Params);
 template __global__ void i8_pingpong_kernel<true, false>(const I8Params);
 template __global__ void i8_pingpong_kernel<true, true>(const I8Params);
-template __global__ void i8_deep_kernel<64, true, true>(const I8Params);
-template __global__ void i8_deep_kernel<128, true, true>(const I8Params);
+template __global__ void i8_mid_kernel<64, 128, true, true>(const I8Params);
+template __global__ void i8_mid_kernel<128, 128, true, true>(const I8Params);
 }  // namespace sg

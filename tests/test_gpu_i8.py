@@ -51,11 +51,11 @@ def run(a, sa, b, sb, **kw):
 
 # Sizes that reach every kernel, with edges in M, N and K.
 SIZES = [
-    (1, 1, 16, "skinny"), (1, 8, 0, "skinny"), (1, 257, 1040, "skinny"), (3, 40, 48, "skinny"),
-    (16, 128, 4096, "skinny"), (17, 100, 80, "skinny"), (32, 264, 528, "skinny"),
-    (33, 130, 144, "skinny"), (64, 513, 2064, "skinny"), (65, 72, 272, "deep"),
-    (100, 999, 128, "deep"), (300, 264, 208, "deep"), (129, 4097, 144, "deep"),
-    (1000, 2050, 400, "deep"), (2000, 2304, 16, "deep"), (4096, 4096, 128, "pingpong"),
+    (1, 1, 16, "stream"), (1, 8, 0, "stream"), (1, 257, 1040, "stream"), (3, 40, 48, "stream"),
+    (16, 128, 4096, "stream"), (17, 100, 80, "stream"), (32, 264, 528, "stream"),
+    (33, 130, 144, "stream"), (64, 513, 2064, "stream"), (65, 72, 272, "mid"),
+    (100, 999, 128, "mid"), (300, 264, 208, "mid"), (129, 4097, 144, "mid"),
+    (1000, 2050, 400, "mid"), (2000, 2304, 16, "mid"), (4096, 4096, 128, "pingpong"),
     (4000, 4111, 192, "pingpong"), (4097, 4096, 256, "pingpong"), (8200, 2056, 80, "pingpong"),
 ]
 
