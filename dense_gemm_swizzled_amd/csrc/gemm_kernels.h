@@ -162,12 +162,15 @@ __device__ __forceinline__ void store_d_chunk(f32x4 v, const c_chunk_t<CD>& c, v
 
 // 16 bytes of one D row (4 fp32 or 8 16-bit values) of which the first `cols`
 // values exist: one store where D's rows are 16-byte aligned (`vec`) and all
-// of them do, else a store for each value.
-template <class V>
+// of them do, else a store for each value.  Stream: past the caches.
+template <bool Stream = false, class V>
 __device__ __forceinline__ void store_any(V* p, u32x4 d, int cols, bool vec) {
   constexpr int kN = 16 / sizeof(V);
   if (vec && cols >= kN) {
-    *reinterpret_cast<u32x4*>(p) = d;
+    if constexpr (Stream)
+      __builtin_nontemporal_store(d, reinterpret_cast<u32x4*>(p));
+    else
+      *reinterpret_cast<u32x4*>(p) = d;
     return;
   }
 #pragma unroll

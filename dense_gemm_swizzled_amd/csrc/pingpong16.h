@@ -505,7 +505,7 @@ struct PingPong16Tile {
 #pragma unroll
         for (int jn = 0; jn < kJ; ++jn) {
           const int nl = 64 * w4 + 16 * jn + 4 * (lane >> 4);
-          store_any(row + nl, __builtin_bit_cast(u32x4, acc[i][jn]), j.n_valid - nl, j.vec);
+          store_any<true>(row + nl, __builtin_bit_cast(u32x4, acc[i][jn]), j.n_valid - nl, j.vec);
         }
       }
       return;
@@ -562,9 +562,7 @@ struct PingPong16Tile {
     const int a_rows = j.m_valid - 128 * g, b_rows = j.n_valid - 128 * g;
     ALoader la;
     HalfLoader<Swz> lb;
-    if constexpr (Rows) {
-      la.init(w4, lane, j.a_pitch, j.rows + 128 * g, a_rows, j.a_total);
-    } else {
+    if constexpr (!Rows) {  // (gathered rows are looked up while B's first loads run)
       la.init(w4, lane, j.a_pitch);
       la.base += (uint32_t)(128 * g) * j.a_pitch;
     }
@@ -606,6 +604,8 @@ struct PingPong16Tile {
           lb.issue(rb, b_ring + t * kTileBytes, w4, i, b_rows, t * 128u, kbytes);
       }
       if (t == 1 && kexact) break;
+      if constexpr (Rows)
+        if (t == 0) la.init(w4, lane, j.a_pitch, j.rows + 128 * g, a_rows, j.a_total);
       if constexpr (AMn) {
         xam.template issue<0>(ra, a_ring + t * kTileBytes, w4, t * kstep_a);
         xam.template issue<1>(ra, a_ring + t * kTileBytes, w4, t * kstep_a);

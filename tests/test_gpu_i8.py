@@ -226,7 +226,8 @@ def quant_reference(x):
 
 @pytest.mark.parametrize("R,K", [(1, 1), (3, 7), (5, 16), (9, 24), (4, 500), (2, 512), (3, 520),
                                  (2, 1032), (7, 5003), (3, 4096), (2, 8192), (2, 10008),
-                                 (2, 16384), (3, 16392), (2, 40001), (300, 128)])
+                                 (2, 16384), (3, 16392), (2, 40001), (300, 128),
+                                 (17, 130), (33, 250), (2, 32768), (1, 70003)])
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_i8_quant(R, K, dtype):
     rng = np.random.default_rng(R * K)
