@@ -715,16 +715,20 @@ def mxfp6_gemm(A, SFA, B, SFB, *, fmt: str = "e2m3", out_dtype=None, out=None):
 # above takes to check them (13 to 19 us), so the checks build their messages
 # only when they fail and the C functions are called directly (6 to 9 us a
 # call).  The launches go to the tensors' device even when another is current.
+# Results carry no autograd history: moe_route_backward is a call of its own,
+# and the 8-bit products are for serving.
 
 _torch = None
+_raw_stream = None
 
 
 def _lib_torch():
     """(the loaded library, torch), imported once."""
-    global _torch
+    global _torch, _raw_stream
     if _torch is None:
         import torch
         load()
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _stream)
         _torch = torch
     return _lib, _torch
 
@@ -733,10 +737,10 @@ def _launch(f, device, *args) -> None:
     """Calls the C function f(*args, stream) with `device` current."""
     index = device.index
     if _torch.cuda.current_device() == index:
-        rc = f(*args, _torch._C._cuda_getCurrentRawStream(index))
+        rc = f(*args, _raw_stream(index))
     else:
         with _torch.cuda.device(index):
-            rc = f(*args, _torch._C._cuda_getCurrentRawStream(index))
+            rc = f(*args, _raw_stream(index))
     if rc:
         raise GemmError(rc, gemm_last_error())
 
@@ -931,6 +935,8 @@ def moe_route(logits, top_k: int, *, score: str = "softmax", bias=None, n_groups
     ldl = _pitch("logits", logits)
     n, E = logits.shape
     dt, code = _float_code("logits", logits.dtype), _score_code(score)
+    top_k, n_groups = int(top_k), int(n_groups)
+    top_groups = n_groups if top_groups is None else int(top_groups)
     groups = _GROUP_SCORES.get(group_score)
     if groups is None:
         _fail(-6, f"group_score must be one of {sorted(_GROUP_SCORES)}, got {group_score!r}")
@@ -948,9 +954,8 @@ def moe_route(logits, top_k: int, *, score: str = "softmax", bias=None, n_groups
         _packed("ids", ids, (n, top_k), T.int32)
         _on_one_device(logits, bias, weights, ids)
     _launch(lib.moe_route_run, logits.device, n, E, top_k, logits.data_ptr(), ldl, dt,
-            None if bias is None else bias.data_ptr(), code, n_groups,
-            n_groups if top_groups is None else top_groups, groups, 1 if renorm else 0, scale,
-            weights.data_ptr(), ids.data_ptr())
+            None if bias is None else bias.data_ptr(), code, n_groups, top_groups, groups,
+            1 if renorm else 0, float(scale), weights.data_ptr(), ids.data_ptr())
     return weights, ids
 
 
@@ -979,7 +984,7 @@ def moe_route_backward(dweights, logits, ids, *, score: str = "softmax", renorm:
     if out is None:
         out = T.empty((n, E), dtype=logits.dtype, device=dev)
     _launch(lib.moe_route_backward_run, dev, n, E, top_k, dweights.data_ptr(),
-            logits.data_ptr(), ldl, dt, ids.data_ptr(), code, 1 if renorm else 0, scale,
+            logits.data_ptr(), ldl, dt, ids.data_ptr(), code, 1 if renorm else 0, float(scale),
             out.data_ptr(), lddl)
     return out
 
@@ -999,7 +1004,7 @@ def moe_plan(ids, n_experts: int, *, out=None, workspace=None):
         _fail(-3, f"ids must be 2-D, got shape {tuple(ids.shape)}")
     n, top_k = ids.shape
     _packed("ids", ids, (n, top_k), T.int32)
-    P = n * top_k
+    P, n_experts = n * top_k, int(n_experts)
     need = lib.moe_plan_workspace_bytes(P, n_experts)
     if need < 0:
         _fail(need, gemm_last_error())

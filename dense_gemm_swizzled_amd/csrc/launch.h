@@ -24,6 +24,17 @@ struct I8Params;
 struct RouteParams;
 struct PlanParams;
 
+// A grid of `blocks` workgroups over x and y: a launch has fewer than 2^32
+// threads along x.  The kernel's block index is block_index().
+inline dim3 grid_of(int64_t blocks) {
+  constexpr int64_t kX = int64_t{1} << 20;
+  return blocks <= kX ? dim3((unsigned)blocks)
+                      : dim3((unsigned)kX, (unsigned)((blocks + kX - 1) / kX));
+}
+__device__ __forceinline__ int64_t block_index() {
+  return (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+}
+
 // Name of the kernel instantiation this thread launched last (set by every
 // launcher; read through gemm_last_kernel()).
 const char*& last_kernel();

@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kBlockThreads) moe_route_kernel(const RoutePar
   __shared__ RouteScratch<Lanes, Wide> scratch[kTokens];
   __shared__ Chosen chosen_all[kTokens * SG_MAX_TOP_K];
   const int lane = threadIdx.x % Lanes, slot = threadIdx.x / Lanes;
-  const int64_t t = (int64_t)blockIdx.x * kTokens + slot;
+  const int64_t t = block_index() * kTokens + slot;
   const bool live = t < p.T;  // lanes past the last token go along for the wave
   Chosen* const chosen = chosen_all + slot * SG_MAX_TOP_K;
   const float kNone = -__builtin_inff();
@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(kBlockThreads) moe_route_backward_kernel(
   __shared__ __attribute__((aligned(16))) float rows[kTokens][Lanes * kHeld];
   __shared__ Chosen us_all[kTokens * SG_MAX_TOP_K];
   const int lane = threadIdx.x % Lanes, slot = threadIdx.x / Lanes;
-  const int64_t t = (int64_t)blockIdx.x * kTokens + slot;
+  const int64_t t = block_index() * kTokens + slot;
   const bool live = t < p.T;
   const int e0 = kHeld * lane;
   float* const row = rows[slot];
@@ -594,7 +594,7 @@ constexpr const char* dt_label(int dt) {
 template <int DT, int Lanes, bool Back>
 hipError_t go_route(const RouteParams& p, hipStream_t s) {
   constexpr int kTokens = kBlockThreads / Lanes;
-  const dim3 grid((unsigned)((p.T + kTokens - 1) / kTokens));
+  const dim3 grid = grid_of((p.T + kTokens - 1) / kTokens);
   constexpr const char* kL = Lanes == 8 ? "8" : Lanes == 16 ? "16" : Lanes == 32 ? "32" : "64";
   if constexpr (Back) {
     static const char* const name = kernel_label("moe_route_backward_kernel", dt_label(DT), kL);

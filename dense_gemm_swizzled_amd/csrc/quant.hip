@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(Threads < 256 ? 256 : Threads)
   __shared__ uint32_t lds[16];
   constexpr int kRows = Threads < 256 ? 256 / Threads : 1;
   const int t = threadIdx.x % Threads;
-  const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / Threads;
+  const int64_t row = block_index() * kRows + threadIdx.x / Threads;
   if (row >= R) return;  // a row's threads together
   const int64_t x0 = row * ldx;
   int8_t* const q = Q + row * ldq;
@@ -167,7 +167,7 @@ hipError_t go(const void* X, int64_t R, int64_t K, int64_t ldx, int8_t* Q, int64
       "i8_quant_kernel", Threads <= 64 ? "wave" : Threads == 256 ? "256" : "1024",
       NV == 0 ? "twice" : "once");
   last_kernel() = name;
-  hipLaunchKernelGGL((i8_quant_kernel<DT, Threads, NV>), dim3((R + kRows - 1) / kRows),
+  hipLaunchKernelGGL((i8_quant_kernel<DT, Threads, NV>), grid_of((R + kRows - 1) / kRows),
                      dim3(Threads < 256 ? 256 : Threads), 0, s, X, R, K, ldx, Q, ldq, S);
   return hipGetLastError();
 }

@@ -321,6 +321,7 @@ int gemm_layout128_run(int layout, int64_t M, int64_t N, int64_t K, const void* 
  *       which the sum cannot overflow.  K = 0 gives D = 0.
  *   lda, ldb are multiples of 16, A and B 16-byte aligned.
  * Codes are any of -128 .. 127.  A NaN scale makes its row or column NaN.
+ * Here and in the calls below no output may overlap an input or another output.
  * Errors: SG_ERR_NULL, SG_ERR_ALIGN, SG_ERR_SHAPE (also a leading dimension
  * below its minimum, or a tile's panel of 2^31 bytes or more), SG_ERR_DTYPE,
  * SG_ERR_HIP.
@@ -513,8 +514,9 @@ int gemm_lds_image(const void* X, int64_t rows_total, int64_t K, int elem_bytes,
  * gemm_clock_trace -- turns the clock trace of this thread's later launches
  * on (buf non-NULL) or off (buf NULL).  While on, every kernel of a gemm_run,
  * gemm_strided_run, gemm_layout_run, gemm_layout128_run, grouped_gemm_run,
- * mx_gemm_run, mxfp4_gemm_run or mxfp6_gemm_run call records, for each
- * workgroup b < slots, buf[4b .. 4b+3] = {shader-clock counter at its start,
+ * mx_gemm_run, mxfp4_gemm_run, mxfp6_gemm_run, i8_gemm_run or
+ * i8_grouped_gemm_run call (of the last, the workgroups that have a tile)
+ * records, for each workgroup b < slots, buf[4b .. 4b+3] = {shader-clock counter at its start,
  * the same at the end of its first wave, real-time counter at the start, the
  * same at the end}.  The shader-clock counter (s_memtime) advances once per
  * core clock; the real-time counter (s_memrealtime) at the constant rate

@@ -55,7 +55,7 @@ SIZES = [
     (16, 128, 4096, "stream"), (17, 100, 80, "stream"), (32, 264, 528, "stream"),
     (33, 130, 144, "stream"), (64, 513, 2064, "stream"), (65, 72, 272, "mid"),
     (100, 999, 128, "mid"), (300, 264, 208, "mid"), (129, 4097, 144, "mid"),
-    (1000, 2050, 400, "mid"), (2000, 2304, 16, "mid"), (4096, 4096, 128, "pingpong"),
+    (1000, 2050, 400, "mid"), (200, 264, 16, "mid"), (2000, 2304, 16, "pingpong"), (4096, 4096, 128, "pingpong"),
     (4000, 4111, 192, "pingpong"), (4097, 4096, 256, "pingpong"), (8200, 2056, 80, "pingpong"),
 ]
 
@@ -196,6 +196,27 @@ def test_bad_offsets_stay_inside_d(R):
                            out=buf[1:R + 1])
         torch.cuda.synchronize()
         assert bool((buf[0] == 5.0).all()) and bool((buf[-1] == 5.0).all())
+
+
+@pytest.mark.parametrize("M,N", [(3, 40), (20, 40), (60, 40), (100, 72), (4096, 4100)])
+def test_k_of_zero_gives_zeros(M, N):
+    a, b = torch.zeros(M, 0, dtype=torch.int8), torch.zeros(N, 0, dtype=torch.int8)
+    for dtype in DTYPES:
+        out = torch.full((M, N), 3.0, dtype=dtype, device="cuda")
+        run(a, torch.ones(M), b, torch.ones(N), out=out)
+        assert bool((out == 0).all())
+    off = torch.tensor([0, M // 2, M], dtype=torch.int32).cuda()
+    out = torch.full((M, N), 3.0, device="cuda")
+    sg.i8_grouped_gemm(a.cuda(), torch.ones(M).cuda(), torch.zeros(2, N, 0, dtype=torch.int8).cuda(),
+                       torch.ones(2, N).cuda(), off, out=out)
+    assert bool((out == 0).all())
+
+
+def test_quant_of_no_columns_and_no_rows():
+    q, s = sg.i8_quant(torch.zeros(3, 0, device="cuda"))
+    assert q.shape == (3, 0) and bool((s == 2.0 ** -100 / 127).all())
+    q, s = sg.i8_quant(torch.zeros(0, 40, device="cuda"))
+    assert q.shape == (0, 48) and s.shape == (0,)
 
 
 def test_no_rows_and_empty_a():

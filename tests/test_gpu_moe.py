@@ -301,6 +301,30 @@ def test_route_backward_strided():
     assert bool((buf == 5.0).all())
 
 
+def test_no_tokens():
+    x = torch.zeros(0, 8, device="cuda")
+    w, ids = sg.moe_route(x, 2)
+    assert w.shape == ids.shape == (0, 2)
+    assert sg.moe_route_backward(w, x, ids).shape == (0, 8)
+
+
+def test_routing_on_another_stream():
+    rng = np.random.default_rng(14)
+    x = logits(rng, 300, 64, torch.float32).cuda()
+    want = sg.moe_route(x, 6, score="sigmoid")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        w, ids = sg.moe_route(x, 6, score="sigmoid")
+        plan = sg.moe_plan(ids, 64)
+        dx = sg.moe_route_backward(w, x, ids, score="sigmoid")
+    side.synchronize()
+    assert torch.equal(w, want[0]) and torch.equal(ids, want[1])
+    for a, b in zip(plan, sg.moe_plan(want[1], 64)):
+        assert torch.equal(a, b)
+    assert torch.equal(dx, sg.moe_route_backward(want[0], x, want[1], score="sigmoid"))
+
+
 # ------------------------------------------------------------------------ the plan
 
 def plan_reference(ids, E):
