@@ -71,6 +71,56 @@ def test_i8_gemm(M, N, K, kind, dtype):
     assert kind in sg.gemm_last_kernel(), sg.gemm_last_kernel()
 
 
+# One size for every instantiation that the tile choice can pick.
+KERNELS = [
+    (1, 4096, 1040, "i8_stream_kernel<16,16,dense>"), (7, 4500, 1040, "i8_stream_kernel<16,32,dense>"),
+    (16, 33000, 112, "i8_stream_kernel<16,64,dense>"), (20, 200, 528, "i8_stream_kernel<32,16,dense>"),
+    (29, 5001, 528, "i8_stream_kernel<32,32,dense>"), (32, 9000, 272, "i8_stream_kernel<32,32,dense>"),
+    (50, 2900, 1040, "i8_stream_kernel<64,32,dense>"), (64, 9000, 272, "i8_mid_kernel<64,64,dense>"),
+    (333, 4104, 1040, "i8_mid_kernel<64,128,dense>"), (768, 4096, 1040, "i8_mid_kernel<128,128,dense>"),
+]
+
+
+@pytest.mark.parametrize("M,N,K,name", KERNELS)
+def test_every_dense_kernel(M, N, K, name):
+    rng = np.random.default_rng(M + N + K)
+    a, b, sa, sb = codes(rng, M, K), codes(rng, N, K), scales(rng, M), scales(rng, N)
+    for dtype in (torch.bfloat16, torch.float32):
+        d = run(a, sa, b, sb, out_dtype=dtype)
+        assert sg.gemm_last_kernel() == name
+        check(d, reference(a, sa, b, sb))
+
+
+GROUPED_KERNELS = [
+    # G, N, K, rows of each group on average
+    (3, 200, 528, 4, "i8_stream_kernel<16,16,%s>"), (9, 1000, 1040, 8, "i8_stream_kernel<16,32,%s>"),
+    (40, 1000, 80, 5, "i8_stream_kernel<16,64,%s>"), (6, 300, 272, 40, "i8_mid_kernel<64,64,%s>"),
+    (5, 2800, 1040, 60, "i8_mid_kernel<64,128,%s>"), (4, 2000, 1040, 300, "i8_mid_kernel<128,128,%s>"),
+    (32, 2048, 144, 30, "i8_pingpong_kernel<%s>"),
+]
+
+
+@pytest.mark.parametrize("G,N,K,mean,name", GROUPED_KERNELS)
+@pytest.mark.parametrize("gather", [True, False])
+def test_every_grouped_kernel(G, N, K, mean, name, gather):
+    rng = np.random.default_rng(G + N + K)
+    sizes = rng.multinomial(G * mean, rng.dirichlet(np.full(G, 2.0)))
+    offsets = [0] + np.cumsum(sizes).tolist()
+    R = offsets[-1]
+    T = R // 2 + 1 if gather else R
+    rows = rng.integers(0, T, R) if gather else np.arange(R)
+    a, b, sa, sb = codes(rng, T, K), codes(rng, G, N, K), scales(rng, T), scales(rng, G, N)
+    d = sg.i8_grouped_gemm(a.cuda(), sa.cuda(), b.cuda(), sb.cuda(),
+                           torch.tensor(offsets, dtype=torch.int32).cuda(),
+                           rows=torch.from_numpy(rows.astype(np.int32)).cuda() if gather else None)
+    assert sg.gemm_last_kernel() == name % ("grouped,rows" if gather else "grouped")
+    want = torch.empty(R, N, dtype=torch.float64)
+    for g in range(G):
+        r = rows[offsets[g]:offsets[g + 1]]
+        want[offsets[g]:offsets[g + 1]] = reference(a[r], sa[r], b[g], sb[g])
+    check(d, want)
+
+
 @pytest.mark.parametrize("M", [1, 40, 70, 200])
 def test_largest_sum_is_exact(M):
     K = 131056
