@@ -713,22 +713,23 @@ def mxfp6_gemm(A, SFA, B, SFB, *, fmt: str = "e2m3", out_dtype=None, out=None):
 #
 # Small calls of these take less time on the GPU than a wrapper of the kind
 # above takes to check them (13 to 19 us), so the checks build their messages
-# only when they fail and the C functions are called directly (6 to 9 us a
-# call).  The launches go to the tensors' device even when another is current.
+# only when they fail and the C functions are called directly (6 to 8 us a
+# call, 4 of them the launch itself).  The launches go to the tensors' device even when another is current.
 # Results carry no autograd history: moe_route_backward is a call of its own,
 # and the 8-bit products are for serving.
 
 _torch = None
-_raw_stream = None
+_raw_stream = _current_device = None
 
 
 def _lib_torch():
     """(the loaded library, torch), imported once."""
-    global _torch, _raw_stream
+    global _torch, _raw_stream, _current_device
     if _torch is None:
         import torch
         load()
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _stream)
+        _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
         _torch = torch
     return _lib, _torch
 
@@ -736,7 +737,7 @@ def _lib_torch():
 def _launch(f, device, *args) -> None:
     """Calls the C function f(*args, stream) with `device` current."""
     index = device.index
-    if _torch.cuda.current_device() == index:
+    if _current_device() == index:
         rc = f(*args, _raw_stream(index))
     else:
         with _torch.cuda.device(index):
@@ -842,7 +843,7 @@ def i8_quant(X, *, out=None, out_scale=None):
     _on_one_device(X, out, out_scale)
     dev = X.device
     if out is None:
-        out = T.empty((R, Kp), dtype=T.int8, device=dev)
+        out = T.empty(R, Kp, dtype=T.int8, device=dev)
     if out_scale is None:
         out_scale = T.empty(R, dtype=T.float32, device=dev)
     _launch(lib.i8_quant_run, dev, R, K, X.data_ptr(), ldx, dt, out.data_ptr(), ldq,
@@ -867,7 +868,7 @@ def i8_gemm(A, SA, B, SB, *, out_dtype=None, out=None):
     _on_one_device(A, SA, B, SB, out)
     dev = A.device
     if out is None:
-        out = T.empty((M, N), dtype=out_dtype or T.bfloat16, device=dev)
+        out = T.empty(M, N, dtype=out_dtype or T.bfloat16, device=dev)
     _launch(lib.i8_gemm_run, dev, M, N, K, A.data_ptr(), lda, SA.data_ptr(), B.data_ptr(), ldb,
             SB.data_ptr(), out.data_ptr(), ldd, _float_code("out", out.dtype))
     return out
@@ -901,7 +902,7 @@ def i8_grouped_gemm(A, SA, B, SB, offsets, *, rows=None, out_dtype=None, out=Non
     _on_one_device(A, SA, B, SB, offsets, rows, out)
     dev = A.device
     if out is None:
-        out = T.empty((R, N), dtype=out_dtype or T.bfloat16, device=dev)
+        out = T.empty(R, N, dtype=out_dtype or T.bfloat16, device=dev)
     _launch(lib.i8_grouped_gemm_run, dev, G, R, N, K, offsets.data_ptr(), A.data_ptr(), lda,
             a_rows, None if rows is None else rows.data_ptr(), SA.data_ptr(), B.data_ptr(),
             SB.data_ptr(), out.data_ptr(), ldd, _float_code("out", out.dtype))
@@ -946,8 +947,8 @@ def moe_route(logits, top_k: int, *, score: str = "softmax", bias=None, n_groups
         _vector("bias", bias, E, T.float32)
     if out is None:
         _on_one_device(logits, bias)
-        weights = T.empty((n, top_k), dtype=T.float32, device=logits.device)
-        ids = T.empty((n, top_k), dtype=T.int32, device=logits.device)
+        weights = T.empty(n, top_k, dtype=T.float32, device=logits.device)
+        ids = T.empty_like(weights, dtype=T.int32)
     else:
         weights, ids = out
         _packed("weights", weights, (n, top_k), T.float32)
@@ -982,7 +983,7 @@ def moe_route_backward(dweights, logits, ids, *, score: str = "softmax", renorm:
     _on_one_device(logits, dweights, ids, out)
     dev = logits.device
     if out is None:
-        out = T.empty((n, E), dtype=logits.dtype, device=dev)
+        out = T.empty(n, E, dtype=logits.dtype, device=dev)
     _launch(lib.moe_route_backward_run, dev, n, E, top_k, dweights.data_ptr(),
             logits.data_ptr(), ldl, dt, ids.data_ptr(), code, 1 if renorm else 0, float(scale),
             out.data_ptr(), lddl)
@@ -1024,7 +1025,7 @@ def moe_plan(ids, n_experts: int, *, out=None, workspace=None):
         _on_one_device(ids, workspace)
         offsets = T.empty(n_experts + 1, dtype=T.int32, device=dev)
         rows = T.empty(P, dtype=T.int32, device=dev)
-        slots = T.empty((n, top_k), dtype=T.int32, device=dev)
+        slots = T.empty_like(ids)
     if workspace is None and need:
         workspace = T.empty(need, dtype=T.uint8, device=dev)
     _launch(lib.moe_plan_run, dev, n, n_experts, top_k, ids.data_ptr(), offsets.data_ptr(),

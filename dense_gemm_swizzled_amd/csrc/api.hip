@@ -678,11 +678,12 @@ bool rows_of_four(const void* p, int64_t ld, int dtype) {
   return ld % 4 == 0 && reinterpret_cast<uintptr_t>(p) % (4 * elem_bytes(dtype)) == 0;
 }
 
-// Pairs a workgroup of the plan sorts, and how many workgroups there are.
+// Pairs that a workgroup of the plan sorts, a multiple of 64 for each of its 16
+// waves: all of them up to 4096, in one launch (us, one launch / two: 4096
+// pairs 7.3 / 8.1, 8192 12.0 / 8.5), else shared by at most 256 workgroups.
 int64_t plan_chunk(int64_t P) {
-  if (P <= 4096) return 4096;
-  const int64_t chunk = cdiv(cdiv(P, 256), 1024) * 1024;
-  return chunk;
+  const int64_t share = P <= 4096 ? P : cdiv(P, 256);
+  return (share > 1024 ? cdiv(share, 1024) : 1) * 1024;
 }
 
 }  // namespace

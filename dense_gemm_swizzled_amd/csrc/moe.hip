@@ -267,6 +267,13 @@ __device__ __forceinline__ int choose(const RouteParams& p, int lane, const Key 
 // unit of the key.  If two keys whose order matters lie closer than twice that
 // -- four times for sums of two -- the wave decides again in 64 bits: with 256
 // experts about one token in a thousand does (sigmoid; softmax fewer).
+//
+// Bound by the instructions of the rounds (about 30 of a wave each), not by
+// the logits' bytes: 16384 tokens, top 8, softmax, us in a graph: 256 experts
+// fp32 13.4 (3.4 for the bytes), 128 bf16 8.2, 64 fp32 5.5, 16 bf16 4.5; with
+// sigmoid scores, a bias and groups 25, 18, 12, 10.  (Keys compared as floats,
+// every score divided and a wider bound of doubt: 16.6 and 30 for 256.)  Four
+// tokens of 256 experts with groups take 6.2, of which 3 are a launch.
 template <int DT, int Lanes, bool Scores>
 __global__ void __launch_bounds__(kBlockThreads) moe_route_kernel(const RouteParams p) {
   constexpr int kTokens = kBlockThreads / Lanes;
@@ -375,7 +382,9 @@ __device__ __forceinline__ void store_row4(const RouteParams& p, int64_t t, int 
 // Only ratios of scores appear, so small scores lose nothing.  Bound by
 // memory: the gradient's rows are written whole; softmax reads the logits'
 // rows, sigmoid only the chosen logits.  Lane j of a token's lanes handles its
-// j-th expert and puts the result into the token's row in LDS.
+// j-th expert and puts the result into the token's row in LDS.  16384 x 256
+// fp32, us in a graph: sigmoid 8.5, softmax 11.7 (the two rows' bytes 6.7);
+// every lane comparing every chosen id with its experts instead took 15.4.
 template <int DT, int Lanes>
 __global__ void __launch_bounds__(kBlockThreads) moe_route_backward_kernel(
     const RouteParams p) {
@@ -459,6 +468,11 @@ __global__ void __launch_bounds__(kBlockThreads) moe_route_backward_kernel(
 // of its waves a contiguous part of the chunk.  Lanes of a wave that hold the
 // same id find each other by one ballot per bit of the id, which gives their
 // order; no atomic decides a place, so the result is the same every time.
+//
+// Bound by latency: up to 4096 pairs one workgroup does all (1024 pairs 4.1 us,
+// 4096 7.3, of which 3 are a launch), beyond that a launch counts and a second
+// places, over at most 256 workgroups (8192 pairs 8.5, 131072 10.1; their
+// bytes alone 0.3).
 
 constexpr int kPlanThreads = 1024, kPlanWaves = kPlanThreads / 64;
 constexpr int kPlanBins = SG_MAX_GROUPS + 1;
