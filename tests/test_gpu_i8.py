@@ -56,7 +56,8 @@ SIZES = [
     (33, 130, 144, "stream"), (64, 513, 2064, "stream"), (65, 72, 272, "mid"),
     (100, 999, 128, "mid"), (300, 264, 208, "mid"), (129, 4097, 144, "mid"),
     (1000, 2050, 400, "mid"), (200, 264, 16, "mid"), (2000, 2304, 16, "pingpong"), (4096, 4096, 128, "pingpong"),
-    (4000, 4111, 192, "pingpong"), (4097, 4096, 256, "pingpong"), (8200, 2056, 80, "pingpong"),
+    (4000, 4111, 192, "pingpong"), (8200, 2056, 80, "pingpong"), (4097, 4096, 256, "pingpong"),
+    (4096, 4000, 384, "pingpong"), (5100, 4111, 640, "pingpong"), (9000, 5001, 256, "pingpong"),
 ]
 
 
@@ -96,7 +97,8 @@ GROUPED_KERNELS = [
     (3, 200, 528, 4, "i8_stream_kernel<16,16,%s>"), (9, 1000, 1040, 8, "i8_stream_kernel<16,32,%s>"),
     (40, 1000, 80, 5, "i8_stream_kernel<16,64,%s>"), (6, 300, 272, 40, "i8_mid_kernel<64,64,%s>"),
     (5, 2800, 1040, 60, "i8_mid_kernel<64,128,%s>"), (4, 2000, 1040, 300, "i8_mid_kernel<128,128,%s>"),
-    (32, 2048, 144, 30, "i8_pingpong_kernel<%s>"),
+    (32, 2048, 144, 30, "i8_pingpong_kernel<%s>"), (32, 2048, 256, 30, "i8_pingpong_kernel<%s>"),
+    (20, 2100, 384, 500, "i8_pingpong_kernel<%s>"), (3, 4111, 640, 2500, "i8_pingpong_kernel<%s>"),
 ]
 
 
@@ -135,7 +137,7 @@ def test_largest_sum_is_exact(M):
 
 
 @pytest.mark.parametrize("M,N,K", [(5, 50, 96), (50, 33, 160), (90, 75, 272), (300, 2001, 144),
-                                   (4096, 4100, 144)])
+                                   (4096, 4100, 144), (4200, 4100, 256)])
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_padded_rows_are_read_and_kept(M, N, K, dtype):
     """Rows of A, B and D inside wider buffers: the padding of A and B (127s)
@@ -230,12 +232,13 @@ def test_grouped_matches_the_dense_product_bit_for_bit():
             assert torch.equal(d[lo:hi], run(a[lo:hi], sa[lo:hi], b[g], sb[g]))
 
 
-@pytest.mark.parametrize("R", [6, 60, 600])
-def test_bad_offsets_stay_inside_d(R):
+@pytest.mark.parametrize("R,N,K,name", [(6, 48, 64, "stream"), (60, 48, 64, "mid"),
+                                        (600, 48, 64, "mid"), (9000, 2048, 256, "pingpong")])
+def test_bad_offsets_stay_inside_d(R, N, K, name):
     """The device clamps offsets: whatever they are, nothing outside D's rows
     is written."""
     rng = np.random.default_rng(R)
-    G, N, K = 4, 48, 64
+    G = 4
     a, b = codes(rng, R, K).cuda(), codes(rng, G, N, K).cuda()
     sa, sb = scales(rng, R).cuda(), scales(rng, G, N).cuda()
     top = 2 ** 31 - 1
@@ -245,6 +248,7 @@ def test_bad_offsets_stay_inside_d(R):
         sg.i8_grouped_gemm(a, sa, b, sb, torch.tensor(off, dtype=torch.int32).cuda(),
                            out=buf[1:R + 1])
         torch.cuda.synchronize()
+        assert name in sg.gemm_last_kernel()
         assert bool((buf[0] == 5.0).all()) and bool((buf[-1] == 5.0).all())
 
 
