@@ -69,12 +69,15 @@ __device__ __forceinline__ F sigmoid_of(F x) {
   return (x < 0 ? z : F(1)) / (F(1) + z);
 }
 
-template <int Lanes>
-__device__ __forceinline__ float row_top(const float (&x)[kHeld]) {
+__device__ __forceinline__ float lane_top(const float (&x)[kHeld]) {
   float m = x[0];
 #pragma unroll
   for (int i = 1; i < kHeld; ++i) m = OpMax{}(m, x[i]);
-  return lane_reduce<Lanes>(m, OpMax{});
+  return m;
+}
+template <int Lanes>
+__device__ __forceinline__ float row_top(const float (&x)[kHeld]) {
+  return lane_reduce<Lanes>(lane_top(x), OpMax{});
 }
 
 // The scores of a token's experts in type F, up to a common divisor, which is
@@ -382,37 +385,50 @@ __device__ __forceinline__ void store_row4(const RouteParams& p, int64_t t, int 
 // Only ratios of scores appear, so small scores lose nothing.  Bound by
 // memory: the gradient's rows are written whole; softmax reads the logits'
 // rows, sigmoid only the chosen logits.  Lane j of a token's lanes handles its
-// j-th expert and puts the result into the token's row in LDS.  16384 x 256
-// fp32, us in a graph: sigmoid 8.5, softmax 11.7 (the two rows' bytes 6.7);
-// every lane comparing every chosen id with its experts instead took 15.4.
-template <int DT, int Lanes>
+// j-th expert and puts the result into the token's row in LDS; quad q of the
+// lane holds experts from 4 * (q * Lanes + lane), so that a quad's loads and
+// stores of neighbouring lanes adjoin.  16384 x 256 fp32, us in a graph:
+// sigmoid 6.5, softmax 9.7 (the two rows' bytes 6.7); every lane comparing
+// every chosen id with its experts instead took 15.4 (with one quad).
+template <int DT, int Lanes, int Quads>
 __global__ void __launch_bounds__(kBlockThreads) moe_route_backward_kernel(
     const RouteParams p) {
   constexpr int kTokens = kBlockThreads / Lanes;
-  __shared__ __attribute__((aligned(16))) float rows[kTokens][Lanes * kHeld];
+  __shared__ __attribute__((aligned(16))) float rows[kTokens][Quads * Lanes * kHeld];
   __shared__ Chosen us_all[kTokens * SG_MAX_TOP_K];
   const int lane = threadIdx.x % Lanes, slot = threadIdx.x / Lanes;
   const int64_t t = block_index() * kTokens + slot;
   const bool live = t < p.T;
-  const int e0 = kHeld * lane;
+  auto first = [&](int q) { return kHeld * (q * Lanes + lane); };
   float* const row = rows[slot];
   Chosen* const us = us_all + slot * SG_MAX_TOP_K;
   const bool soft = p.score == SG_SCORE_SOFTMAX;
 
   // Softmax: the row's largest logit and sum of exponentials.
-  float x[kHeld], s[kHeld] = {}, top = 0.0f, total = 1.0f;
+  float s[Quads][kHeld] = {}, top = 0.0f, total = 1.0f;
   if (soft) {
-    load_row4<DT>(p, t, e0, live, x);
-    top = row_top<Lanes>(x);
+    top = -__builtin_inff();
+#pragma unroll
+    for (int q = 0; q < Quads; ++q) {
+      load_row4<DT>(p, t, first(q), live, s[q]);
+      top = OpMax{}(top, lane_top(s[q]));
+    }
+    top = lane_reduce<Lanes>(top, OpMax{});
     total = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-      s[i] = x[i] > -__builtin_inff() ? expf(x[i] - top) : 0.0f;
-      total += s[i];
+    for (int q = 0; q < Quads; ++q) {
+      float part = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) {
+        s[q][i] = s[q][i] > -__builtin_inff() ? expf(s[q][i] - top) : 0.0f;
+        part += s[q][i];
+      }
+      total += part;
     }
     total = __builtin_fmaxf(lane_reduce<Lanes>(total, OpSum{}), kTiny);
   }
-  *reinterpret_cast<f32x4*>(row + e0) = f32x4{};
+#pragma unroll
+  for (int q = 0; q < Quads; ++q) *reinterpret_cast<f32x4*>(row + first(q)) = f32x4{};
 
   // The chosen experts' scores, then their sum and mean gradient.
   float sum = 0.0f;
@@ -452,13 +468,18 @@ __global__ void __launch_bounds__(kBlockThreads) moe_route_backward_kernel(
     if ((uint32_t)id < (uint32_t)p.E) row[id] = u;
   }
   wave_sync();
-  if (!live || e0 >= p.E) return;
-  f32x4 d = *reinterpret_cast<const f32x4*>(row + e0);
+  if (!live) return;
   const float all = p.renorm && !floor ? 0.0f : dot / total;
-  if (soft)
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) d[i] -= s[i] * all;
-  store_row4<DT>(p, t, e0, d);
+  for (int q = 0; q < Quads; ++q) {
+    const int e0 = first(q);
+    if (e0 >= p.E) return;
+    f32x4 d = *reinterpret_cast<const f32x4*>(row + e0);
+    if (soft)
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) d[i] -= s[q][i] * all;
+    store_row4<DT>(p, t, e0, d);
+  }
 }
 
 // ------------------------------------------------------------------ the plan
@@ -605,42 +626,90 @@ constexpr const char* dt_label(int dt) {
   return dt == SG_F32 ? "f32" : dt == SG_BF16 ? "bf16" : "f16";
 }
 
-template <int DT, int Lanes, bool Back>
+dim3 route_grid(int64_t T, int lanes) {
+  const int tokens = kBlockThreads / lanes;
+  return grid_of((T + tokens - 1) / tokens);
+}
+constexpr const char* digits(int n) {
+  return n == 1    ? "1"
+         : n == 2  ? "2"
+         : n == 4  ? "4"
+         : n == 8  ? "8"
+         : n == 16 ? "16"
+         : n == 32 ? "32"
+                   : "64";
+}
+
+template <int DT, int Lanes>
 hipError_t go_route(const RouteParams& p, hipStream_t s) {
-  constexpr int kTokens = kBlockThreads / Lanes;
-  const dim3 grid = grid_of((p.T + kTokens - 1) / kTokens);
-  constexpr const char* kL = Lanes == 8 ? "8" : Lanes == 16 ? "16" : Lanes == 32 ? "32" : "64";
-  if constexpr (Back) {
-    static const char* const name = kernel_label("moe_route_backward_kernel", dt_label(DT), kL);
-    last_kernel() = name;
-    hipLaunchKernelGGL((moe_route_backward_kernel<DT, Lanes>), grid, dim3(kBlockThreads), 0, s, p);
-  } else {
-    static const char* const names[2] = {
-        kernel_label("moe_route_kernel", dt_label(DT), kL, "logits"),
-        kernel_label("moe_route_kernel", dt_label(DT), kL, "scores")};
-    last_kernel() = names[p.by_score ? 1 : 0];
-    if (p.by_score)
-      hipLaunchKernelGGL((moe_route_kernel<DT, Lanes, true>), grid, dim3(kBlockThreads), 0, s, p);
-    else
-      hipLaunchKernelGGL((moe_route_kernel<DT, Lanes, false>), grid, dim3(kBlockThreads), 0, s, p);
-  }
+  static const char* const names[2] = {
+      kernel_label("moe_route_kernel", dt_label(DT), digits(Lanes), "logits"),
+      kernel_label("moe_route_kernel", dt_label(DT), digits(Lanes), "scores")};
+  last_kernel() = names[p.by_score ? 1 : 0];
+  const dim3 grid = route_grid(p.T, Lanes);
+  if (p.by_score)
+    hipLaunchKernelGGL((moe_route_kernel<DT, Lanes, true>), grid, dim3(kBlockThreads), 0, s, p);
+  else
+    hipLaunchKernelGGL((moe_route_kernel<DT, Lanes, false>), grid, dim3(kBlockThreads), 0, s, p);
   return hipGetLastError();
 }
 
-// The fewest lanes that hold a token's experts, four to a lane.
-template <int DT, bool Back>
-hipError_t by_experts(const RouteParams& p, hipStream_t s) {
-  if (p.E <= 32) return go_route<DT, 8, Back>(p, s);
-  if (p.E <= 64) return go_route<DT, 16, Back>(p, s);
-  if (p.E <= 128) return go_route<DT, 32, Back>(p, s);
-  return go_route<DT, 64, Back>(p, s);
+template <int DT, int Lanes, int Quads>
+hipError_t go_back(const RouteParams& p, hipStream_t s) {
+  static const char* const name =
+      kernel_label("moe_route_backward_kernel", dt_label(DT), digits(Lanes), digits(Quads));
+  last_kernel() = name;
+  hipLaunchKernelGGL((moe_route_backward_kernel<DT, Lanes, Quads>), route_grid(p.T, Lanes),
+                     dim3(kBlockThreads), 0, s, p);
+  return hipGetLastError();
+}
+
+// The fewest lanes that hold a token's experts, four to a lane.  Eight a lane
+// made the choice slower at every size: 4 tokens of 256 experts 4.0 -> 5.4 us,
+// 16384 of 128 8.2 -> 9.5 us, a round having more to look at in one chain.
+template <int DT>
+hipError_t forward(const RouteParams& p, hipStream_t s) {
+  if (p.E <= 32) return go_route<DT, 8>(p, s);
+  if (p.E <= 64) return go_route<DT, 16>(p, s);
+  if (p.E <= 128) return go_route<DT, 32>(p, s);
+  return go_route<DT, 64>(p, s);
+}
+
+// The gradient takes one quad of experts a lane while its waves fit the card
+// about at once, then fewer lanes with two or four, so that the short steps
+// over the choice serve more tokens of a wave.  Microseconds with 1 | 2 | 4
+// quads: 512 tokens of 256 fp32 softmax 4.0 | 4.3 | 5.0, 4096 5.3 | 5.0 | 5.5,
+// 16384 12.3 | 10.1 | 9.7, sigmoid 9.1 | 7.2 | 6.5; 16384 of 128 bf16 softmax
+// 6.8 | 5.7 | 5.9, 65536 19.4 | 14.2 | 12.9.
+template <int DT>
+hipError_t backward(const RouteParams& p, hipStream_t s) {
+  if (p.E <= 32) return go_back<DT, 8, 1>(p, s);
+  const int lanes = p.E <= 64 ? 16 : p.E <= 128 ? 32 : 64;
+  const int64_t threads = p.T * lanes;
+  if (threads < 1 << 18) {
+    if (p.E <= 64) return go_back<DT, 16, 1>(p, s);
+    if (p.E <= 128) return go_back<DT, 32, 1>(p, s);
+    return go_back<DT, 64, 1>(p, s);
+  }
+  if (p.E <= 64) return go_back<DT, 8, 2>(p, s);
+  if (threads < 1 << 20)
+    return p.E <= 128 ? go_back<DT, 16, 2>(p, s) : go_back<DT, 32, 2>(p, s);
+  return p.E <= 128 ? go_back<DT, 8, 4>(p, s) : go_back<DT, 16, 4>(p, s);
+}
+
+template <bool Back, int DT>
+hipError_t either(const RouteParams& p, hipStream_t s) {
+  if constexpr (Back)
+    return backward<DT>(p, s);
+  else
+    return forward<DT>(p, s);
 }
 
 template <bool Back>
 hipError_t by_type(int dtype, const RouteParams& p, hipStream_t s) {
-  if (dtype == SG_F32) return by_experts<SG_F32, Back>(p, s);
-  if (dtype == SG_BF16) return by_experts<SG_BF16, Back>(p, s);
-  return by_experts<SG_F16, Back>(p, s);
+  if (dtype == SG_F32) return either<Back, SG_F32>(p, s);
+  if (dtype == SG_BF16) return either<Back, SG_BF16>(p, s);
+  return either<Back, SG_F16>(p, s);
 }
 
 }  // namespace

@@ -301,6 +301,43 @@ def test_route_backward_strided():
     assert bool((buf == 5.0).all())
 
 
+# Every split of a token's experts over lanes, on both sides of each change,
+# with a last block that is part full and experts that are not whole quads.
+# The sums of a row's scores take 10 roundings in every split (3 in a quad, the
+# quads, the lanes), as the bound of check_grad counts.
+@pytest.mark.parametrize("T,E,k,split", [
+    (16383, 61, 4, "16,1"), (16389, 64, 4, "8,2"), (8191, 128, 8, "32,1"),
+    (8197, 125, 8, "16,2"), (32767, 66, 3, "16,2"), (32773, 101, 8, "8,4"),
+    (32771, 128, 32, "8,4"), (4095, 256, 8, "64,1"), (4097, 250, 8, "32,2"),
+    (16383, 131, 2, "32,2"), (16387, 256, 8, "16,4"), (16385, 139, 19, "16,4"),
+    (40001, 32, 6, "8,1")])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_backward_of_many_tokens(T, E, k, split, score):
+    rng = np.random.default_rng(T + E)
+    dtype = DTYPES[(T + E) % 3]
+    x = logits(rng, T, E, dtype, 1.5)
+    x[5] = -math.inf
+    x[T - 1, 1:] = -math.inf
+    x[::7, E - 1] = math.nan
+    _, ids = sg.moe_route(x.cuda(), k, score=score)
+    ids = ids.cpu()
+    ids[3, :2] = E - 2                                # one expert twice
+    ids[9, 0], ids[10, 1] = E, -2 ** 31               # outside the experts
+    g = torch.from_numpy(rng.standard_normal((T, k)).astype(np.float32))
+    for renorm in (True, False):
+        dx, _ = check_grad(x, ids, g, dtype, score=score, renorm=renorm, scale=1.5)
+        assert sg.gemm_last_kernel().endswith(split + ">"), sg.gemm_last_kernel()
+        assert bool((dx[5] == 0).all()) and bool(torch.isfinite(dx).all())
+    # strided rows that no vector fits, with what lies between them kept
+    wide = torch.full((T, E + 3), 7.0, dtype=dtype, device="cuda")
+    odd = torch.zeros(T, E + 1, dtype=dtype, device="cuda")
+    odd[:, 1:] = x.cuda()
+    sg.moe_route_backward(g.cuda(), odd[:, 1:], ids.cuda(), score=score, renorm=False, scale=1.5,
+                          out=wide[:, 1:E + 1])
+    assert torch.equal(wide[:, 1:E + 1], dx)
+    assert bool((wide[:, 0] == 7).all()) and bool((wide[:, E + 1:] == 7).all())
+
+
 def test_no_tokens():
     x = torch.zeros(0, 8, device="cuda")
     w, ids = sg.moe_route(x, 2)
