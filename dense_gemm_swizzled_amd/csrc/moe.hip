@@ -15,7 +15,7 @@ namespace sg {
 
 namespace {
 
-constexpr int kHeld = 4;             // experts a lane holds: 4 * lane .. 4 * lane + 3
+constexpr int kHeld = 4;             // experts of a quad: a lane holds one, or more in the gradient
 constexpr float kTiny = 0x1p-126f;   // smallest sum that weights are divided by
 constexpr int kBlockThreads = 256;
 
@@ -388,7 +388,7 @@ __device__ __forceinline__ void store_row4(const RouteParams& p, int64_t t, int 
 // j-th expert and puts the result into the token's row in LDS; quad q of the
 // lane holds experts from 4 * (q * Lanes + lane), so that a quad's loads and
 // stores of neighbouring lanes adjoin.  16384 x 256 fp32, us in a graph:
-// sigmoid 6.5, softmax 9.7 (the two rows' bytes 6.7); every lane comparing
+// sigmoid 6.5, softmax 9.7 (both rows' bytes 6.7, one's written 3.4); every lane comparing
 // every chosen id with its experts instead took 15.4 (with one quad).
 template <int DT, int Lanes, int Quads>
 __global__ void __launch_bounds__(kBlockThreads) moe_route_backward_kernel(
