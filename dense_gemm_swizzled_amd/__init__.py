@@ -714,9 +714,10 @@ def mxfp6_gemm(A, SFA, B, SFB, *, fmt: str = "e2m3", out_dtype=None, out=None):
 # Small calls of these take less time on the GPU than a wrapper of the kind
 # above takes to check them (13 to 19 us), so the checks build their messages
 # only when they fail and the C functions are called directly (6 to 8 us a
-# call, 4 of them the launch itself).  The launches go to the tensors' device even when another is current.
-# Results carry no autograd history: moe_route_backward is a call of its own,
-# and the 8-bit products are for serving.
+# call, 4 of them the launch itself).  The launches go to the tensors' device
+# even when another is current.  Results carry no autograd history:
+# moe_route_backward is a call of its own, and the 8-bit products are for
+# serving.
 
 _torch = None
 _raw_stream = _current_device = None
@@ -748,6 +749,14 @@ def _launch(f, device, *args) -> None:
 
 def _fail(code: int, msg: str):
     raise GemmError(code, msg)
+
+
+def _int(name: str, v) -> int:
+    """v as an int that a C int holds."""
+    v = int(v)
+    if not -0x80000000 <= v <= 0x7fffffff:
+        _fail(-3, f"{name}={v} is outside 32 bits")
+    return v
 
 
 def _on_one_device(first, *others) -> None:
@@ -888,6 +897,7 @@ def i8_grouped_gemm(A, SA, B, SB, offsets, *, rows=None, out_dtype=None, out=Non
     if B.dim() != 3:
         _fail(-3, f"B must be [G][N][K], got shape {tuple(B.shape)}")
     G, N, Kb = B.shape
+    _int("G", G)
     _packed("B", B, B.shape, T.int8)
     if Kb != K:
         _fail(-3, f"A and B disagree on K ({K} vs {Kb})")
@@ -936,8 +946,9 @@ def moe_route(logits, top_k: int, *, score: str = "softmax", bias=None, n_groups
     ldl = _pitch("logits", logits)
     n, E = logits.shape
     dt, code = _float_code("logits", logits.dtype), _score_code(score)
-    top_k, n_groups = int(top_k), int(n_groups)
-    top_groups = n_groups if top_groups is None else int(top_groups)
+    _int("E", E)
+    top_k, n_groups = int(top_k), _int("n_groups", n_groups)
+    top_groups = n_groups if top_groups is None else _int("top_groups", top_groups)
     groups = _GROUP_SCORES.get(group_score)
     if groups is None:
         _fail(-6, f"group_score must be one of {sorted(_GROUP_SCORES)}, got {group_score!r}")
@@ -970,7 +981,8 @@ def moe_route_backward(dweights, logits, ids, *, score: str = "softmax", renorm:
     dt, code = _float_code("logits", logits.dtype), _score_code(score)
     if ids.dim() != 2:
         _fail(-3, f"ids must be 2-D, got shape {tuple(ids.shape)}")
-    top_k = ids.shape[1]
+    _int("E", E)
+    top_k = _int("top_k", ids.shape[1])
     _packed("ids", ids, (n, top_k), T.int32)
     _packed("dweights", dweights, (n, top_k), T.float32)
     lddl = E
@@ -1005,7 +1017,8 @@ def moe_plan(ids, n_experts: int, *, out=None, workspace=None):
         _fail(-3, f"ids must be 2-D, got shape {tuple(ids.shape)}")
     n, top_k = ids.shape
     _packed("ids", ids, (n, top_k), T.int32)
-    P, n_experts = n * top_k, int(n_experts)
+    _int("top_k", top_k)
+    P, n_experts = n * top_k, _int("n_experts", n_experts)
     need = lib.moe_plan_workspace_bytes(P, n_experts)
     if need < 0:
         _fail(need, gemm_last_error())

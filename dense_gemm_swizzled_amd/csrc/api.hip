@@ -599,8 +599,9 @@ int i8_run(const char* who, int G, int64_t M, int64_t N, int64_t K, const int32_
   if (lda < K || ldb < K || ldd < N)
     return fail(SG_ERR_SHAPE, "%s: a leading dimension is below its minimum (lda %lld, ldb %lld, "
                               "ldd %lld)", who, (long long)lda, (long long)ldb, (long long)ldd);
-  if (M >= kMaxExtent || N >= kMaxExtent || a_rows >= kMaxExtent)
-    return fail(SG_ERR_SHAPE, "%s: 2^31 rows or columns or more", who);
+  if (M >= kMaxExtent || N >= kMaxExtent || a_rows >= kMaxExtent || lda >= kMaxExtent ||
+      ldb >= kMaxExtent)
+    return fail(SG_ERR_SHAPE, "%s: 2^31 rows or columns or more, or such a pitch", who);
   if (M == 0 || N == 0) return ok();
   if (!D || (G > 0 && !offsets)) return fail(SG_ERR_NULL, "%s: D or offsets is NULL", who);
   const bool no_a = rows && a_rows == 0;  // no index names a row

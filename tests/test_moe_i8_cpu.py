@@ -249,3 +249,27 @@ def test_moe_plan_checks():
     big = i32(5000, 2)
     assert _code(sg.moe_plan, big, 8, workspace=torch.zeros(8, dtype=torch.uint8)) == SHAPE
     assert _code(sg.moe_plan, big, 8, workspace=torch.zeros(1 << 16)) == DTYPE
+
+
+# Sizes that a C int or a byte offset does not hold are refused, not wrapped.
+@pytest.mark.parametrize("ld", [1 << 31, 1 << 56, 1 << 57, 1 << 62])
+def test_pitches_that_overflow(ld):
+    assert _gemm(lda=ld) == SHAPE
+    assert _gemm(ldb=ld) == SHAPE
+    assert _gemm(M=4097, lda=ld) == SHAPE
+    assert _grouped(lda=ld) == SHAPE
+    assert _grouped(lda=ld, rows=None) == SHAPE
+
+
+def test_sizes_beyond_32_bits():
+    wide, x, ids = (1 << 32) + 8, torch.zeros(6, 16), i32(6, 2)
+    assert _code(sg.moe_plan, ids, wide) == SHAPE
+    assert _code(sg.moe_plan, i32(0, wide), 8) == SHAPE
+    assert _code(sg.moe_route, torch.zeros(0, wide), 2) == SHAPE
+    assert _code(sg.moe_route, x, 2, n_groups=wide) == SHAPE
+    assert _code(sg.moe_route, x, 2, n_groups=8, top_groups=wide) == SHAPE
+    assert _code(sg.moe_route_backward, torch.zeros(0, 2), torch.zeros(0, wide), i32(0, 2)) == SHAPE
+    assert _code(sg.moe_route_backward, torch.zeros(0, wide), torch.zeros(0, 16),
+                 i32(0, wide)) == SHAPE
+    assert _code(sg.i8_grouped_gemm, i8(8, 16), torch.ones(8), i8(wide, 0, 16),
+                 torch.zeros(wide, 0), i32(9)) == SHAPE
