@@ -679,12 +679,22 @@ bool rows_of_four(const void* p, int64_t ld, int dtype) {
   return ld % 4 == 0 && reinterpret_cast<uintptr_t>(p) % (4 * elem_bytes(dtype)) == 0;
 }
 
+// Up to so many pairs the plan is one launch (us, one launch / two, 256
+// experts: 8192 pairs 5.6 / 7.0, 16384 7.2 / 7.2, 32768 10.2 / 7.3).
+constexpr int64_t kPlanAlone = 16384;
+
 // Pairs that a workgroup of the plan sorts, a multiple of 64 for each of its 16
-// waves: all of them up to 4096, in one launch (us, one launch / two: 4096
-// pairs 7.3 / 8.1, 8192 12.0 / 8.5), else shared by at most 256 workgroups.
-int64_t plan_chunk(int64_t P) {
-  const int64_t share = P <= 4096 ? P : cdiv(P, 256);
-  return (share > 1024 ? cdiv(share, 1024) : 1) * 1024;
+// waves.  Every workgroup reads the n workgroups' counts of E experts, n * E
+// in all, and places P / n pairs, about 8 / n of the time a count takes for
+// each: fewer workgroups the more experts (256 experts, us, this / 1024 pairs
+// a workgroup up to 256 of them: 131072 pairs 9.2 / 10.3, 524288 13.9 / 16.2).
+int64_t plan_chunk(int64_t P, int E) {
+  int64_t chunk = 1024;
+  if (P <= kPlanAlone) return chunk;
+  for (;; chunk *= 2) {
+    const int64_t n = cdiv(P, chunk);
+    if (n <= 256 && n * n * E <= 8 * P) return chunk;
+  }
 }
 
 }  // namespace
@@ -808,8 +818,7 @@ int moe_route_backward_run(int64_t T, int E, int top_k, const float* dweights, c
 int64_t moe_plan_workspace_bytes(int64_t P, int E) {
   if (P < 0 || P >= kMaxExtent || E < 1 || E > SG_MAX_GROUPS)
     return fail(SG_ERR_SHAPE, "moe_plan_workspace_bytes: P=%lld E=%d", (long long)P, E);
-  const int64_t blocks = cdiv(P, plan_chunk(P));
-  return blocks <= 1 ? 0 : blocks * (E + 1) * 4;
+  return P <= kPlanAlone ? 0 : cdiv(P, plan_chunk(P, E)) * E * 4;
 }
 
 int moe_plan_run(int64_t T, int E, int top_k, const int32_t* ids, int32_t* offsets, int32_t* rows,
@@ -834,12 +843,14 @@ int moe_plan_run(int64_t T, int E, int top_k, const int32_t* ids, int32_t* offse
   p.P = P;
   p.E = E;
   p.top_k = top_k;
-  p.chunk = plan_chunk(P);
+  p.chunk = plan_chunk(P, E);
   p.ids = ids;
   p.offsets = offsets;
   p.rows = rows;
   p.slots = slots;
-  p.counts = static_cast<int32_t*>(workspace);
+  p.counts = need > 0 ? static_cast<int32_t*>(workspace) : nullptr;
+  p.div_shift = top_k > 1 ? 32 - __builtin_clz(top_k - 1) : 0;
+  p.div_mul = (uint32_t)(((1ull << 32) * ((1ull << p.div_shift) - top_k)) / top_k + 1);
   hipError_t e = sg::launch_moe_plan(p, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail(e, who);
   return ok();

@@ -33,7 +33,9 @@ struct PlanParams {
   int32_t* offsets;         // [E + 1]
   int32_t* rows;            // [P]
   int32_t* slots;           // [P]
-  int32_t* counts;          // workspace: [workgroups][E + 1], with more than one
+  int32_t* counts;          // workspace: [workgroups][E], or null for one launch
+  uint32_t div_mul;         // of a division by top_k
+  int div_shift;
 };
 
 }  // namespace sg

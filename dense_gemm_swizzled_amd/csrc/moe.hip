@@ -484,19 +484,23 @@ __global__ void __launch_bounds__(kBlockThreads) moe_route_backward_kernel(
 
 // ------------------------------------------------------------------ the plan
 //
-// A stable counting sort of P = T * top_k ids: bucket of an id outside [0, E)
-// is E, behind all experts.  Each block owns a contiguous chunk of pairs, each
-// of its waves a contiguous part of the chunk.  Lanes of a wave that hold the
-// same id find each other by one ballot per bit of the id, which gives their
-// order; no atomic decides a place, so the result is the same every time.
+// A stable counting sort of the P = T * top_k ids in [0, E); the others have
+// no place.  Each block owns a contiguous chunk of pairs, each of its waves a
+// contiguous part of the chunk.  A pair's place is the count of smaller ids,
+// of its id in earlier blocks, in earlier waves and in earlier lanes.  Lanes
+// of a wave that hold the same id find each other by one ballot per bit of the
+// id, which gives their order; no atomic decides a place, so the result is the
+// same every time.
 //
-// Bound by latency: up to 4096 pairs one workgroup does all (1024 pairs 4.1 us,
-// 4096 7.3, of which 3 are a launch), beyond that a launch counts and a second
-// places, over at most 256 workgroups (8192 pairs 8.5, 131072 10.1; their
-// bytes alone 0.3).
+// The ballots make a step of 64 pairs about 100 instructions of a wave, so
+// that many workgroups share them; counting takes a tenth.  Up to 16384 pairs
+// each workgroup counts all ids by itself, beyond that a launch before counts
+// them by chunks.  us in a graph, 8 | 256 experts, of which 3 are a launch:
+// 256 pairs 3.1 | 3.3, 4096 4.3 | 4.8, 16384 6.6 | 7.2, 131072 6.8 | 9.2 (the
+// pairs' bytes 0.3).  One workgroup for all 4096 took 6.0 | 7.3.
 
 constexpr int kPlanThreads = 1024, kPlanWaves = kPlanThreads / 64;
-constexpr int kPlanBins = SG_MAX_GROUPS + 1;
+static_assert(SG_MAX_GROUPS == 256, "four experts a lane");
 
 // The lanes of the wave that hold the same key (0 .. 2^bits - 1).
 __device__ __forceinline__ uint64_t same_key(int key, int bits) {
@@ -510,75 +514,107 @@ __device__ __forceinline__ uint64_t same_key(int key, int bits) {
 }
 
 __global__ void __launch_bounds__(kPlanThreads) moe_plan_count_kernel(const PlanParams p) {
-  __shared__ int bins[kPlanBins];
-  const int n = p.E + 1;
-  for (int e = threadIdx.x; e < n; e += kPlanThreads) bins[e] = 0;
+  __shared__ int bins[SG_MAX_GROUPS];
+  if (threadIdx.x < SG_MAX_GROUPS) bins[threadIdx.x] = 0;
   __syncthreads();
   const int64_t c0 = (int64_t)blockIdx.x * p.chunk;
   const int64_t c1 = c0 + p.chunk < p.P ? c0 + p.chunk : p.P;
   for (int64_t i = c0 + threadIdx.x; i < c1; i += kPlanThreads) {
     const int id = p.ids[i];
-    atomicAdd(&bins[(uint32_t)id < (uint32_t)p.E ? id : p.E], 1);  // counts: any order
+    if ((uint32_t)id < (uint32_t)p.E) atomicAdd(&bins[id], 1);  // counts: any order
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < n; e += kPlanThreads)
-    p.counts[(int64_t)blockIdx.x * n + e] = bins[e];
+  if ((int)threadIdx.x < p.E) p.counts[(int64_t)blockIdx.x * p.E + threadIdx.x] = bins[threadIdx.x];
 }
 
-// Multi: the chunks' counts are in p.counts; else this block owns all pairs.
-template <bool Multi>
+// Counted: the chunks' counts are in p.counts; else a chunk is kPlanThreads
+// pairs and the block counts the others' ids itself.
+template <bool Counted>
 __global__ void __launch_bounds__(kPlanThreads) moe_plan_place_kernel(const PlanParams p) {
-  __shared__ int bins[kPlanWaves][kPlanBins];  // first counts, then next places
-  __shared__ int start[kPlanBins];
+  // One counter of an expert for each eighth lane, so that ids that are all
+  // the same do not take 64 turns (8192 pairs of one expert 10.3 us with one).
+  constexpr int kCopies = Counted ? 1 : 8;
+  __shared__ int bins[kPlanWaves][SG_MAX_GROUPS];  // first counts, then next places
+  __shared__ int earlier[SG_MAX_GROUPS][kCopies], others[SG_MAX_GROUPS][kCopies];
   __shared__ int wave_sum[kPlanWaves];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int n = p.E + 1, bits = 32 - __builtin_clz(p.E);
-  for (int e = tid; e < kPlanWaves * kPlanBins; e += kPlanThreads) (&bins[0][0])[e] = 0;
-  __syncthreads();
+  const int bits = 32 - __builtin_clz(2 * p.E - 1) - 1;  // of E - 1, none for one expert
 
-  const int64_t c0 = (int64_t)blockIdx.x * p.chunk;
-  const int64_t c1 = c0 + p.chunk < p.P ? c0 + p.chunk : p.P;
-  const int64_t per = ((p.chunk + kPlanWaves - 1) / kPlanWaves + 63) / 64 * 64;
-  const int64_t w0 = c0 + wave * per, w1 = w0 + per < c1 ? w0 + per : c1;
-  auto bucket = [&](int64_t i) {
-    if (i >= w1) return -1;
-    const int id = p.ids[i];
-    return (uint32_t)id < (uint32_t)p.E ? id : p.E;
+  // Pairs, and sums of a chunk and its start, are below 2^32.
+  const uint32_t P = (uint32_t)p.P, chunk = (uint32_t)p.chunk;
+  const uint32_t block = blockIdx.x, blocks = gridDim.x;
+  const uint32_t c0 = block * chunk, c1 = c0 + chunk < P ? c0 + chunk : P;
+  const uint32_t per = chunk / kPlanWaves;  // a multiple of 64
+  const uint32_t w0 = c0 + wave * per, w1 = w0 + per < c1 ? w0 + per : c1;
+  auto id_at = [&](uint32_t i, uint32_t end) {
+    const int id = i < end ? p.ids[i] : -1;
+    return (uint32_t)id < (uint32_t)p.E ? id : -1;
   };
-  for (int64_t b = w0; b < w1; b += 64) {
-    const int key = bucket(b + lane);
-    if (key >= 0) atomicAdd(&bins[wave][key], 1);
+  int next = id_at(w0 + lane, w1);
+  for (int e = tid; e < kPlanWaves * SG_MAX_GROUPS; e += kPlanThreads) (&bins[0][0])[e] = 0;
+  if (blocks > 1)
+    for (int e = tid; e < SG_MAX_GROUPS * kCopies; e += kPlanThreads)
+      (&earlier[0][0])[e] = (&others[0][0])[e] = 0;
+  __syncthreads();
+  // The wave's own counts: the last lane of an id knows the first step's.
+  uint64_t same = 0;
+  if (w0 < w1) same = same_key(next, bits) & __ballot(next >= 0);
+  if (next >= 0 && (same >> lane) == 1) bins[wave][next] = __builtin_popcountll(same);
+  wave_sync();
+  for (uint32_t b = w0 + 64; b < w1; b += 64) {
+    const int id = id_at(b + lane, w1);
+    if (id >= 0) atomicAdd(&bins[wave][id], 1);
+  }
+  // The other blocks' counts of each expert, and the earlier ones' among them.
+  if constexpr (Counted) {
+    // 2^bits threads a chunk's row, eight chunks' loads in flight.
+    const int e = tid & ((1 << bits) - 1);
+    const uint32_t step = kPlanThreads >> bits;
+    int sum = 0, first = 0;
+    for (uint32_t b0 = tid >> bits; b0 < blocks; b0 += 8 * step) {
+      int v[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const uint32_t b = b0 + q * step;
+        v[q] = p.counts[(b < blocks ? b : block) * (uint32_t)p.E + (e < p.E ? e : 0)];
+      }
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const uint32_t b = b0 + q * step;
+        sum += b < blocks && b != block ? v[q] : 0;
+        first += b < block ? v[q] : 0;
+      }
+    }
+    if (e < p.E) {
+      atomicAdd(&others[e][0], sum);
+      atomicAdd(&earlier[e][0], first);
+    }
+  } else {
+    // Here `others` has the later blocks' alone until the sums below.
+#pragma unroll 4
+    for (uint32_t b = 0; b < blocks; ++b) {
+      const int id = b == block ? -1 : id_at(b * kPlanThreads + tid, P);
+      if (id >= 0) atomicAdd(&(b < block ? earlier : others)[id][tid % kCopies], 1);
+    }
   }
   __syncthreads();
 
-  // Totals of the buckets, and how many of each come before this block: the
-  // waves share the blocks' counts, lane l taking buckets l, l + 64 ... (one
-  // thread a bucket going through 128 blocks took 25 us of latency).
+  // Expert tid's pairs: in all, and before this block; then the exclusive scan
+  // over the experts (the first four waves).
   int total = 0, before = 0;
-  if constexpr (Multi) {
-    __shared__ int sums[kPlanWaves][kPlanBins], firsts[kPlanWaves][kPlanBins];
-    for (int e = lane; e < n; e += 64) {
-      int sum = 0, first = 0;
-#pragma unroll 8
-      for (int b = wave; b < (int)gridDim.x; b += kPlanWaves) {
-        const int v = p.counts[(int64_t)b * n + e];
-        sum += v;
-        first += b < (int)blockIdx.x ? v : 0;
+  if (tid < SG_MAX_GROUPS) {
+    if (blocks > 1) {
+#pragma unroll
+      for (int c = 0; c < kCopies; ++c) {
+        total += others[tid][c];
+        before += earlier[tid][c];
       }
-      sums[wave][e] = sum;
-      firsts[wave][e] = first;
+      if (!Counted) total += before;
     }
-    __syncthreads();
-    if (tid < n)
-      for (int w = 0; w < kPlanWaves; ++w) {
-        total += sums[w][tid];
-        before += firsts[w][tid];
-      }
-  } else if (tid < n) {
+#pragma unroll
     for (int w = 0; w < kPlanWaves; ++w) total += bins[w][tid];
   }
-  // Exclusive scan of the totals (the first n <= 257 threads: waves 0 .. 4).
   int upto = total;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
@@ -587,16 +623,17 @@ __global__ void __launch_bounds__(kPlanThreads) moe_plan_place_kernel(const Plan
   }
   if (lane == 63) wave_sum[wave] = upto;
   __syncthreads();
-  if (tid < n) {
-    int first = upto - total;
-    for (int w = 0; w < wave; ++w) first += wave_sum[w];
-    if (blockIdx.x == 0) p.offsets[tid] = first;  // n = E + 1 entries
-    start[tid] = first + before;
-  }
-  __syncthreads();
-  if (tid < n) {  // counts of the waves become their first places
-    int at = start[tid];
-    for (int w = 0; w < kPlanWaves; ++w) {
+  const int last = wave_sum[0] + wave_sum[1] + wave_sum[2] + wave_sum[3];  // offsets[E]
+  if (tid < SG_MAX_GROUPS) {
+    int at = upto - total;
+    for (int w = 0; w < wave; ++w) at += wave_sum[w];
+    if (block == 0) {
+      if (tid < p.E) p.offsets[tid] = at;
+      if (tid == 0) p.offsets[p.E] = last;
+    }
+    at += before;
+#pragma unroll
+    for (int w = 0; w < kPlanWaves; ++w) {  // counts of the waves become their first places
       const int c = bins[w][tid];
       bins[w][tid] = at;
       at += c;
@@ -604,20 +641,25 @@ __global__ void __launch_bounds__(kPlanThreads) moe_plan_place_kernel(const Plan
   }
   __syncthreads();
 
-  for (int64_t b = w0; b < w1; b += 64) {
-    const int64_t i = b + lane;
-    const int key = bucket(i);
-    const bool in = key >= 0;
-    const uint64_t same = same_key(in ? key : 0, bits) & __ballot(in);
+  for (uint32_t b = w0; b < w1; b += 64) {
+    const uint32_t i = b + lane;
+    const int id = next;
+    const bool in = id >= 0;
+    if (b > w0) same = same_key(id, bits) & __ballot(in);
+    next = id_at(i + 64, w1);
     if (in) {
-      const int before_me = __builtin_popcountll(same & ((1ull << lane) - 1));
-      const int place = bins[wave][key] + before_me;
-      p.slots[i] = key < p.E ? place : -1;
-      if (place < p.P) p.rows[place] = key < p.E ? (int)(i / p.top_k) : -1;
+      const int place = bins[wave][id] + __builtin_popcountll(same & ((1ull << lane) - 1));
+      // t = i / top_k, i below 2^31 (the multiplier is 2^32 (2^shift - top_k) / top_k + 1)
+      const uint32_t t = (__umulhi(p.div_mul, i) + i) >> p.div_shift;
+      p.slots[i] = place;
+      if ((uint32_t)place < P) p.rows[place] = (int)t;
+    } else if (i < w1) {
+      p.slots[i] = -1;
     }
+    if (i < w1 && i >= (uint32_t)last) p.rows[i] = -1;
     wave_sync();
     if (in && (same >> lane) == 1)  // the last lane of its id moves the place on
-      bins[wave][key] += __builtin_popcountll(same);
+      bins[wave][id] += __builtin_popcountll(same);
     wave_sync();
   }
 }
@@ -723,12 +765,12 @@ hipError_t launch_moe_route_backward(int dtype, const RouteParams& p, hipStream_
 }
 
 hipError_t launch_moe_plan(const PlanParams& p, hipStream_t s) {
-  static const char* const names[2] = {kernel_label("moe_plan_place_kernel", "single"),
-                                       kernel_label("moe_plan_place_kernel", "multi")};
-  const int blocks = (int)((p.P + p.chunk - 1) / p.chunk);
-  last_kernel() = names[blocks > 1 ? 1 : 0];
-  if (blocks <= 1) {
-    hipLaunchKernelGGL((moe_plan_place_kernel<false>), dim3(1), dim3(kPlanThreads), 0, s, p);
+  static const char* const names[2] = {kernel_label("moe_plan_place_kernel", "alone"),
+                                       kernel_label("moe_plan_place_kernel", "counted")};
+  const int blocks = (int)(p.P > 0 ? (p.P + p.chunk - 1) / p.chunk : 1);
+  last_kernel() = names[p.counts ? 1 : 0];
+  if (!p.counts) {
+    hipLaunchKernelGGL((moe_plan_place_kernel<false>), dim3(blocks), dim3(kPlanThreads), 0, s, p);
     return hipGetLastError();
   }
   hipLaunchKernelGGL(moe_plan_count_kernel, dim3(blocks), dim3(kPlanThreads), 0, s, p);

@@ -434,7 +434,7 @@ int moe_route_backward_run(int64_t T, int E, int top_k, const float* dweights, c
  *            outside [0, E).
  *   ids      int32 [T][top_k].
  *   workspace  DEVICE, moe_plan_workspace_bytes(T * top_k, E) bytes, 4-byte
- *            aligned (0 bytes up to 4096 pairs: may be NULL).  It holds nothing
+ *            aligned (0 bytes up to 16384 pairs: may be NULL).  It holds nothing
  *            between calls; calls that may run at the same time need their own.
  * T = 0 writes offsets only.  Errors: SG_ERR_NULL, SG_ERR_ALIGN, SG_ERR_SHAPE,
  * SG_ERR_HIP.

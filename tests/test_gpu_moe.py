@@ -405,6 +405,54 @@ def test_plan_of_one_expert_and_of_none(T):
     check_plan(torch.full((T, 4), -1, dtype=torch.int32), 8)
 
 
+# Both sides of each change of the split: workgroups of 1024 pairs that count
+# by themselves (up to 16), chunks of 1024, 2048, 4096 and 8192 pairs with
+# counts of their own, partial last chunks, and divisions by every kind of k.
+@pytest.mark.parametrize("T,k,E,kind", [
+    (1025, 1, 256, "alone"), (341, 3, 2, "alone"), (2048, 8, 256, "alone"),
+    (64, 256, 256, "alone"), (65, 255, 9, "counted"), (16385, 1, 1, "counted"),
+    (5462, 3, 256, "counted"), (8193, 4, 256, "counted"), (16385, 8, 256, "counted"),
+    (29128, 9, 129, "counted"), (90001, 11, 60, "counted"), (262147, 8, 200, "counted")])
+@pytest.mark.parametrize("spread", ["all", "one", "sorted"])
+def test_plan_splits(T, k, E, kind, spread):
+    rng = np.random.default_rng(T + k + E)
+    ids = rng.integers(-1, E + 1, (T, k)).astype(np.int32)
+    if spread == "one":
+        ids[rng.random((T, k)) < 0.97] = E - 1
+    if spread == "sorted":
+        ids = np.sort(ids.reshape(-1))[::-1].reshape(T, k).copy()
+    check_plan(torch.from_numpy(ids), E)
+    assert sg.gemm_last_kernel() == "moe_plan_place_kernel<%s>" % kind
+
+
+def test_plan_of_the_most_pairs():
+    k = 7
+    T = (2 ** 31 - 1) // k
+    P, half = T * k, T * k // 2
+    ids = torch.zeros(T, k, dtype=torch.int32, device="cuda")
+    flat = ids.view(-1)
+    flat[:half] = 1                                   # the first half goes behind the second
+    flat[P - 5:] = 3                                  # and five pairs name no expert
+    offsets, rows, slots = sg.moe_plan(ids, 3)
+    n0 = P - 5 - half
+    assert offsets.tolist() == [0, n0, P - 5, P - 5]
+    i = torch.arange(P, dtype=torch.int32, device="cuda")
+    slots = slots.view(-1)
+    assert torch.equal(slots[:half], i[:half] + n0) and torch.equal(slots[half:P - 5], i[:n0])
+    assert bool((slots[P - 5:] == -1).all()) and bool((rows[P - 5:] == -1).all())
+    i //= k
+    assert torch.equal(rows[:n0], i[half:P - 5]) and torch.equal(rows[n0:P - 5], i[:half])
+
+
+@pytest.mark.parametrize("T,E", [(4097, 8), (16385, 256), (65537, 256)])
+def test_plan_writes_its_workspace_only(T, E):
+    ids = torch.from_numpy(np.random.default_rng(T).integers(0, E, (T, 4)).astype(np.int32))
+    n = sg.moe_plan_workspace_bytes(T * 4, E)
+    ws = torch.full((n + 132,), 85, dtype=torch.uint8, device="cuda")
+    check_plan(ids, E, workspace=ws[68:])             # 4-byte aligned
+    assert n > 0 and bool((ws[:68] == 85).all()) and bool((ws[68 + n:] == 85).all())
+
+
 def test_plan_into_buffers_with_a_workspace():
     rng = np.random.default_rng(6)
     T, k, E = 3000, 4, 40
