@@ -684,10 +684,10 @@ bool rows_of_four(const void* p, int64_t ld, int dtype) {
 constexpr int64_t kPlanAlone = 16384;
 
 // Pairs that a workgroup of the plan sorts, a multiple of 64 for each of its 16
-// waves.  Every workgroup reads the n workgroups' counts of E experts, n * E
-// in all, and places P / n pairs, about 8 / n of the time a count takes for
-// each: fewer workgroups the more experts (256 experts, us, this / 1024 pairs
-// a workgroup up to 256 of them: 131072 pairs 9.2 / 10.3, 524288 13.9 / 16.2).
+// waves.  Each of n workgroups reads n * E counts and places P / n pairs, and
+// a pair takes as long as about eight counts: so n^2 E <= 8 P, fewer workgroups
+// the more experts (256 experts, us, this / 1024 pairs a workgroup up to 256 of
+// them: 131072 pairs 9.2 / 10.3, 524288 13.9 / 16.2).
 int64_t plan_chunk(int64_t P, int E) {
   int64_t chunk = 1024;
   if (P <= kPlanAlone) return chunk;
