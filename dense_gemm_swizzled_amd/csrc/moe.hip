@@ -266,10 +266,12 @@ __device__ __forceinline__ int choose(const RouteParams& p, int lane, const Key 
 // 2^-24 of the row's largest score, a sigmoid is off by at most 8 (expf 4, the
 // sum and the quotient 1 each, twice), a softmax score by 40 (the rounded
 // difference in the exponent and expf 24, the sum over the experts 10, the
-// divisor's reciprocal and product 3), and the sum with the bias by half a
-// unit of the key.  If two keys whose order matters lie closer than twice that
-// -- four times for sums of two -- the wave decides again in 64 bits: with 256
-// experts about one token in a thousand does (sigmoid; softmax fewer).
+// divisor's reciprocal and product 3), and the sum with the bias by a unit of
+// the key.  If two keys whose order matters lie closer than twice that, the
+// wave decides again in 64 bits, and so it does for groups closer than eight
+// times that: a sum of two keys has both errors and rounds by up to two units
+// of the larger key itself.  With 256 experts about one token in a thousand is
+// decided again (sigmoid; softmax fewer).
 //
 // Bound by the instructions of the rounds (about 30 of a wave each), not by
 // the logits' bytes: 16384 tokens, top 8, softmax, us in a graph: 256 experts
@@ -321,7 +323,7 @@ __global__ void __launch_bounds__(kBlockThreads) moe_route_kernel(const RoutePar
         p, reinterpret_cast<RouteScratch<Lanes, float>&>(scratch[slot]), lane, key);
   int found = choose<Lanes, Scores>(p, lane, key, s, chosen, gap);
   if constexpr (Scores) {
-    if (__any(!(gap > 2 * off) || !(group_gap > 4 * off))) {
+    if (__any(!(gap > 2 * off) || !(group_gap > 8 * off))) {
       double wide[kHeld];
       const double div = scores_of<Lanes>(x, p.score, wide);
 #pragma unroll

@@ -1,0 +1,88 @@
+"""Experts and groups in the order of their 64-bit keys, where keys made in
+32 bits would put them in another."""
+import numpy as np
+import pytest
+import torch
+
+import dense_gemm_swizzled_amd as sg
+
+pytestmark = pytest.mark.gpu
+
+
+def keys64(x, score, bias):
+    x = x.astype(np.float64)
+    if score == "sigmoid":
+        s = np.where(x < 0, np.exp(np.minimum(x, 0)), 1.0) / (1 + np.exp(-np.abs(x)))
+    else:
+        e = np.exp(x - x.max(1, keepdims=True))
+        s = e / e.sum(1, keepdims=True)
+    return s if bias is None else s + bias.astype(np.float64)
+
+
+def choice64(key, k, n_groups=1, top_groups=1):
+    """(ids, sums): the choice by top-2 groups for keys [T][E], and the groups'
+    sums [T][n_groups]."""
+    T, E = key.shape
+    key = key.copy()
+    sums = None
+    if n_groups > 1:
+        g = key.reshape(T, n_groups, E // n_groups)
+        top = -np.sort(-g, axis=2)[:, :, :2]
+        sums = top[:, :, 0] + (top[:, :, 1] if top.shape[2] > 1 else 0)
+        order = np.argsort(-sums, axis=1, kind="stable")
+        np.put_along_axis(g, order[:, top_groups:, None], -np.inf, axis=1)
+        key = g.reshape(T, E)
+    return np.argsort(-key, axis=1, kind="stable")[:, :k], sums
+
+
+def gpu_ids(x, k, bias, **kw):
+    b = None if bias is None else torch.from_numpy(bias).cuda()
+    return sg.moe_route(torch.from_numpy(x).cuda(), k, bias=b, **kw)[1].cpu().numpy()
+
+
+def halves(rng, n, base):
+    """(logits, bias): two groups of two sigmoid experts whose keys lie in the
+    middle between two fp32 values near `base`, those of group 0 by a little
+    above it and those of group 1 below in fp32: each key is off by half a
+    step u in favour of group 0, and so is each group's sum (by u).  The exact
+    sums favour group 1 by less than 2^-25."""
+    u = float(np.spacing(np.float32(base)))
+    # Experts 0 and 2: scores that fp32 rounds to 1/2, keys on the middle, from
+    # where an odd step rounds up and an even one down.
+    q0, q2, q1, q3 = 1, 2, 40, 37
+    bias = base + np.array([(q0 + 0.5) * u - 0.5, q1 * u, (q2 + 0.5) * u - 0.5, q3 * u])
+    assert np.array_equal(bias.astype(np.float32).astype(np.float64), bias)
+    x = np.empty((n, 4))
+    x[:, 0], x[:, 2] = -rng.uniform(2e-8, 5e-8, n), rng.uniform(2e-8, 5e-8, n)
+    # Experts 1 and 3: small scores (fp32 has them to 2^-31) next to the middle,
+    # with equal whole steps in both groups, one more than a multiple of four.
+    r1 = 4 * rng.integers(max(1, int(9e-4 / u / 4)), int(6e-3 / u / 4), n)
+    r1 += (1 - q0 - q1) % 4
+    r3 = r1 + q0 + q1 - q2 - q3
+    for e, s in ((1, (r1 + 0.5) * u + 1.2e-9), (3, (r3 + 0.5) * u - 1.2e-9)):
+        x[:, e] = np.log(s / (1 - s))
+    return x.astype(np.float32), bias.astype(np.float32)
+
+
+@pytest.mark.parametrize("base", [8, 16, 64, 128, 512, 1024])
+@pytest.mark.parametrize("swap", [False, True])
+def test_group_sums_whose_rounding_matters(base, swap):
+    x, bias = halves(np.random.default_rng(base), 4000, base)
+    if swap:
+        x, bias = np.ascontiguousarray(x[:, [2, 3, 0, 1]]), bias[[2, 3, 0, 1]]
+    want, sums = choice64(keys64(x, "sigmoid", bias), 2, 2, 1)
+    # Far beyond what 64 bits leave open (2^-52 of the base a sum), and nearly
+    # always against the order of the fp32 sums.
+    clear = np.abs(sums[:, 0] - sums[:, 1]) > 2.0 ** -48 * base
+    assert clear.mean() > 0.99 and (want[:, 0] // 2 == (0 if swap else 1)).mean() > 0.9
+    got = gpu_ids(x, 2, bias, score="sigmoid", n_groups=2, top_groups=1, group_score="top2")
+    wrong = (got != want).any(1) & clear
+    assert not wrong.any(), (int(wrong.sum()), x[wrong][:3].tolist())
+
+
+def test_a_group_sum_off_by_its_rounding():
+    x = np.array([[-3e-8, -6.795358, 3e-8, -6.958249]], np.float32)
+    bias = np.array([63.50004196, 64.00019836, 63.50015640, 64.00025177], np.float32)
+    want, _ = choice64(keys64(x, "sigmoid", bias), 2, 2, 1)
+    got = gpu_ids(x, 2, bias, score="sigmoid", n_groups=2, top_groups=1, group_score="top2")
+    assert np.array_equal(got, want)
