@@ -118,7 +118,8 @@ struct RouteScratch {
 };
 
 // Masks (kNone) the experts outside the top_groups best groups.  2^j lanes
-// share a group's members and merge their two largest.  Returns the gap
+// share a group's members and merge their two largest; half of their sum is
+// the group's score, which no finite keys make infinite.  Returns the gap
 // between the last kept and the first dropped group.
 template <int Lanes, class Key>
 __device__ __forceinline__ Key keep_groups(const RouteParams& p, RouteScratch<Lanes, Key>& sc,
@@ -146,7 +147,9 @@ __device__ __forceinline__ Key keep_groups(const RouteParams& p, RouteScratch<La
       b0 = OpMax{}(b0, o0);
     }
     if (g < G && part == 0)
-      sc.best[g] = p.group_score == SG_GROUP_TOP2 && b1 > kNone ? b0 + b1 : b0;
+      sc.best[g] = p.group_score != SG_GROUP_TOP2 ? b0
+                   : b1 > kNone                     ? b0 / 2 + b1 / 2
+                                                    : b0 / 2;
   }
   wave_sync();
   Key kept = (Key)__builtin_inff(), dropped = kNone;
@@ -268,10 +271,10 @@ __device__ __forceinline__ int choose(const RouteParams& p, int lane, const Key 
 // difference in the exponent and expf 24, the sum over the experts 10, the
 // divisor's reciprocal and product 3), and the sum with the bias by a unit of
 // the key.  If two keys whose order matters lie closer than twice that, the
-// wave decides again in 64 bits, and so it does for groups closer than eight
-// times that: a sum of two keys has both errors and rounds by up to two units
-// of the larger key itself.  With 256 experts about one token in a thousand is
-// decided again (sigmoid; softmax fewer).
+// wave decides again in 64 bits, and so it does for groups closer than four
+// times that: half a sum of two keys has half of both errors and rounds by up
+// to a unit of the larger key itself.  With 256 experts about one token in a
+// thousand is decided again (sigmoid; softmax fewer).
 //
 // Bound by the instructions of the rounds (about 30 of a wave each), not by
 // the logits' bytes: 16384 tokens, top 8, softmax, us in a graph: 256 experts
@@ -323,7 +326,7 @@ __global__ void __launch_bounds__(kBlockThreads) moe_route_kernel(const RoutePar
         p, reinterpret_cast<RouteScratch<Lanes, float>&>(scratch[slot]), lane, key);
   int found = choose<Lanes, Scores>(p, lane, key, s, chosen, gap);
   if constexpr (Scores) {
-    if (__any(!(gap > 2 * off) || !(group_gap > 8 * off))) {
+    if (__any(!(gap > 2 * off) || !(group_gap > 4 * off))) {
       double wide[kHeld];
       const double div = scores_of<Lanes>(x, p.score, wide);
 #pragma unroll

@@ -86,3 +86,26 @@ def test_a_group_sum_off_by_its_rounding():
     want, _ = choice64(keys64(x, "sigmoid", bias), 2, 2, 1)
     got = gpu_ids(x, 2, bias, score="sigmoid", n_groups=2, top_groups=1, group_score="top2")
     assert np.array_equal(got, want)
+
+
+def test_group_sums_beyond_the_largest_float():
+    """Biases whose sums of two pass fp32's range: large ones, and the type's
+    lowest value as a mask, which is finite and no -inf."""
+    rng = np.random.default_rng(5)
+    x = rng.standard_normal((64, 16)).astype(np.float32)
+    low = float(np.finfo(np.float32).min)
+    # (two of a group's four experts; unequal, so that only the sums are close)
+    for groups in ([(3.0e38, 3.1e38), (3.3e38, 3.2e38), (2.9e38, 3.2e38), (0.0, 3.4e38)],
+                   [(low, 0.9 * low), (low, 0.8 * low), (0.7 * low, 0.9 * low), (low, low)],
+                   [(0.9 * low, 0.8 * low), (0.7 * low, 0.6 * low), (0.75 * low, 0.5 * low),
+                    (0.1 * low, 0.95 * low)],
+                   [(3.3e38, low), (low, 0.9 * low), (2.0e38, 3.0e38), (3.4e38, 1.0)]):
+        bias = np.full(16, low, np.float32)
+        for g, pair in enumerate(groups):
+            bias[4 * g:4 * g + 2] = pair
+        for score in ("sigmoid", "softmax"):
+            for top, k in ((1, 1), (1, 2), (2, 1), (2, 2), (2, 3), (3, 4)):
+                want, _ = choice64(keys64(x, score, bias), k, 4, top)
+                got = gpu_ids(x, k, bias, score=score, n_groups=4, top_groups=top,
+                              group_score="top2")
+                assert np.array_equal(got, want), (groups, score, top, k)
