@@ -17,6 +17,7 @@ namespace {
 
 constexpr int kHeld = 4;             // experts of a quad: a lane holds one, or more in the gradient
 constexpr float kTiny = 0x1p-126f;   // smallest sum that weights are divided by
+constexpr float kDenormalOff = 0x1p-146f;  // error of a score below 2^-126, eight steps
 constexpr int kBlockThreads = 256;
 
 template <int DT>
@@ -270,7 +271,9 @@ __device__ __forceinline__ int choose(const RouteParams& p, int lane, const Key 
 // sum and the quotient 1 each, twice), a softmax score by 40 (the rounded
 // difference in the exponent and expf 24, the sum over the experts 10, the
 // divisor's reciprocal and product 3), and the sum with the bias by a unit of
-// the key.  If two keys whose order matters lie closer than twice that, the
+// the key.  Scores below 2^-126 are 2^-149 apart and off by up to three such
+// steps (expf 2, the quotient and a half sum of two the third), whatever their
+// size.  If two keys whose order matters lie closer than twice all that, the
 // wave decides again in 64 bits, and so it does for groups closer than four
 // times that: half a sum of two keys has half of both errors and rounds by up
 // to a unit of the larger key itself.  With 256 experts about one token in a
@@ -319,7 +322,7 @@ __global__ void __launch_bounds__(kBlockThreads) moe_route_kernel(const RoutePar
       far = a < __builtin_inff() ? OpMax{}(far, a) : far;
     }
     const float units = p.score == SG_SCORE_SIGMOID ? 8.0f : 40.0f;
-    off = 0x1p-24f * lane_reduce<Lanes>(units * top + far, OpMax{});
+    off = 0x1p-24f * lane_reduce<Lanes>(units * top + far, OpMax{}) + kDenormalOff;
   }
   if (p.n_groups > 1)
     group_gap = keep_groups<Lanes>(

@@ -109,3 +109,19 @@ def test_group_sums_beyond_the_largest_float():
                 got = gpu_ids(x, k, bias, score=score, n_groups=4, top_groups=top,
                               group_score="top2")
                 assert np.array_equal(got, want), (groups, score, top, k)
+
+
+@pytest.mark.parametrize("E,n_groups", [(16, 4), (64, 8), (256, 8)])
+@pytest.mark.parametrize("with_bias", [False, True])
+def test_sums_of_scores_that_are_denormal(E, n_groups, with_bias):
+    """Sigmoid scores below 2^-126 are 2^-149 apart in fp32, far coarser than
+    a relative bound of their error."""
+    rng = np.random.default_rng(E)
+    x = rng.uniform(-103.9, -88.0, (3000, E)).astype(np.float32)
+    x[:1000] = rng.uniform(-103.9, -100.0, (1000, E))
+    bias = (2.0 ** -146 * rng.integers(0, 3, E)).astype(np.float32) if with_bias else None
+    want, _ = choice64(keys64(x, "sigmoid", bias), 4, n_groups, n_groups // 2)
+    got = gpu_ids(x, 4, bias, score="sigmoid", n_groups=n_groups, top_groups=n_groups // 2,
+                  group_score="top2")
+    wrong = (got != want).any(1)
+    assert not wrong.any(), (int(wrong.sum()), x[wrong][:1].tolist())
