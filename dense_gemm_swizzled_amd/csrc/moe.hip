@@ -115,16 +115,20 @@ template <int Lanes, class Key>
 struct RouteScratch {
   Key keys[Lanes * kHeld];
   Key best[SG_MAX_ROUTE_GROUPS];
+  Key slack[SG_MAX_ROUTE_GROUPS];
   int keep[SG_MAX_ROUTE_GROUPS];
 };
 
 // Masks (kNone) the experts outside the top_groups best groups.  2^j lanes
 // share a group's members and merge their two largest; half of their sum is
-// the group's score, which no finite keys make infinite.  Returns the gap
-// between the last kept and the first dropped group.
-template <int Lanes, class Key>
-__device__ __forceinline__ Key keep_groups(const RouteParams& p, RouteScratch<Lanes, Key>& sc,
-                                           int lane, Key (&key)[kHeld]) {
+// the group's score, which no finite keys make infinite.  With Certify, keys
+// are fp32 sums of a bias and a score that is off by up to `noise`; returns
+// whether every kept group stays above every dropped one whatever the errors.
+// In units of 2^-24 of a group's larger key, half the sum is off by noise, one
+// unit for the keys' own rounding and one for the sum's; a bound rounds by one.
+template <int Lanes, bool Certify, class Key>
+__device__ __forceinline__ bool keep_groups(const RouteParams& p, RouteScratch<Lanes, Key>& sc,
+                                            int lane, Key (&key)[kHeld], Key noise = 0) {
   const Key kNone = -(Key)__builtin_inff();
 #pragma unroll
   for (int i = 0; i < kHeld; ++i) sc.keys[kHeld * lane + i] = key[i];
@@ -147,13 +151,19 @@ __device__ __forceinline__ Key keep_groups(const RouteParams& p, RouteScratch<La
       b1 = OpMax{}(OpMax{}(b1, o1), b0 < o0 ? b0 : o0);
       b0 = OpMax{}(b0, o0);
     }
-    if (g < G && part == 0)
-      sc.best[g] = p.group_score != SG_GROUP_TOP2 ? b0
-                   : b1 > kNone                     ? b0 / 2 + b1 / 2
-                                                    : b0 / 2;
+    if (g < G && part == 0) {
+      const bool two = p.group_score == SG_GROUP_TOP2;
+      sc.best[g] = !two ? b0 : b1 > kNone ? b0 / 2 + b1 / 2 : b0 / 2;
+      if constexpr (Certify) {
+        const Key a0 = __builtin_fabsf(b0), a1 = __builtin_fabsf(b1);
+        const Key inf = __builtin_inff();
+        const Key m0 = a0 < inf ? a0 : 0, m1 = two && a1 < inf ? a1 : 0;
+        sc.slack[g] = noise + 0x1p-22f * OpMax{}(m0, m1);
+      }
+    }
   }
   wave_sync();
-  Key kept = (Key)__builtin_inff(), dropped = kNone;
+  Key low = (Key)__builtin_inff(), high = kNone;  // of the kept and the dropped groups
   for (int g = lane; g < G; g += Lanes) {
     const Key mine = sc.best[g];
     int above = 0;  // groups before this one; ties go to the lowest
@@ -163,8 +173,11 @@ __device__ __forceinline__ Key keep_groups(const RouteParams& p, RouteScratch<La
     }
     const bool keep = above < p.top_groups;
     sc.keep[g] = keep;
-    kept = keep && mine < kept ? mine : kept;
-    dropped = keep ? dropped : OpMax{}(dropped, mine);
+    if constexpr (Certify) {
+      const Key slack = sc.slack[g];
+      low = keep && mine - slack < low ? mine - slack : low;
+      high = keep ? high : OpMax{}(high, mine + slack);
+    }
   }
   wave_sync();
   const int inv = (65536 + size - 1) / size;  // e / size for e < 256
@@ -173,12 +186,10 @@ __device__ __forceinline__ Key keep_groups(const RouteParams& p, RouteScratch<La
     const int e = kHeld * lane + i;
     if (e < p.E && !sc.keep[(e * inv) >> 16]) key[i] = kNone;
   }
-  kept = -lane_reduce<Lanes>(-kept, OpMax{});
-  dropped = lane_reduce<Lanes>(dropped, OpMax{});
-  // (a dropped group without a key leaves no doubt, nor do two infinite ones
-  // beyond their order by index)
-  return dropped > kNone && kept < (Key)__builtin_inff() ? kept - dropped
-                                                         : (Key)__builtin_inff();
+  if constexpr (!Certify) return true;
+  low = -lane_reduce<Lanes>(-low, OpMax{});
+  high = lane_reduce<Lanes>(high, OpMax{});
+  return !(high > kNone) || low > high;  // (a dropped group without a key leaves no doubt)
 }
 
 // What keys are compared as: doubles as they are, floats as integers of the
@@ -199,7 +210,8 @@ __device__ __forceinline__ float key_at(int o) {
 // compares the lanes' heads, finds the lowest lane that holds the largest and
 // pops it.  Returns how many experts were found; with Gaps, `gap` is the
 // smallest distance between one choice and the next, the first expert not
-// chosen included.
+// chosen included, less what the keys' own rounding can make up: two units of
+// 2^-24 of the larger.
 struct Chosen {
   int id;
   float s;
@@ -233,14 +245,16 @@ __device__ __forceinline__ int choose(const RouteParams& p, int lane, const Key 
   int found = 0;
   Key last = (Key)__builtin_inff();
   gap = (Key)__builtin_inff();
+  // (Infinite keys are exact, as is the end of the keys: their NaN is no gap.)
+  auto note = [&](Key v) {
+    const Key m = OpMax{}(__builtin_fabsf(last), __builtin_fabsf(v));
+    gap = __builtin_fminf(gap, __builtin_fmaf(-0x1p-23f, m, last - v));
+    last = v;
+  };
   for (int k = 0; k < p.top_k; ++k) {
     const Ord m = lane_reduce<Lanes>(h[0], OpMax{});
     const bool any = m > kNone;
-    if constexpr (Gaps) {
-      const Key v = key_at(m), d = last - v;
-      gap = any && d < gap ? d : gap;
-      last = v;
-    }
+    if constexpr (Gaps) note(key_at(m));
     const uint64_t eq = __ballot(h[0] == m) & mask;
     found += any;
     if (any && (int)__builtin_ctzll(eq) == self) {
@@ -256,8 +270,7 @@ __device__ __forceinline__ int choose(const RouteParams& p, int lane, const Key 
   }
   if constexpr (Gaps) {
     const Ord m = lane_reduce<Lanes>(h[0], OpMax{});
-    const Key d = last - key_at(m);
-    gap = m > kNone && d < gap ? d : gap;
+    note(key_at(m));
   }
   return found;
 }
@@ -273,11 +286,12 @@ __device__ __forceinline__ int choose(const RouteParams& p, int lane, const Key 
 // divisor's reciprocal and product 3), and the sum with the bias by a unit of
 // the key.  Scores below 2^-126 are 2^-149 apart and off by up to three such
 // steps (expf 2, the quotient and a half sum of two the third), whatever their
-// size.  If two keys whose order matters lie closer than twice all that, the
-// wave decides again in 64 bits, and so it does for groups closer than four
-// times that: half a sum of two keys has half of both errors and rounds by up
-// to a unit of the larger key itself.  With 256 experts about one token in a
-// thousand is decided again (sigmoid; softmax fewer).
+// size.  If two keys whose order matters lie closer than twice all that, or
+// two groups than their bounds allow, the wave decides again in 64 bits: with
+// 256 experts, top 8, some four tokens in ten thousand are (softmax one).  The
+// unit is that of the two keys: rounding is monotonic, so no expert behind them
+// passes them by an error of its own size, and a large bias that switches an
+// expert off (or forces it) sends no token to the 64 bits.
 //
 // Bound by the instructions of the rounds (about 30 of a wave each), not by
 // the logits' bytes: 16384 tokens, top 8, softmax, us in a graph: 256 experts
@@ -307,29 +321,29 @@ __global__ void __launch_bounds__(kBlockThreads) moe_route_kernel(const RoutePar
     }
   }
   const float over = scores_of<Lanes>(x, p.score, s);
-  float group_gap = __builtin_inff(), gap;
-  float off = 0.0f;  // the largest error of a key
+  float noise = 0.0f;  // the largest error of a score
 #pragma unroll
   for (int i = 0; i < kHeld; ++i) key[i] = x[i];
   if constexpr (Scores) {
     const float inv = 1.0f / over;
-    float top = 0.0f, far = 0.0f;  // the largest score and finite |key|
+    float top = 0.0f;  // the largest score
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {
-      const float v = s[i] * inv, k = v + b[i], a = __builtin_fabsf(k);
+      const float v = s[i] * inv, k = v + b[i];
       key[i] = x[i] > kNone && k > kNone ? k : kNone;
       top = OpMax{}(top, v);
-      far = a < __builtin_inff() ? OpMax{}(far, a) : far;
     }
     const float units = p.score == SG_SCORE_SIGMOID ? 8.0f : 40.0f;
-    off = 0x1p-24f * lane_reduce<Lanes>(units * top + far, OpMax{}) + kDenormalOff;
+    noise = 0x1p-24f * units * lane_reduce<Lanes>(top, OpMax{}) + kDenormalOff;
   }
+  bool sure = true;
   if (p.n_groups > 1)
-    group_gap = keep_groups<Lanes>(
-        p, reinterpret_cast<RouteScratch<Lanes, float>&>(scratch[slot]), lane, key);
+    sure = keep_groups<Lanes, Scores>(
+        p, reinterpret_cast<RouteScratch<Lanes, float>&>(scratch[slot]), lane, key, noise);
+  float gap;
   int found = choose<Lanes, Scores>(p, lane, key, s, chosen, gap);
   if constexpr (Scores) {
-    if (__any(!(gap > 2 * off) || !(group_gap > 4 * off))) {
+    if (__any(!sure || !(gap > 2 * noise))) {
       double wide[kHeld];
       const double div = scores_of<Lanes>(x, p.score, wide);
 #pragma unroll
@@ -338,7 +352,7 @@ __global__ void __launch_bounds__(kBlockThreads) moe_route_kernel(const RoutePar
         wide[i] = x[i] > kNone && k > (double)kNone ? k : (double)kNone;
       }
       wave_sync();
-      if (p.n_groups > 1) keep_groups<Lanes>(p, scratch[slot], lane, wide);
+      if (p.n_groups > 1) keep_groups<Lanes, false>(p, scratch[slot], lane, wide);
       double ignored;
       found = choose<Lanes, false>(p, lane, wide, s, chosen, ignored);
     }

@@ -125,3 +125,47 @@ def test_sums_of_scores_that_are_denormal(E, n_groups, with_bias):
                   group_score="top2")
     wrong = (got != want).any(1)
     assert not wrong.any(), (int(wrong.sum()), x[wrong][:1].tolist())
+
+
+OFF = [-1e3, -1e4, -1e9, -3e38]
+
+
+@pytest.mark.parametrize("E,k,n_groups,top_groups", [(16, 4, 1, 1), (64, 6, 8, 3), (128, 8, 1, 1),
+                                                     (256, 8, 8, 4)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_experts_switched_off_by_a_bias(E, k, n_groups, top_groups, score):
+    rng = np.random.default_rng(E)
+    x = (2 * rng.standard_normal((500, E))).astype(np.float32)
+    for off in OFF + [1e9]:                           # (or forced to the front)
+        bias = (0.1 * rng.standard_normal(E)).astype(np.float32)
+        bias[[1, E // 2, E - 1]] = off
+        bias[2] = np.float32(0.9) * off
+        want, _ = choice64(keys64(x, score, bias), k, n_groups, top_groups)
+        got = gpu_ids(x, k, bias, score=score, n_groups=n_groups, top_groups=top_groups,
+                      group_score="top2")
+        assert np.array_equal(got, want), off
+
+
+@pytest.mark.parametrize("n_groups,top_groups", [(1, 1), (8, 4)])
+def test_an_expert_switched_off_costs_nothing(n_groups, top_groups):
+    """Its bias takes no part in the choice, so no more tokens need 64 bits:
+    counted with its size, every token did, and a call took 1.8 times as long."""
+    T, E, k = 32768, 256, 8
+    x = torch.randn(T, E, generator=torch.Generator().manual_seed(1)).cuda()
+    biases = [torch.zeros(E, device="cuda") for _ in range(2)]
+    biases[1][5] = -1e9
+    out = sg.moe_route(x, k, score="sigmoid", bias=biases[0])
+
+    def once(bias):
+        marks = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+        marks[0].record()
+        for _ in range(10):
+            sg.moe_route(x, k, score="sigmoid", bias=bias, n_groups=n_groups,
+                         top_groups=top_groups, group_score="top2", out=out)
+        marks[1].record()
+        marks[1].synchronize()
+        return marks[0].elapsed_time(marks[1])
+
+    times = np.array([[once(b) for b in biases] for _ in range(12)])[2:]
+    plain, off = np.median(times, axis=0)
+    assert off < 1.35 * plain, (plain, off)
