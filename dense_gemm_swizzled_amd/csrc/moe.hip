@@ -404,7 +404,8 @@ __device__ __forceinline__ void store_row4(const RouteParams& p, int64_t t, int 
 // and of the logits, summing u_j over the j that name the expert,
 //   sigmoid  dx_e = u_e (1 - s_e),
 //   softmax  dx_e = u_e - s_e sum_j u_j   (the sum is zero with renorm).
-// Only ratios of scores appear, so small scores lose nothing.  Bound by
+// Only ratios of scores appear, so small scores lose nothing; 1 - s_e is made
+// from the logit, so that scores near one do not either.  Bound by
 // memory: the gradient's rows are written whole; softmax reads the logits'
 // rows, sigmoid only the chosen logits.  Lane j of a token's lanes handles its
 // j-th expert and puts the result into the token's row in LDS; quad q of the
@@ -412,18 +413,23 @@ __device__ __forceinline__ void store_row4(const RouteParams& p, int64_t t, int 
 // stores of neighbouring lanes adjoin.  16384 x 256 fp32, us in a graph:
 // sigmoid 6.5, softmax 9.7 (both rows' bytes 6.7, one's written 3.4); every lane comparing
 // every chosen id with its experts instead took 15.4 (with one quad).
+struct Graded {
+  int id;
+  float s;     // the score, then its gradient u
+  float rest;  // 1 - s of a sigmoid
+};
 template <int DT, int Lanes, int Quads>
 __global__ void __launch_bounds__(kBlockThreads) moe_route_backward_kernel(
     const RouteParams p) {
   constexpr int kTokens = kBlockThreads / Lanes;
   __shared__ __attribute__((aligned(16))) float rows[kTokens][Quads * Lanes * kHeld];
-  __shared__ Chosen us_all[kTokens * SG_MAX_TOP_K];
+  __shared__ Graded us_all[kTokens * SG_MAX_TOP_K];
   const int lane = threadIdx.x % Lanes, slot = threadIdx.x / Lanes;
   const int64_t t = block_index() * kTokens + slot;
   const bool live = t < p.T;
   auto first = [&](int q) { return kHeld * (q * Lanes + lane); };
   float* const row = rows[slot];
-  Chosen* const us = us_all + slot * SG_MAX_TOP_K;
+  Graded* const us = us_all + slot * SG_MAX_TOP_K;
   const bool soft = p.score == SG_SCORE_SOFTMAX;
 
   // Softmax: the row's largest logit and sum of exponentials.
@@ -456,12 +462,17 @@ __global__ void __launch_bounds__(kBlockThreads) moe_route_backward_kernel(
   float sum = 0.0f;
   for (int k = lane; k < p.top_k; k += Lanes) {
     const int id = live ? p.ids[t * p.top_k + k] : -1;
-    float sk = 0.0f;
+    float sk = 0.0f, rest = 0.0f;
     if ((uint32_t)id < (uint32_t)p.E) {
       const float xk = clean(load_logit<DT>(p.logits, t * p.ldl + id));
-      if (xk > -__builtin_inff()) sk = soft ? expf(xk - top) / total : sigmoid_of(xk);
+      if (xk > -__builtin_inff()) {
+        const float z = expf(soft ? xk - top : -__builtin_fabsf(xk));
+        const float under = soft ? total : 1.0f + z;
+        sk = (soft || xk < 0 ? z : 1.0f) / under;
+        rest = (xk < 0 ? 1.0f : z) / under;
+      }
     }
-    us[k] = {id, sk};
+    us[k] = {id, sk, rest};
     sum += sk;
   }
   sum = lane_reduce<Lanes>(sum, OpSum{});
@@ -477,7 +488,7 @@ __global__ void __launch_bounds__(kBlockThreads) moe_route_backward_kernel(
     float u = 0.0f;
     if (sk > 0.0f) {
       u = sk / div * (p.dweights[t * p.top_k + k] * p.scale - mean);
-      if (!soft) u *= 1.0f - sk;
+      if (!soft) u *= us[k].rest;
     }
     us[k].s = u;
   }
