@@ -99,6 +99,7 @@ struct TileJob {
   const float* sb;      // scales of the tile's columns
   int a_total;          // rows of A (with `rows`)
   bool vec;             // D's rows are 16-byte aligned
+  bool past;            // a 16-bit D is stored past the caches (256x256 tiles)
 };
 
 // Epilogue element work shared by every kernel.  One chunk is 4 consecutive

@@ -22,9 +22,19 @@
 namespace sg {
 
 // The panels of the tile at D row row0 (m_valid rows) and column n0 (bn wide).
+// A 16-bit D of 256x256 tiles goes past the caches when grouped, whose tiles
+// come from many B (us alone / with a quantiser that reads D next, past |
+// through: 8192 x 2048 x 2048 of 64 groups 80.5 / 94.4 | 86.0 / 94.2; 32768 x
+// 4096 x 1024 of 32 180 / 242 | 193 / 253; x 2048, gathered 305 / 349 | 310 /
+// 357).  A dense product's reader finds it in the caches, and one of few K
+// tiles is faster itself (8192 x 8192 x 1024 82 / 115 | 74 / 104; x 8192 366 /
+// 415 | 375 / 405; 4096 x 16384 x 4096 204 / 255 | 207 / 241).  An fp32 D is
+// stored 16 bytes a lane, in parts of lines that the caches put together
+// (8192 x 4096 x 1024 72 / 99 | 51 / 76; 32768 x 4096 x 2048 of 32 groups 407 /
+// 528 | 357 / 487).
 template <bool Rows>
 __device__ __forceinline__ TileJob i8_job(const I8Params& p, int64_t row0, int m_valid,
-                                          int64_t n0, int bn, int g) {
+                                          int64_t n0, int bn, int g, bool past) {
   TileJob j;
   j.m_valid = m_valid;
   j.n_valid = (int)min<int64_t>(bn, p.N - n0);
@@ -52,6 +62,7 @@ __device__ __forceinline__ TileJob i8_job(const I8Params& p, int64_t row0, int m
   j.alpha = 1.0f;
   j.beta = 0.0f;
   j.vec = p.vec;
+  j.past = past;
   return j;
 }
 
@@ -61,7 +72,8 @@ __device__ __forceinline__ TileJob i8_dense_job(const I8Params& p, int wg, int b
   int tm, tn;
   raster(t, p.tiles_m, p.tiles_n, p.group_m, tm, tn);
   const int64_t m0 = (int64_t)tm * BM;
-  return i8_job<false>(p, m0, (int)min<int64_t>(BM, p.M - m0), (int64_t)tn * bn, bn, 0);
+  return i8_job<false>(p, m0, (int)min<int64_t>(BM, p.M - m0), (int64_t)tn * bn, bn, 0,
+                       false);
 }
 
 // The tile of workgroup `wg` among the groups' tiles, found from the offsets
@@ -118,7 +130,7 @@ __device__ __forceinline__ bool i8_grouped_job(const I8Params& p, int wg, TileJo
   int tm, tn;
   raster(t - first * p.tiles_n, tiles_g, p.tiles_n, p.group_m, tm, tn);
   const int m0 = tm * BM;
-  j = i8_job<Rows>(p, (int64_t)row0 + m0, min(BM, rows_g - m0), (int64_t)tn * bn, bn, g);
+  j = i8_job<Rows>(p, (int64_t)row0 + m0, min(BM, rows_g - m0), (int64_t)tn * bn, bn, g, true);
   return true;
 }
 

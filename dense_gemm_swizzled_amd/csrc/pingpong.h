@@ -273,9 +273,10 @@ __device__ __forceinline__ void store_d16_block(char* const (&cq)[4], const Tile
     if (ml >= j.m_valid || nl >= j.n_valid) continue;
     uint16_t* p = static_cast<uint16_t*>(D) + (j.d_row0 + ml) * ldd + j.n0 + nl;
     if constexpr (AnyD) {
-      // D goes past the caches, whose space the operands' panels use (measured
-      // 2-3% at 16 K tiles a workgroup, 12% at 8).
-      store_any<true>(p, d, j.n_valid - nl, j.vec);
+      if (j.past)
+        store_any<true>(p, d, j.n_valid - nl, j.vec);
+      else
+        store_any<false>(p, d, j.n_valid - nl, j.vec);
       continue;
     }
     if (j.n_valid - nl >= 8)

@@ -505,7 +505,7 @@ struct PingPong16Tile {
 #pragma unroll
         for (int jn = 0; jn < kJ; ++jn) {
           const int nl = 64 * w4 + 16 * jn + 4 * (lane >> 4);
-          store_any<true>(row + nl, __builtin_bit_cast(u32x4, acc[i][jn]), j.n_valid - nl, j.vec);
+          store_any(row + nl, __builtin_bit_cast(u32x4, acc[i][jn]), j.n_valid - nl, j.vec);
         }
       }
       return;
