@@ -483,6 +483,9 @@ namespace {
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 constexpr int64_t kI8MaxK = 131056;  // 2^14 * K < 2^31, K a multiple of 16
+// A launch has fewer than 2^32 threads along x, 512 a tile.  (A grid over x and
+// y would take more; 2^23 tiles are 2^29 columns of one row, or 2^37 outputs.)
+constexpr int64_t kI8MaxTiles = (int64_t{1} << 23) - 1;
 
 struct I8Shape {
   int64_t rows, cols;
@@ -626,7 +629,10 @@ int i8_run(const char* who, int G, int64_t M, int64_t N, int64_t K, const int32_
   // Row tiles: every group may end in a partial one.
   const int64_t groups = G == 0 ? 1 : G < M ? G : M;
   const int64_t tiles_m = G == 0 ? cdiv(M, T) : (M + groups * (T - 1)) / T;
-  if (tiles_m * tiles_n > 0x7fffffffLL) return fail(SG_ERR_SHAPE, "%s: too many tiles", who);
+  if (tiles_m * tiles_n > kI8MaxTiles)
+    return fail(SG_ERR_SHAPE, "%s: %lld tiles of %lld x %lld, at most %lld in a call", who,
+                (long long)(tiles_m * tiles_n), (long long)T, (long long)tn,
+                (long long)kI8MaxTiles);
   sg::I8Params p;
   p.A = A;
   p.B = B;

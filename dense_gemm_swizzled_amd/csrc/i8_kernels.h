@@ -82,7 +82,9 @@ __device__ __forceinline__ TileJob i8_dense_job(const I8Params& p, int wg, int b
 // the group.  About a microsecond of latency against a host round trip for
 // the offsets.  Offsets outside [0, M] are clamped and a decreasing pair is
 // an empty group, so no offsets make the kernel leave its buffers; tiles that
-// such offsets add beyond the grid are not computed.  False: no tile.
+// such offsets add beyond the grid are not computed.  (Nor do they overflow
+// the counts: the host keeps R / BM below 2^23, and of 256 groups at most 128
+// can rise over all R rows.)  False: no tile.
 template <int BM, bool Rows>
 __device__ __forceinline__ bool i8_grouped_job(const I8Params& p, int wg, TileJob& j, int bn) {
   const int lane = threadIdx.x & 63;

@@ -323,8 +323,9 @@ int gemm_layout128_run(int layout, int64_t M, int64_t N, int64_t K, const void* 
  * Codes are any of -128 .. 127.  A NaN scale makes its row or column NaN.
  * Here and in the calls below no output may overlap an input or another output.
  * Errors: SG_ERR_NULL, SG_ERR_ALIGN, SG_ERR_SHAPE (also a leading dimension
- * below its minimum, or a tile's panel of 2^31 bytes or more), SG_ERR_DTYPE,
- * SG_ERR_HIP.
+ * below its minimum, a tile's panel of 2^31 bytes or more, or 2^23 tiles or
+ * more: the tiles are 16 to 64 columns wide for up to 64 rows, 64 x 64 to 256 x
+ * 256 beyond), SG_ERR_DTYPE, SG_ERR_HIP.
  */
 int i8_gemm_run(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const float* SA,
                 const void* B, int64_t ldb, const float* SB, void* D, int64_t ldd, int d_dtype,
