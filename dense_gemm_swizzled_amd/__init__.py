@@ -715,9 +715,9 @@ def mxfp6_gemm(A, SFA, B, SFB, *, fmt: str = "e2m3", out_dtype=None, out=None):
 # above takes to check them (13 to 19 us), so the checks build their messages
 # only when they fail and the C functions are called directly (6 to 8 us a
 # call, 4 of them the launch itself).  The launches go to the tensors' device
-# even when another is current.  Results carry no autograd history:
-# moe_route_backward is a call of its own, and the 8-bit products are for
-# serving.
+# even when another is current.  moe_route's weights carry autograd history
+# (its backward pass is moe_route_backward); the 8-bit results carry none, their
+# codes are for serving.
 
 _torch = None
 _raw_stream = _current_device = None
@@ -930,6 +930,35 @@ def _score_code(score) -> int:
     return code
 
 
+_route_function = None
+
+
+def _routed(logits, top_k, score, renorm, scale, rest):
+    """moe_route with moe_route_backward as the gradient of the logits."""
+    global _route_function
+    if _route_function is None:
+
+        class MoeRoute(_torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, logits, top_k, form, rest):  # (gradients are off in here)
+                weights, ids = moe_route(logits, top_k, **form, **rest)
+                ctx.save_for_backward(logits, ids)
+                ctx.form = form
+                ctx.mark_non_differentiable(ids)
+                return weights, ids
+
+            @staticmethod
+            @_torch.autograd.function.once_differentiable
+            def backward(ctx, dweights, _):
+                logits, ids = ctx.saved_tensors
+                return (moe_route_backward(dweights.contiguous(), logits, ids, **ctx.form),
+                        None, None, None)
+
+        _route_function = MoeRoute
+    return _route_function.apply(logits, top_k, {"score": score, "renorm": renorm, "scale": scale},
+                                 rest)
+
+
 def moe_route(logits, top_k: int, *, score: str = "softmax", bias=None, n_groups: int = 1,
               top_groups: Optional[int] = None, group_score: str = "max", renorm: bool = True,
               scale: float = 1.0, out=None):
@@ -941,8 +970,15 @@ def moe_route(logits, top_k: int, *, score: str = "softmax", bias=None, n_groups
     ones the lowest index.  Weights are the scores of the chosen ones (without
     the bias), divided by their sum (renorm), times scale.  Logits of -inf or
     NaN are masked; a token with no expert left has ids -1 and weights 0.
-    out: (weights, ids) to write."""
+
+    Where the logits require a gradient, the weights carry it (the choice held
+    fixed; bias gets none).  out: (weights, ids) to write, which carry no
+    history: their gradient is a call of moe_route_backward."""
     lib, T = _lib_torch()
+    if out is None and logits.requires_grad and T.is_grad_enabled():
+        return _routed(logits, top_k, score, renorm, scale, {
+            "bias": bias, "n_groups": n_groups, "top_groups": top_groups,
+            "group_score": group_score})
     ldl = _pitch("logits", logits)
     n, E = logits.shape
     dt, code = _float_code("logits", logits.dtype), _score_code(score)
