@@ -99,8 +99,10 @@ def test_forward_and_gradient_in_a_graph():
     g = logits(40, 4, torch.float32, 1)
 
     def step():
+        # (No graph of x outlives the step: a captured one and an eager one of
+        # the same leaf would belong to two streams.)
         w, ids = sg.moe_route(x, 4, score="sigmoid")
-        return w, ids, torch.autograd.grad(w, x, g)[0]
+        return w.detach(), ids, torch.autograd.grad(w, x, g)[0]
 
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
