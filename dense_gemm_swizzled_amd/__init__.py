@@ -969,7 +969,8 @@ def moe_route(logits, top_k: int, *, score: str = "softmax", bias=None, n_groups
     scores), within the top_groups best of n_groups equal groups; among equal
     ones the lowest index.  Weights are the scores of the chosen ones (without
     the bias), divided by their sum (renorm), times scale.  Logits of -inf or
-    NaN are masked; a token with no expert left has ids -1 and weights 0.
+    NaN are masked (+inf is the largest float); a token with no expert left has
+    ids -1 and weights 0.
 
     Where the logits require a gradient, the weights carry it (the choice held
     fixed; bias gets none).  out: (weights, ids) to write, which carry no

@@ -387,7 +387,8 @@ int i8_quant_run(int64_t R, int64_t K, const void* X, int64_t ldx, int x_dtype, 
  * weights.
  *   scores   s[e] = softmax over the token's logits, or sigmoid of each.  A
  *            logit of -inf or NaN is masked: it scores 0, takes no part in the
- *            softmax and is never chosen.
+ *            softmax and is never chosen.  A logit of +inf counts as the largest
+ *            finite fp32 value (two of them, or one and that value, are equal).
  *   keys     s[e] + bias[e] evaluated in 64 bits.  Without a bias (and without
  *            SG_GROUP_TOP2 groups) the experts are ordered by their logits,
  *            which is the exact order of their scores.  A key of -inf or NaN

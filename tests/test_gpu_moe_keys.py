@@ -169,3 +169,22 @@ def test_an_expert_switched_off_costs_nothing(n_groups, top_groups):
     times = np.array([[once(b) for b in biases] for _ in range(12)])[2:]
     plain, off = np.median(times, axis=0)
     assert off < 1.35 * plain, (plain, off)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_an_infinite_logit_is_the_largest_float(score):
+    top = float(np.finfo(np.float32).max)
+    x = torch.zeros(4, 12)
+    x[0, 3] = float("inf")
+    x[1, [2, 7]] = float("inf")
+    x[2, 5], x[2, 9] = float("inf"), top
+    x[3, 4], x[3, 9] = top, float("inf")
+    w, ids = sg.moe_route(x.cuda(), 2, score=score)
+    w2, ids2 = sg.moe_route(x.clamp(max=top).cuda(), 2, score=score)
+    assert torch.equal(w, w2) and torch.equal(ids, ids2)
+    assert ids.tolist() == [[3, 0], [2, 7], [5, 9], [4, 9]]
+    if score == "softmax":
+        assert w.tolist() == [[1, 0], [0.5, 0.5], [0.5, 0.5], [0.5, 0.5]]
+    g = torch.ones(4, 2).cuda()
+    assert torch.equal(sg.moe_route_backward(g, x.cuda(), ids, score=score),
+                       sg.moe_route_backward(g, x.clamp(max=top).cuda(), ids, score=score))
