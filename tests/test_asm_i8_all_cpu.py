@@ -6,7 +6,7 @@ import subprocess
 
 import pytest
 
-from test_asm_lint_cpu import HIPCC, ROOT
+from test_asm_lint_cpu import HIPCC, ROOT, lint
 from test_asm_lint_i8_cpu import kernels
 
 
@@ -39,3 +39,33 @@ def test_stores_past_the_caches(listing):
             assert len(past) == 32 and all("dwordx4" in t for t in past), (name, len(past))
         else:
             assert not past, (name, past[:3])
+
+
+def library_kernels():
+    """The 8-bit kernels of the built library: the launch stubs of its objects."""
+    from dense_gemm_swizzled_amd import _build
+    obj = os.path.join(_build.BUILD, "launch_i8.o")
+    if not os.path.exists(obj):
+        pytest.skip("the library's objects are not here")
+    names = subprocess.run(["nm", obj], capture_output=True, text=True, check=True).stdout
+    return set(re.findall(r"__device_stub__(i8_\w+_kernelI\w+?E)EvNS_8I8ParamsE", names))
+
+
+def test_every_kernel_of_the_library_is_here(listing):
+    here = {re.search(r"(i8_\w+_kernelI\w+?E)EvNS_8I8ParamsE", n).group(1)
+            for n, _ in kernels(listing)}
+    assert len(here) == 25
+    assert here == library_kernels()
+
+
+def test_no_kernel_spills_or_loses_its_m0(listing):
+    found = dict(kernels(listing))
+    assert len(found) == 25, sorted(found)
+    for name, body in found.items():
+        bad, n = lint(body)
+        assert n > 0, f"{name}: no direct-to-LDS loads found"
+        assert not bad, f"{name}: {bad[:5]}"
+    spills = re.findall(r"\.vgpr_spill_count:\s*(\d+)", listing)
+    assert len(spills) == 25 and set(spills) == {"0"}
+    scratch = re.findall(r"\.private_segment_fixed_size:\s*(\d+)", listing)
+    assert len(scratch) == 25 and set(scratch) == {"0"}
