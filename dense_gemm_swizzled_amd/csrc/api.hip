@@ -510,8 +510,16 @@ I8Shape i8_shape(sg::I8Tile t) {
 // of B in all.  Narrow tiles while 16 columns a workgroup are no more
 // workgroups than CUs, then 32 (MI355X, us, 16 / 32 / 64 columns: 1 x 4096 x
 // 4096 5.5 / 6.0 / 7.0; 1 x 8192 x 8192 15.4 / 15.0 / 16.6); 64 where there
-// are many workgroups of few stages each (1 x 65536 x 2048 38 / 30 / 28; 64
-// experts of 2048 x 2048 79 / 53 / 47, but 128 of 1024 x 4096 106 / 86 / 91).
+// are many workgroups of few stages each.  How many changes with the columns
+// (us, 32 / 64, by K):
+//                          1024       2048       2560       3328       4096
+//   1 x 33024           11.4 10.0  19.1 19.5  20.2 22.8  25.0 29.2  33.2 37.8
+//   1 x 65536           20.9 17.7  30.3 27.7  32.8 32.1  42.2 40.7  53.5 56.2
+//   16 x 131072         40.0 30.7  57.5 54.2  69.6 64.3  84.3 79.6  94.9 104
+//   64 experts of 2048  48.0 35.4  66.9 56.2  70.3 66.9  86.4 83.1  103  106
+//   128 experts of 1024 48.6 34.9  66.9 56.3  70.9 67.0  87.1 83.3  103  106
+// Up to K = 2048, 64 columns cost at most 5% and gain up to 27%; beyond, they
+// gain at most 8% where there are many and lose 13 to 17% where there are few.
 // 17 to 32 rows: five stages for one workgroup a CU, two stages for more (32 x
 // 8192 x 8192 16.5 / 20.0, 32 x 28672 x 8192 55 / 49).
 sg::I8Tile pick_i8_stream(int64_t M, int64_t cols, int64_t K) {
