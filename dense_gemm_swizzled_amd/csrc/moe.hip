@@ -115,8 +115,7 @@ template <int Lanes, class Key>
 struct RouteScratch {
   Key keys[Lanes * kHeld];
   Key best[SG_MAX_ROUTE_GROUPS];
-  Key slack[SG_MAX_ROUTE_GROUPS];
-  int keep[SG_MAX_ROUTE_GROUPS];
+  int keep[SG_MAX_ROUTE_GROUPS];  // first the bits of a group's slack
 };
 
 // Masks (kNone) the experts outside the top_groups best groups.  2^j lanes
@@ -128,7 +127,7 @@ struct RouteScratch {
 // unit for the keys' own rounding and one for the sum's; a bound rounds by one.
 template <int Lanes, bool Certify, class Key>
 __device__ __forceinline__ bool keep_groups(const RouteParams& p, RouteScratch<Lanes, Key>& sc,
-                                            int lane, Key (&key)[kHeld], Key noise = 0) {
+                                            int lane, Key (&key)[kHeld], float noise = 0.0f) {
   const Key kNone = -(Key)__builtin_inff();
 #pragma unroll
   for (int i = 0; i < kHeld; ++i) sc.keys[kHeld * lane + i] = key[i];
@@ -155,10 +154,9 @@ __device__ __forceinline__ bool keep_groups(const RouteParams& p, RouteScratch<L
       const bool two = p.group_score == SG_GROUP_TOP2;
       sc.best[g] = !two ? b0 : b1 > kNone ? b0 / 2 + b1 / 2 : b0 / 2;
       if constexpr (Certify) {
-        const Key a0 = __builtin_fabsf(b0), a1 = __builtin_fabsf(b1);
-        const Key inf = __builtin_inff();
-        const Key m0 = a0 < inf ? a0 : 0, m1 = two && a1 < inf ? a1 : 0;
-        sc.slack[g] = noise + 0x1p-22f * OpMax{}(m0, m1);
+        const float a0 = __builtin_fabsf(b0), a1 = __builtin_fabsf(b1), inf = __builtin_inff();
+        const float m0 = a0 < inf ? a0 : 0.0f, m1 = two && a1 < inf ? a1 : 0.0f;
+        sc.keep[g] = __builtin_bit_cast(int, noise + 0x1p-22f * OpMax{}(m0, m1));
       }
     }
   }
@@ -172,12 +170,12 @@ __device__ __forceinline__ bool keep_groups(const RouteParams& p, RouteScratch<L
       above += o > mine || (o == mine && h < g);
     }
     const bool keep = above < p.top_groups;
-    sc.keep[g] = keep;
     if constexpr (Certify) {
-      const Key slack = sc.slack[g];
+      const float slack = __builtin_bit_cast(float, sc.keep[g]);
       low = keep && mine - slack < low ? mine - slack : low;
       high = keep ? high : OpMax{}(high, mine + slack);
     }
+    sc.keep[g] = keep;
   }
   wave_sync();
   const int inv = (65536 + size - 1) / size;  // e / size for e < 256
