@@ -293,10 +293,12 @@ __device__ __forceinline__ int choose(const RouteParams& p, int lane, const Key 
 //
 // Bound by the instructions of the rounds (about 30 of a wave each), not by
 // the logits' bytes: 16384 tokens, top 8, softmax, us in a graph: 256 experts
-// fp32 13.4 (3.4 for the bytes), 128 bf16 8.2, 64 fp32 5.5, 16 bf16 4.5; with
-// sigmoid scores, a bias and groups 25, 18, 12, 10.  (Keys compared as floats,
-// every score divided and a wider bound of doubt: 16.6 and 30 for 256.)  Four
-// tokens of 256 experts with groups take 6.2, of which 3 are a launch.
+// fp32 13.6 to 14.5 (3.4 for the bytes), 128 bf16 8.3 to 8.7, 64 fp32 5.6, 16
+// bf16 4.6; with sigmoid scores, a bias and groups 26.5 to 28, 17 to 18, 12.4,
+// 6.7 to 10.7, of which the bounds that decide between 32 and 64 bits are half
+// a microsecond.  (Keys compared as floats and every score divided: 16.6 and
+// 30 for 256.)  Four tokens of 256 experts with groups take 6.3, of which 3
+// are a launch.
 template <int DT, int Lanes, bool Scores>
 __global__ void __launch_bounds__(kBlockThreads) moe_route_kernel(const RouteParams p) {
   constexpr int kTokens = kBlockThreads / Lanes;
@@ -409,8 +411,9 @@ __device__ __forceinline__ void store_row4(const RouteParams& p, int64_t t, int 
 // j-th expert and puts the result into the token's row in LDS; quad q of the
 // lane holds experts from 4 * (q * Lanes + lane), so that a quad's loads and
 // stores of neighbouring lanes adjoin.  16384 x 256 fp32, us in a graph:
-// sigmoid 6.5, softmax 9.7 (both rows' bytes 6.7, one's written 3.4); every lane comparing
-// every chosen id with its experts instead took 15.4 (with one quad).
+// sigmoid 6.5, softmax 9.7, and 7.8 and 10.7 with three sets of rows in turn
+// (both rows' bytes 6.7, one's written 3.4); every lane comparing every chosen
+// id with its experts instead took 15.4 (with one quad).
 struct Graded {
   int id;
   float s;     // the score, then its gradient u

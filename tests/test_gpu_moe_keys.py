@@ -146,6 +146,21 @@ def test_experts_switched_off_by_a_bias(E, k, n_groups, top_groups, score):
         assert np.array_equal(got, want), off
 
 
+@pytest.mark.parametrize("n_groups,top_groups", [(1, 1), (8, 1), (8, 3)])
+def test_experts_forced_by_an_infinite_bias(n_groups, top_groups):
+    rng = np.random.default_rng(9)
+    x = (2 * rng.standard_normal((300, 64))).astype(np.float32)
+    for forced in ([5], [5, 6], [5, 50], [50, 51, 3]):
+        bias = (0.1 * rng.standard_normal(64)).astype(np.float32)
+        bias[forced] = np.inf
+        bias[[9, 60]] = -np.inf
+        for k in (1, 4):
+            want, _ = choice64(keys64(x, "sigmoid", bias), k, n_groups, top_groups)
+            got = gpu_ids(x, k, bias, score="sigmoid", n_groups=n_groups, top_groups=top_groups,
+                          group_score="top2")
+            assert np.array_equal(got, want), (forced, k)
+
+
 @pytest.mark.parametrize("n_groups,top_groups", [(1, 1), (8, 4)])
 def test_an_expert_switched_off_costs_nothing(n_groups, top_groups):
     """Its bias takes no part in the choice, so no more tokens need 64 bits:
