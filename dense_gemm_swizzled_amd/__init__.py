@@ -13,12 +13,15 @@ Two layers:
   ``gemm_lds_layout``, ``gemm_lds_layout_mxfp6``, ``gemm_lds_layout_cblock``,
   ``gemm_lds_image``, ``i8_gemm_run``, ``i8_grouped_gemm_run``, ``i8_quant_run``,
   ``moe_route_run``, ``moe_route_backward_run``, ``moe_plan_run``,
-  ``moe_plan_workspace_bytes``: the C entry points under the same names, taking
+  ``moe_plan_workspace_bytes``, ``moe_balance_run``, ``moe_balance_backward_run``,
+  ``moe_balance_workspace_bytes``, ``gemm_xent_run``, ``gemm_xent_backward_run``,
+  ``gemm_xent_workspace_bytes``, ``gemm_xent_backward_workspace_bytes``: the C entry points under the same names, taking
   integer device pointers.
 * ``gemm``, ``gemm_strided``, ``grouped_gemm``, ``mx_gemm``, ``mxfp4_gemm``,
   ``mxfp6_gemm``, ``mx_scales_blocks``, ``mx_gemm_blocks``, ``gemm_layout``,
   ``gemm_layout128``, ``i8_gemm``, ``i8_grouped_gemm``, ``i8_quant``,
-  ``moe_route``, ``moe_route_backward``, ``moe_plan``: the same calls on torch CUDA
+  ``moe_route``, ``moe_route_backward``, ``moe_plan``, ``moe_balance``,
+  ``moe_balance_backward``, ``gemm_xent``, ``gemm_xent_backward``: the same calls on torch CUDA
   tensors (shapes read from the tensors, output allocated by torch, launched
   on torch's current stream).
 """
@@ -49,12 +52,17 @@ __all__ = [
     "i8_gemm", "i8_grouped_gemm", "i8_quant", "moe_route", "moe_route_backward", "moe_plan",
     "SG_SCORE_SOFTMAX", "SG_SCORE_SIGMOID", "SG_GROUP_MAX", "SG_GROUP_TOP2", "SG_MAX_TOP_K",
     "SG_MAX_ROUTE_GROUPS",
+    "moe_balance_run", "moe_balance_backward_run", "moe_balance_workspace_bytes",
+    "moe_balance", "moe_balance_backward",
+    "gemm_xent_run", "gemm_xent_backward_run", "gemm_xent_workspace_bytes",
+    "gemm_xent_backward_workspace_bytes", "gemm_xent", "gemm_xent_backward", "SG_I32", "SG_I64",
     "library_path", "load",
 ]
 
 SG_OK = 0
 SG_NONE, SG_F16, SG_BF16, SG_F32, SG_E4M3, SG_E8M0 = 0, 1, 2, 3, 4, 5
 SG_E2M1, SG_E2M3, SG_E3M2 = 6, 7, 8
+SG_I32, SG_I64 = 9, 10
 SG_SF_ROWS, SG_SF_BLOCKS = 0, 1
 SG_K_MAJOR, SG_MN_MAJOR = 0, 1
 SG_MAX_GROUPS = 256
@@ -128,7 +136,20 @@ def load():
     lib.moe_plan_run.argtypes = [i64, i32, i32, vp, vp, vp, vp, vp, i64, vp]
     lib.moe_plan_workspace_bytes.argtypes = [i64, i32]
     lib.moe_plan_workspace_bytes.restype = ctypes.c_int64
-    for f in (lib.i8_gemm_run, lib.i8_grouped_gemm_run, lib.i8_quant_run, lib.moe_route_run,
+    lib.moe_balance_run.argtypes = [i64, i32, i32, vp, i64, i32, vp, i32, vp, vp, vp, vp, i64, vp]
+    lib.moe_balance_backward_run.argtypes = [i64, i32, vp, vp, i64, i32, vp, vp, i32, vp, i64, vp]
+    lib.moe_balance_workspace_bytes.argtypes = [i64, i32]
+    lib.moe_balance_workspace_bytes.restype = ctypes.c_int64
+    lib.gemm_xent_run.argtypes = [i64, i64, i64, f32, vp, i64, vp, i64, i32, vp, i32, vp, vp, vp,
+                                  i64, vp]
+    lib.gemm_xent_backward_run.argtypes = [i64, i64, i64, f32, vp, vp, vp, i64, vp, i64, i32, vp,
+                                           i32, vp, vp, i64, vp, i64, vp, i64, vp]
+    lib.gemm_xent_workspace_bytes.argtypes = [i64, i64, i64]
+    lib.gemm_xent_backward_workspace_bytes.argtypes = [i64, i64, i64, i64]
+    for f in (lib.gemm_xent_workspace_bytes, lib.gemm_xent_backward_workspace_bytes):
+        f.restype = i64
+    for f in (lib.moe_balance_run, lib.moe_balance_backward_run, lib.gemm_xent_run, lib.gemm_xent_backward_run,
+              lib.i8_gemm_run, lib.i8_grouped_gemm_run, lib.i8_quant_run, lib.moe_route_run,
               lib.moe_route_backward_run, lib.moe_plan_run, lib.mx_scales_to_blocks, lib.mx_gemm_blocks_run, lib.gemm_run, lib.gemm_strided_run, lib.grouped_gemm_run, lib.mx_gemm_run,
               lib.mxfp4_gemm_run, lib.mxfp6_gemm_run,
               lib.gemm_layout_run, lib.gemm_layout128_run, lib.gemm_layout_io_run,
@@ -242,6 +263,44 @@ def moe_plan_run(T, E, top_k, ids, offsets, rows, slots, workspace, workspace_by
 
 def moe_plan_workspace_bytes(P, E) -> int:
     return load().moe_plan_workspace_bytes(P, E)
+
+
+def moe_balance_run(T, E, top_k, logits, ldl, dtype, ids, score, loss, counts, tokens, workspace,
+                    workspace_bytes, stream) -> int:
+    return load().moe_balance_run(T, E, top_k, logits, ldl, dtype, ids, score, loss, counts,
+                                  tokens, workspace, workspace_bytes, stream)
+
+
+def moe_balance_backward_run(T, E, dloss, logits, ldl, dtype, counts, tokens, score, dlogits,
+                             lddl, stream) -> int:
+    return load().moe_balance_backward_run(T, E, dloss, logits, ldl, dtype, counts, tokens,
+                                           score, dlogits, lddl, stream)
+
+
+def moe_balance_workspace_bytes(T, E) -> int:
+    return load().moe_balance_workspace_bytes(T, E)
+
+
+def gemm_xent_run(M, N, K, alpha, A, lda, B, ldb, ab_dtype, targets, target_dtype, loss, lse,
+                  workspace, workspace_bytes, stream) -> int:
+    return load().gemm_xent_run(M, N, K, alpha, A, lda, B, ldb, ab_dtype, targets, target_dtype,
+                                loss, lse, workspace, workspace_bytes, stream)
+
+
+def gemm_xent_backward_run(M, N, K, alpha, dloss, dlse, A, lda, B, ldb, ab_dtype, targets,
+                           target_dtype, lse, dA, ldda, dB, lddb, workspace, workspace_bytes,
+                           stream) -> int:
+    return load().gemm_xent_backward_run(M, N, K, alpha, dloss, dlse, A, lda, B, ldb, ab_dtype,
+                                         targets, target_dtype, lse, dA, ldda, dB, lddb,
+                                         workspace, workspace_bytes, stream)
+
+
+def gemm_xent_workspace_bytes(M, N, K) -> int:
+    return load().gemm_xent_workspace_bytes(M, N, K)
+
+
+def gemm_xent_backward_workspace_bytes(M, N, K, ldb) -> int:
+    return load().gemm_xent_backward_workspace_bytes(M, N, K, ldb)
 
 
 def gemm_last_error() -> str:
@@ -1081,3 +1140,249 @@ def moe_plan(ids, n_experts: int, *, out=None, workspace=None):
     _launch(lib.moe_plan_run, dev, n, n_experts, top_k, ids.data_ptr(), offsets.data_ptr(),
             rows.data_ptr(), slots.data_ptr(), workspace.data_ptr() if need else None, need)
     return offsets, rows, slots
+
+
+# ------------------------------------------------- the routing's balance loss
+
+_balance_function = None
+
+
+def _balanced(logits, ids, score, workspace):
+    """moe_balance with moe_balance_backward as the gradient of the logits."""
+    global _balance_function
+    if _balance_function is None:
+
+        class MoeBalance(_torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, logits, ids, score, workspace):  # (gradients are off in here)
+                loss, counts, tokens = moe_balance(logits, ids, score=score, workspace=workspace)
+                ctx.save_for_backward(logits, counts, tokens)
+                ctx.score = score
+                ctx.mark_non_differentiable(counts, tokens)
+                return loss, counts, tokens
+
+            @staticmethod
+            @_torch.autograd.function.once_differentiable
+            def backward(ctx, dloss, *_):
+                logits, counts, tokens = ctx.saved_tensors
+                return (moe_balance_backward(dloss, logits, counts, tokens, score=ctx.score),
+                        None, None, None)
+
+        _balance_function = MoeBalance
+    return _balance_function.apply(logits, ids, score, workspace)
+
+
+def moe_balance(logits, ids, *, score: str = "softmax", out=None, workspace=None):
+    """How evenly a router spreads its tokens over the experts, from its logits
+    [T][E] and moe_route's ids int32 [T][top_k]: (loss float32 [], counts int32
+    [E], tokens int32 []).
+
+    loss = sum over the experts of E * their share of the pairs * the mean over
+    the tokens of their share of the token's scores (softmax or sigmoid): 1 for
+    an even load, E at most.  counts are the pairs of each expert, tokens those
+    that have an expert left; ids outside [0, E) and masked logits (-inf, NaN)
+    do not count.
+
+    Where the logits require a gradient, the loss carries it (the counts held
+    fixed).  out: (loss, counts, tokens) to write, which carry no history: their
+    gradient is a call of moe_balance_backward.  workspace: a uint8 tensor of at
+    least moe_balance_workspace_bytes(T, E) bytes; by default one is allocated
+    for the call."""
+    lib, T = _lib_torch()
+    if out is None and logits.requires_grad and T.is_grad_enabled():
+        return _balanced(logits, ids, score, workspace)
+    ldl = _pitch("logits", logits)
+    n, E = logits.shape
+    dt, code = _float_code("logits", logits.dtype), _score_code(score)
+    if ids.dim() != 2:
+        _fail(-3, f"ids must be 2-D, got shape {tuple(ids.shape)}")
+    _int("E", E)
+    top_k = _int("top_k", ids.shape[1])
+    _packed("ids", ids, (n, top_k), T.int32)
+    if out is None:
+        _on_one_device(logits, ids, workspace)
+    else:
+        loss, counts, tokens = out
+        _packed("loss", loss, (), T.float32)
+        _vector("counts", counts, E, T.int32)
+        _packed("tokens", tokens, (), T.int32)
+        _on_one_device(logits, ids, loss, counts, tokens, workspace)
+    dev = logits.device
+    workspace = _workspace(workspace, lib.moe_balance_workspace_bytes(n, E), dev)
+    if out is None:
+        loss = T.empty((), dtype=T.float32, device=dev)
+        counts = T.empty(E, dtype=T.int32, device=dev)
+        tokens = T.empty((), dtype=T.int32, device=dev)
+    _launch(lib.moe_balance_run, dev, n, E, top_k, logits.data_ptr(), ldl, dt, ids.data_ptr(),
+            code, loss.data_ptr(), counts.data_ptr(), tokens.data_ptr(), workspace.data_ptr(),
+            workspace.numel())
+    return loss, counts, tokens
+
+
+def moe_balance_backward(dloss, logits, counts, tokens, *, score: str = "softmax", out=None):
+    """The gradient of the logits [T][E] (their type) from dloss float32 [], the
+    gradient of moe_balance's loss, and its counts and tokens."""
+    lib, T = _lib_torch()
+    ldl = _pitch("logits", logits)
+    n, E = logits.shape
+    dt, code = _float_code("logits", logits.dtype), _score_code(score)
+    _int("E", E)
+    _packed("dloss", dloss, (), T.float32)
+    _vector("counts", counts, E, T.int32)
+    _packed("tokens", tokens, (), T.int32)
+    lddl = E
+    if out is not None:
+        if out.shape != (n, E):
+            _fail(-3, f"out has shape {tuple(out.shape)}, expected ({n}, {E})")
+        if out.dtype is not logits.dtype:
+            _fail(-4, f"out has dtype {out.dtype}, expected {logits.dtype}")
+        lddl = _pitch("out", out)
+    _on_one_device(logits, dloss, counts, tokens, out)
+    dev = logits.device
+    if out is None:
+        out = T.empty(n, E, dtype=logits.dtype, device=dev)
+    _launch(lib.moe_balance_backward_run, dev, n, E, dloss.data_ptr(), logits.data_ptr(), ldl, dt,
+            counts.data_ptr(), tokens.data_ptr(), code, out.data_ptr(), lddl)
+    return out
+
+
+# ---------------------------------------------- cross entropy over a vocabulary
+
+def _xent_args(A, B, targets):
+    """(M, N, K, lda, ldb, the SG_* codes of A's and the targets' types)."""
+    T = _torch
+    lda, ldb = _pitch("A", A), _pitch("B", B)
+    M, K = A.shape
+    N, Kb = B.shape
+    if Kb != K:
+        _fail(-3, f"A and B disagree on K ({K} vs {Kb})")
+    if A.dtype is not B.dtype:
+        _fail(-4, f"A and B dtypes differ ({A.dtype} vs {B.dtype})")
+    dt = _float_code("A", A.dtype)
+    if dt == SG_F32:
+        _fail(-4, "A has dtype torch.float32, expected float16 or bfloat16")
+    wide = targets.dtype is T.int64
+    _vector("targets", targets, M, T.int64 if wide else T.int32)
+    return M, N, K, lda, ldb, dt, SG_I64 if wide else SG_I32
+
+
+def _workspace(given, need: int, device):
+    """`given` checked against `need` bytes, or a new workspace of them."""
+    if need < 0:
+        _fail(need, gemm_last_error())
+    if given is None:
+        return _torch.empty(need, dtype=_torch.uint8, device=device)
+    _vector("workspace", given, given.numel(), _torch.uint8)
+    if given.numel() < need:
+        _fail(-3, f"workspace has {given.numel()} bytes, {need} are needed")
+    return given
+
+
+_xent_function = None
+
+
+def _xent(A, B, targets, alpha, workspace):
+    """gemm_xent with gemm_xent_backward as the gradient of A and B."""
+    global _xent_function
+    if _xent_function is None:
+
+        class GemmXent(_torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, A, B, targets, alpha, workspace):  # (gradients are off in here)
+                loss, lse = gemm_xent(A, B, targets, alpha=alpha, workspace=workspace)
+                ctx.save_for_backward(A, B, targets, lse)
+                ctx.alpha = alpha
+                ctx.set_materialize_grads(False)
+                return loss, lse
+
+            @staticmethod
+            @_torch.autograd.function.once_differentiable
+            def backward(ctx, dloss, dlse):
+                if dloss is None and dlse is None:
+                    return None, None, None, None, None
+                A, B, targets, lse = ctx.saved_tensors
+                dloss = _torch.zeros_like(lse) if dloss is None else dloss.contiguous()
+                dA, dB = gemm_xent_backward(
+                    dloss, A, B, targets, lse, alpha=ctx.alpha,
+                    dlse=None if dlse is None else dlse.contiguous(),
+                    need=ctx.needs_input_grad[:2])
+                return dA, dB, None, None, None
+
+        _xent_function = GemmXent
+    return _xent_function.apply(A, B, targets, alpha, workspace)
+
+
+def gemm_xent(A, B, targets, *, alpha: float = 1.0, out=None, workspace=None):
+    """Softmax cross entropy of M tokens over a vocabulary of N words, logits
+    alpha * A @ B.T, which are not kept: (loss float32 [M], lse float32 [M]).
+
+    A [M][K] (tokens) and B [N][K] (a word a row), both float16 or bfloat16,
+    rows padded or not; targets int32 or int64 [M].  lse is the logarithm of the
+    softmax's divisor, loss = lse - the target's logit, or 0 for a token whose
+    target lies outside [0, N).
+
+    Where A or B requires a gradient, loss and lse carry it.  out: (loss, lse)
+    to write, which carry no history: their gradient is a call of
+    gemm_xent_backward.  workspace: a uint8 tensor of at least
+    gemm_xent_workspace_bytes(M, N, K) bytes; by default one is allocated for
+    the call."""
+    lib, T = _lib_torch()
+    alpha = float(alpha)
+    if out is None and (A.requires_grad or B.requires_grad) and T.is_grad_enabled():
+        return _xent(A, B, targets, alpha, workspace)
+    M, N, K, lda, ldb, dt, tt = _xent_args(A, B, targets)
+    if out is not None:
+        loss, lse = out
+        _vector("loss", loss, M, T.float32)
+        _vector("lse", lse, M, T.float32)
+        _on_one_device(A, B, targets, loss, lse, workspace)
+    else:
+        _on_one_device(A, B, targets, workspace)
+    dev = A.device
+    workspace = _workspace(workspace, lib.gemm_xent_workspace_bytes(M, N, K), dev)
+    if out is None:
+        loss, lse = T.empty(2, M, dtype=T.float32, device=dev).unbind(0)
+    _launch(lib.gemm_xent_run, dev, M, N, K, alpha, A.data_ptr(), lda, B.data_ptr(), ldb, dt,
+            targets.data_ptr(), tt, loss.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+            workspace.numel())
+    return loss, lse
+
+
+def gemm_xent_backward(dloss, A, B, targets, lse, *, alpha: float = 1.0, dlse=None,
+                       need=(True, True), out=None, workspace=None):
+    """The gradients (dA [M][K], dB [N][K]), of A's and B's type, from dloss
+    float32 [M], the gradient of gemm_xent's loss, and dlse float32 [M], that of
+    its lse (None: zero).  lse is gemm_xent's.
+
+    need: which of the two are computed; the other is None.  out: (dA, dB) to
+    write (None: a new tensor), rows padded or not.  workspace: a uint8 tensor of
+    at least gemm_xent_backward_workspace_bytes(M, N, K, B.stride(0)) bytes."""
+    lib, T = _lib_torch()
+    M, N, K, lda, ldb, dt, tt = _xent_args(A, B, targets)
+    for name, t in (("dloss", dloss), ("lse", lse), ("dlse", dlse)):
+        if t is not None or name != "dlse":
+            _vector(name, t, M, T.float32)
+    out = out or (None, None)
+    pitch = []
+    for name, t, like, wanted in (("dA", out[0], A, need[0]), ("dB", out[1], B, need[1])):
+        if t is None or not wanted:
+            pitch.append(K)
+            continue
+        if t.shape != like.shape:
+            _fail(-3, f"{name} has shape {tuple(t.shape)}, expected {tuple(like.shape)}")
+        if t.dtype is not like.dtype:
+            _fail(-4, f"{name} has dtype {t.dtype}, expected {like.dtype}")
+        pitch.append(_pitch(name, t))
+    _on_one_device(A, B, targets, dloss, dlse, lse, workspace, *out)
+    dev = A.device
+    size = lib.gemm_xent_backward_workspace_bytes(M, N, K, ldb)
+    workspace = _workspace(workspace, size, dev)
+    dA, dB = (None if not wanted else T.empty_like(like, memory_format=T.contiguous_format)
+              if t is None else t
+              for t, like, wanted in ((out[0], A, need[0]), (out[1], B, need[1])))
+    _launch(lib.gemm_xent_backward_run, dev, M, N, K, float(alpha), dloss.data_ptr(),
+            None if dlse is None else dlse.data_ptr(), A.data_ptr(), lda, B.data_ptr(), ldb, dt,
+            targets.data_ptr(), tt, lse.data_ptr(), None if dA is None else dA.data_ptr(),
+            pitch[0], None if dB is None else dB.data_ptr(), pitch[1], workspace.data_ptr(),
+            workspace.numel())
+    return dA, dB

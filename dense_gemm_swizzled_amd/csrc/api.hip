@@ -14,6 +14,7 @@
 #include "launch.h"
 #include "lds_layout.h"
 #include "moe.h"
+#include "xent_plan.h"
 
 namespace {
 
@@ -56,7 +57,7 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 bool is_out_dtype(int dt) { return dt == SG_F32 || dt == SG_BF16 || dt == SG_F16; }
 
 constexpr int64_t kMaxExtent = (int64_t)1 << 31;  // buffer offsets are 32-bit
-constexpr int kCUs = 256;                          // MI355X compute units
+using sg::kCUs;
 constexpr int kGroupM = 8;
 
 // Largest byte extent one workgroup addresses through a buffer resource
@@ -82,26 +83,6 @@ sg::TileShape pick_tile(int64_t tiles256, int64_t tiles128, bool fits256) {
   if (tiles256 >= kCUs) return sg::kTile256;
   if (fits256 && cdiv(tiles128, kCUs) >= 2) return sg::kTile256;
   return sg::kTile128;
-}
-
-// Dense GEMM: 256x256 tiles when they fill the CUs, else 128x128 tiles when
-// they fill half of them, else 64x64 tiles (small problems: 1024^3 has 64
-// tiles of 128 but 256 of 64).  Between those, when the 256x256 tiles would
-// run on the ping-pong (K-major operands, or K a multiple of 64 with two or
-// more K tiles) and the 128x128 tiles would need three or more rounds of the
-// CUs, one partial round of the ping-pong is faster (bf16 on MI355X, TFLOP/s
-// 256 vs 128 tiles: 3072^3 1056 vs 694, 3584^3 1337 vs 911, 3072x3072x1024
-// 846 vs 585), though not against one or two rounds of 128x128 tiles
-// (2560^3 753 vs 847, 2048x4096x4096 934 vs 1041).
-// `fits256`: 256-row panels stay within 32-bit buffer offsets.
-sg::TileShape pick_dense_tile(int64_t M, int64_t N, int64_t K, bool a_mn, bool b_mn,
-                              bool fits256) {
-  if (cdiv(M, 256) * cdiv(N, 256) >= kCUs) return sg::kTile256;
-  const int64_t tiles128 = cdiv(M, 128) * cdiv(N, 128);
-  const bool pingpong = (!a_mn && !b_mn) || (K % 64 == 0 && K >= 128);
-  if (pingpong && fits256 && cdiv(tiles128, kCUs) >= 3) return sg::kTile256;
-  if (tiles128 >= kCUs / 2) return sg::kTile128;
-  return sg::kTile64;
 }
 
 int64_t tile_rows(sg::TileShape t) { return t == sg::kTile256 ? 256 : t == sg::kTile128 ? 128 : 64; }
@@ -171,9 +152,12 @@ int dense_run(const char* who, DenseMode mode, int swz, int64_t M, int64_t N, in
                        panel_extent(b_major, N, K, ldb, 256, eb) < kMaxExtent;
   const sg::TileShape tile = mode == kAblation256 || mode == kAblationIO ? sg::kTile256
                             : mode == kAblation128 ? sg::kTile128
-                                                   : pick_dense_tile(M, N, K, a_major == SG_MN_MAJOR,
-                                                                     b_major == SG_MN_MAJOR,
-                                                                     fits256);
+                                                   : sg::pick_dense_tile(
+                                                         M, N,
+                                                         (a_major == SG_K_MAJOR &&
+                                                          b_major == SG_K_MAJOR) ||
+                                                             (K % 64 == 0 && K >= 128),
+                                                         fits256);
   const int64_t T = tile_rows(tile);
   if (panel_extent(a_major, M, K, lda, T, eb) >= kMaxExtent ||
       panel_extent(b_major, N, K, ldb, T, eb) >= kMaxExtent ||
@@ -669,6 +653,64 @@ int i8_run(const char* who, int G, int64_t M, int64_t N, int64_t K, const int32_
   return ok();
 }
 
+// The checks that the cross entropy and its gradient share.
+int xent_check(const char* who, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
+               const void* B, int64_t ldb, int ab_dtype, const void* targets, int target_dtype) {
+  if (M < 0 || N < 0 || K < 0 || M >= kMaxExtent || N >= kMaxExtent)
+    return fail(SG_ERR_SHAPE, "%s: M=%lld, N=%lld (both below 2^31), K=%lld", who, (long long)M,
+                (long long)N, (long long)K);
+  if (ab_dtype != SG_F16 && ab_dtype != SG_BF16)
+    return fail(SG_ERR_DTYPE, "%s: ab_dtype %d is not SG_F16/SG_BF16", who, ab_dtype);
+  if (target_dtype != SG_I32 && target_dtype != SG_I64)
+    return fail(SG_ERR_DTYPE, "%s: target_dtype %d is not SG_I32/SG_I64", who, target_dtype);
+  if (K % 8) return fail(SG_ERR_SHAPE, "%s: K=%lld is not a multiple of 8", who, (long long)K);
+  if (lda < K || ldb < K || lda >= sg::kXentMaxLd || ldb >= sg::kXentMaxLd)
+    return fail(SG_ERR_SHAPE, "%s: lda=%lld, ldb=%lld outside [K=%lld, 2^22)", who,
+                (long long)lda, (long long)ldb, (long long)K);
+  if (lda % 8 || ldb % 8)
+    return fail(SG_ERR_ALIGN, "%s: the row pitches of A and B must be multiples of 16 bytes", who);
+  if (M > 0 && !targets) return fail(SG_ERR_NULL, "%s: targets is NULL", who);
+  if (K > 0 && ((M > 0 && !A) || (N > 0 && !B)))
+    return fail(SG_ERR_NULL, "%s: A or B is NULL", who);
+  if (!aligned16(A) || !aligned16(B) ||
+      reinterpret_cast<uintptr_t>(targets) % (target_dtype == SG_I64 ? 8 : 4))
+    return fail(SG_ERR_ALIGN, "%s: A and B must be 16-byte aligned, targets to its elements", who);
+  const int64_t side = sg::tile_side(sg::xent_tile(M, N, K));
+  if (cdiv(M, side) * cdiv(N, side) > sg::kXentMaxTiles)
+    return fail(SG_ERR_SHAPE, "%s: more than 2^23 tiles of %lld x %lld", who, (long long)side,
+                (long long)side);
+  return SG_OK;
+}
+
+sg::XentCall xent_call(int64_t M, int64_t N, int64_t K, float alpha, const void* A, int64_t lda,
+                       const void* B, int64_t ldb, int ab_dtype, const void* targets,
+                       int target_dtype, void* workspace) {
+  sg::XentCall c{};
+  c.M = M;
+  c.N = N;
+  c.K = K;
+  c.alpha = alpha;
+  c.A = A;
+  c.lda = lda;
+  c.B = B;
+  c.ldb = ldb;
+  c.bf16 = ab_dtype == SG_BF16;
+  c.targets = targets;
+  c.wide = target_dtype == SG_I64;
+  c.workspace = workspace;
+  return c;
+}
+
+int workspace_check(const char* who, const void* workspace, int64_t bytes, int64_t need) {
+  if (bytes < need)
+    return fail(SG_ERR_SHAPE, "%s: the workspace has %lld bytes, %lld are needed", who,
+                (long long)bytes, (long long)need);
+  if (need > 0 && !workspace) return fail(SG_ERR_NULL, "%s: workspace is NULL", who);
+  if (!aligned16(workspace))
+    return fail(SG_ERR_ALIGN, "%s: workspace must be 16-byte aligned", who);
+  return SG_OK;
+}
+
 // The checks that the forward and backward routing share.
 int route_check(const char* who, int64_t T, int E, int top_k, const void* logits, int64_t ldl,
                 int dtype, int score) {
@@ -691,6 +733,12 @@ int route_check(const char* who, int64_t T, int E, int top_k, const void* logits
 // Whether four values at any multiple of four of any row are one aligned access.
 bool rows_of_four(const void* p, int64_t ld, int dtype) {
   return ld % 4 == 0 && reinterpret_cast<uintptr_t>(p) % (4 * elem_bytes(dtype)) == 0;
+}
+
+// Tokens that a workgroup of the balance loss adds up: one workgroup up to 256
+// tokens, beyond that up to 256 workgroups.
+int64_t balance_chunk(int64_t T, int E) {
+  return T <= 256 ? 256 : std::max<int64_t>(64, cdiv(cdiv(T, 256), 64) * 64);
 }
 
 // Up to so many pairs the plan is one launch (us, one launch / two, 256
@@ -752,6 +800,84 @@ int i8_quant_run(int64_t R, int64_t K, const void* X, int64_t ldx, int x_dtype, 
                               "elements", who);
   hipError_t e = sg::launch_i8_quant(X, R, K, ldx, x_dtype, Q, ldq, S,
                                      static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, who);
+  return ok();
+}
+
+int64_t gemm_xent_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (M < 0 || N < 0 || K < 0 || M >= kMaxExtent || N >= kMaxExtent)
+    return fail(SG_ERR_SHAPE, "gemm_xent_workspace_bytes: M=%lld N=%lld K=%lld", (long long)M,
+                (long long)N, (long long)K);
+  return sg::xent_workspace(M, N, K);
+}
+
+int64_t gemm_xent_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t ldb) {
+  if (M < 0 || N < 0 || K < 0 || M >= sg::kXentMaxRows || N >= kMaxExtent || ldb < K ||
+      ldb >= sg::kXentMaxLd)
+    return fail(SG_ERR_SHAPE, "gemm_xent_backward_workspace_bytes: M=%lld (below 2^22), N=%lld, "
+                              "K=%lld, ldb=%lld", (long long)M, (long long)N, (long long)K,
+                (long long)ldb);
+  return M == 0 || N == 0 || K == 0 ? 0 : sg::xent_plan(M, N, K, ldb).bytes;
+}
+
+int gemm_xent_run(int64_t M, int64_t N, int64_t K, float alpha, const void* A, int64_t lda,
+                  const void* B, int64_t ldb, int ab_dtype, const void* targets, int target_dtype,
+                  float* loss, float* lse, void* workspace, int64_t workspace_bytes,
+                  void* stream) {
+  const char* who = "gemm_xent_run";
+  if (const int rc = xent_check(who, M, N, K, A, lda, B, ldb, ab_dtype, targets, target_dtype))
+    return rc;
+  if (M == 0) return ok();
+  if (!loss || !lse) return fail(SG_ERR_NULL, "%s: loss or lse is NULL", who);
+  if (!aligned4(loss) || !aligned4(lse))
+    return fail(SG_ERR_ALIGN, "%s: loss and lse must be 4-byte aligned", who);
+  if (const int rc = workspace_check(who, workspace, workspace_bytes,
+                                     sg::xent_workspace(M, N, K)))
+    return rc;
+  sg::XentCall c = xent_call(M, N, K, alpha, A, lda, B, ldb, ab_dtype, targets, target_dtype,
+                             workspace);
+  c.loss = loss;
+  c.lse = lse;
+  const hipError_t e = sg::launch_xent(c, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, who);
+  return ok();
+}
+
+int gemm_xent_backward_run(int64_t M, int64_t N, int64_t K, float alpha, const float* dloss,
+                           const float* dlse, const void* A, int64_t lda, const void* B,
+                           int64_t ldb, int ab_dtype, const void* targets, int target_dtype,
+                           const float* lse, void* dA, int64_t ldda, void* dB, int64_t lddb,
+                           void* workspace, int64_t workspace_bytes, void* stream) {
+  const char* who = "gemm_xent_backward_run";
+  if (const int rc = xent_check(who, M, N, K, A, lda, B, ldb, ab_dtype, targets, target_dtype))
+    return rc;
+  if (M >= sg::kXentMaxRows)
+    return fail(SG_ERR_SHAPE, "%s: M=%lld is not below 2^22", who, (long long)M);
+  if ((dA && ldda < K) || (dB && lddb < K))
+    return fail(SG_ERR_SHAPE, "%s: ldda=%lld or lddb=%lld is below K=%lld", who, (long long)ldda,
+                (long long)lddb, (long long)K);
+  if ((dA && (!aligned16(dA) || ldda % 8)) || (dB && (!aligned16(dB) || lddb % 8)))
+    return fail(SG_ERR_ALIGN, "%s: dA, dB and their row pitches must be 16-byte aligned", who);
+  if (dB && M > 0 && ((M - 1) * lda + K) * 2 >= kMaxExtent)
+    return fail(SG_ERR_SHAPE, "%s: A spans 2^31 bytes or more, too many for dB in one call", who);
+  if (M > 0 && N > 0 && K > 0 && (!dloss || !lse))
+    return fail(SG_ERR_NULL, "%s: dloss or lse is NULL", who);
+  if (!aligned4(dloss) || !aligned4(dlse) || !aligned4(lse))
+    return fail(SG_ERR_ALIGN, "%s: dloss, dlse and lse must be 4-byte aligned", who);
+  if (K == 0 || (!dA && !dB)) return ok();
+  if (const int rc = workspace_check(who, workspace, workspace_bytes,
+                                     gemm_xent_backward_workspace_bytes(M, N, K, ldb)))
+    return rc;
+  sg::XentCall c = xent_call(M, N, K, alpha, A, lda, B, ldb, ab_dtype, targets, target_dtype,
+                             workspace);
+  c.lse = const_cast<float*>(lse);
+  c.dloss = dloss;
+  c.dlse = dlse;
+  c.dA = dA;
+  c.ldda = ldda;
+  c.dB = dB;
+  c.lddb = lddb;
+  const hipError_t e = sg::launch_xent_backward(c, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail(e, who);
   return ok();
 }
@@ -825,6 +951,80 @@ int moe_route_backward_run(int64_t T, int E, int top_k, const float* dweights, c
   p.vec = rows_of_four(logits, ldl, dtype);
   p.vec_d = rows_of_four(dlogits, lddl, dtype);
   hipError_t e = sg::launch_moe_route_backward(dtype, p, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, who);
+  return ok();
+}
+
+int64_t moe_balance_workspace_bytes(int64_t T, int E) {
+  if (T < 0 || T >= kMaxExtent || E < 1 || E > SG_MAX_GROUPS)
+    return fail(SG_ERR_SHAPE, "moe_balance_workspace_bytes: T=%lld E=%d", (long long)T, E);
+  const int64_t parts = cdiv(T, balance_chunk(T, E));
+  return parts <= 1 ? 0 : parts * (E + 1) * 8;
+}
+
+int moe_balance_run(int64_t T, int E, int top_k, const void* logits, int64_t ldl, int dtype,
+                    const int32_t* ids, int score, float* loss, int32_t* counts,
+                    int32_t* tokens, void* workspace, int64_t workspace_bytes, void* stream) {
+  const char* who = "moe_balance_run";
+  if (const int rc = route_check(who, T, E, top_k, logits, ldl, dtype, score)) return rc;
+  if (T * top_k >= kMaxExtent)
+    return fail(SG_ERR_SHAPE, "%s: T * top_k = %lld is not below 2^31", who,
+                (long long)(T * top_k));
+  if (!loss || !counts || !tokens || (T > 0 && !ids))
+    return fail(SG_ERR_NULL, "%s: ids, loss, counts or tokens is NULL", who);
+  if (!aligned4(ids) || !aligned4(loss) || !aligned4(counts) || !aligned4(tokens))
+    return fail(SG_ERR_ALIGN, "%s: ids, loss, counts and tokens must be 4-byte aligned", who);
+  if (const int rc = workspace_check(who, workspace, workspace_bytes,
+                                     moe_balance_workspace_bytes(T, E)))
+    return rc;
+  sg::BalanceParams p{};
+  p.T = T;
+  p.E = E;
+  p.top_k = top_k;
+  p.logits = logits;
+  p.ldl = ldl;
+  p.score = score;
+  p.vec = rows_of_four(logits, ldl, dtype);
+  p.chunk = balance_chunk(T, E);
+  p.ids = ids;
+  p.loss = loss;
+  p.counts = counts;
+  p.tokens = tokens;
+  p.part = workspace;
+  p.parts = T > 0 ? (int)cdiv(T, p.chunk) : 1;
+  const hipError_t e = sg::launch_moe_balance(dtype, p, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, who);
+  return ok();
+}
+
+int moe_balance_backward_run(int64_t T, int E, const float* dloss, const void* logits,
+                             int64_t ldl, int dtype, const int32_t* counts,
+                             const int32_t* tokens, int score, void* dlogits, int64_t lddl,
+                             void* stream) {
+  const char* who = "moe_balance_backward_run";
+  if (const int rc = route_check(who, T, E, 1, logits, ldl, dtype, score)) return rc;
+  if (lddl < E) return fail(SG_ERR_SHAPE, "%s: lddl=%lld is below E=%d", who, (long long)lddl, E);
+  if (T == 0) return ok();
+  if (!dloss || !counts || !tokens || !dlogits)
+    return fail(SG_ERR_NULL, "%s: dloss, counts, tokens or dlogits is NULL", who);
+  if (!aligned4(dloss) || !aligned4(counts) || !aligned4(tokens) ||
+      reinterpret_cast<uintptr_t>(dlogits) % elem_bytes(dtype))
+    return fail(SG_ERR_ALIGN, "%s: every pointer must be aligned to its elements", who);
+  sg::BalanceParams p{};
+  p.T = T;
+  p.E = E;
+  p.logits = logits;
+  p.ldl = ldl;
+  p.score = score;
+  p.vec = rows_of_four(logits, ldl, dtype);
+  p.counts = const_cast<int32_t*>(counts);
+  p.tokens = const_cast<int32_t*>(tokens);
+  p.dloss = dloss;
+  p.dlogits = dlogits;
+  p.lddl = lddl;
+  p.vec_d = rows_of_four(dlogits, lddl, dtype);
+  const hipError_t e =
+      sg::launch_moe_balance_backward(dtype, p, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail(e, who);
   return ok();
 }

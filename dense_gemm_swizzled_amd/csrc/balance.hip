@@ -1,0 +1,331 @@
+// balance.hip -- the balance loss of expert routing (moe_balance_run) and the
+// gradient of the router's logits (moe_balance_backward_run):
+//
+//   share[t][e] = s[t][e] / sum_e s[t][e]     (s: softmax or sigmoid scores),
+//   load[e]     = E counts[e] / sum_e counts[e],
+//   loss        = sum_e load[e] * (1/n) sum_t share[t][e],
+//
+// over the n tokens that have an expert left; 1 where either side is even.
+#include <hip/hip_runtime.h>
+
+#include "launch.h"
+#include "moe.h"
+#include "moe_rows.h"
+
+namespace sg {
+
+namespace {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr int kSumThreads = 1024;
+constexpr int kGradThreads = 256;
+
+// A token's scores over Lanes lanes with Quads quads of experts each (quad q of
+// the lane: experts from 4 * (q * Lanes + lane)), their sum, and for a sigmoid
+// 1 - s.  A masked logit scores zero; a token with all masked has the sum zero.
+template <int Lanes, int Quads, bool Rest>
+__device__ __forceinline__ float scores(float (&x)[Quads][kHeld], float (&rest)[Quads][kHeld],
+                                        bool soft) {
+  float part = 0.0f;
+  if (soft) {
+    float top = -__builtin_inff();
+#pragma unroll
+    for (int q = 0; q < Quads; ++q) top = OpMax{}(top, lane_top(x[q]));
+    top = lane_reduce<Lanes>(top, OpMax{});
+    if (top == -__builtin_inff()) top = 0.0f;
+#pragma unroll
+    for (int q = 0; q < Quads; ++q)
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) {  // (2^-inf is zero)
+        x[q][i] = __builtin_amdgcn_exp2f((x[q][i] - top) * kLog2e);
+        part += x[q][i];
+      }
+  } else {
+#pragma unroll
+    for (int q = 0; q < Quads; ++q)
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) {
+        const float v = x[q][i], z = expf(-__builtin_fabsf(v)), under = 1.0f / (1.0f + z);
+        x[q][i] = (v < 0 ? z : 1.0f) * under;  // (of -inf: z is zero)
+        if constexpr (Rest) rest[q][i] = (v < 0 ? 1.0f : z) * under;
+        part += x[q][i];
+      }
+  }
+  return lane_reduce<Lanes>(part, OpSum{});
+}
+
+// The loss from the sums S and counts of the experts, one thread each (none
+// from E on); n: the tokens.  In 64 bits, added in a fixed order.
+__device__ __forceinline__ void finish(const BalanceParams& p, float S, int count, int n,
+                                       double (&area)[2][4]) {
+  double dot = (double)S * count, all = count;
+  dot = lane_reduce<64>(dot, OpSum{});
+  all = lane_reduce<64>(all, OpSum{});
+  if ((threadIdx.x & 63) == 0 && threadIdx.x < SG_MAX_GROUPS) {
+    area[0][threadIdx.x >> 6] = dot;
+    area[1][threadIdx.x >> 6] = all;
+  }
+  if ((int)threadIdx.x < p.E) p.counts[threadIdx.x] = count;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    dot = (area[0][0] + area[0][1]) + (area[0][2] + area[0][3]);
+    all = (area[1][0] + area[1][1]) + (area[1][2] + area[1][3]);
+    p.loss[0] = n > 0 && all > 0 ? (float)(p.E * dot / (all * n)) : 0.0f;
+    p.tokens[0] = n;
+  }
+}
+
+// The value of the lane 8 places on in its row of 16, round the end.
+__device__ __forceinline__ float eight_away(float v) {
+  return __builtin_bit_cast(
+      float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x128, 0xf, 0xf, true));
+}
+
+// One workgroup adds up the shares of a run of tokens and counts their ids.  A
+// lane keeps the sums of its experts in registers over its tokens (the next
+// token's logits loading meanwhile), the lanes that hold the same experts are
+// added through LDS in a fixed order, the counts are integers in LDS.  Alone:
+// the only workgroup, which finishes the loss itself.
+template <int DT, int Lanes, int Quads, bool Alone>
+__global__ void __launch_bounds__(kSumThreads) moe_balance_kernel(const BalanceParams p) {
+  constexpr int kTokens = kSumThreads / Lanes, kWaves = kSumThreads / 64;
+  constexpr int kExperts = Lanes * Quads * kHeld;
+  __shared__ __attribute__((aligned(16))) float sums[kWaves][kExperts];
+  __shared__ int counts[SG_MAX_GROUPS + 1];  // the last: tokens
+  __shared__ double area[2][4];
+  const int tid = threadIdx.x, lane = tid % Lanes, slot = tid / Lanes;
+  const bool soft = p.score == SG_SCORE_SOFTMAX;
+  const int64_t first = (int64_t)blockIdx.x * p.chunk, end = min(first + p.chunk, p.T);
+  if (tid <= SG_MAX_GROUPS) counts[tid] = 0;
+  __syncthreads();
+
+  for (int64_t i = first * p.top_k + tid; i < end * p.top_k; i += kSumThreads) {
+    const int id = p.ids[i];
+    if ((uint32_t)id < (uint32_t)p.E) atomicAdd(&counts[id], 1);
+  }
+  float sum[Quads][kHeld] = {}, next[Quads][kHeld];
+  int live = 0;
+  auto load = [&](int64_t t) {
+#pragma unroll
+    for (int q = 0; q < Quads; ++q)
+      load_row4<DT>(p, t, kHeld * (q * Lanes + lane), t < end, next[q]);
+  };
+  load(first + slot);
+  for (int64_t t = first + slot; t - slot < end; t += kTokens) {  // (whole waves go round)
+    float x[Quads][kHeld], none[Quads][kHeld];
+#pragma unroll
+    for (int q = 0; q < Quads; ++q)
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) x[q][i] = next[q][i];
+    if (t - slot + kTokens < end) load(t + kTokens);
+    bool any = false;
+#pragma unroll
+    for (int q = 0; q < Quads; ++q) any |= lane_top(x[q]) > -__builtin_inff();
+    const float total = scores<Lanes, Quads, false>(x, none, soft);
+    const uint64_t who = __ballot(any) >> (tid & 63 & ~(Lanes - 1));
+    live += lane == 0 && (Lanes == 64 ? who : who & ((1ull << (Lanes & 63)) - 1)) ? 1 : 0;
+    const float over = 1.0f / __builtin_fmaxf(total, kTiny);
+#pragma unroll
+    for (int q = 0; q < Quads; ++q)
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) sum[q][i] += x[q][i] * over;
+  }
+  if (live) atomicAdd(&counts[SG_MAX_GROUPS], live);
+#pragma unroll
+  for (int q = 0; q < Quads; ++q) {
+    f32x4 v;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      float s = sum[q][i];
+      if constexpr (Lanes <= 8) s += eight_away(s);
+      if constexpr (Lanes <= 16) s = reduce_step<16>(s, OpSum{});
+      if constexpr (Lanes <= 32) s = reduce_step<32>(s, OpSum{});
+      v[i] = s;
+    }
+    if ((tid & 63) < Lanes)
+      *reinterpret_cast<f32x4*>(&sums[tid >> 6][kHeld * (q * Lanes + lane)]) = v;
+  }
+  __syncthreads();
+  float S = 0.0f;
+  if (tid < kExperts) {
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) S += sums[w][tid];
+  }
+  if constexpr (Alone) {
+    finish(p, tid < p.E ? S : 0.0f, tid < p.E ? counts[tid] : 0, counts[SG_MAX_GROUPS], area);
+  } else {
+    // Pairs (sum, count), then (0, tokens).
+    u32x2* const out = static_cast<u32x2*>(p.part) + (int64_t)blockIdx.x * (p.E + 1);
+    if (tid < p.E) out[tid] = u32x2{__builtin_bit_cast(uint32_t, S), (uint32_t)counts[tid]};
+    if (tid == p.E) out[tid] = u32x2{0u, (uint32_t)counts[SG_MAX_GROUPS]};
+  }
+}
+
+// Adds up the workgroups' pairs, a fixed share of them for each of four threads
+// an expert, and finishes the loss.
+__global__ void __launch_bounds__(kSumThreads) moe_balance_join_kernel(const BalanceParams p) {
+  constexpr int kWide = SG_MAX_GROUPS, kSegs = kSumThreads / kWide;
+  __shared__ float sums[kSegs][kWide];
+  __shared__ int counts[kSegs][kWide], tokens[kSumThreads / 64];
+  __shared__ double area[2][4];
+  const int tid = threadIdx.x, e = tid % kWide, seg = tid / kWide;
+  const u32x2* const part = static_cast<const u32x2*>(p.part);
+  const int pitch = p.E + 1;
+  float S = 0.0f;
+  int count = 0, n = 0;
+  if (e < p.E)
+#pragma unroll 8
+    for (int b = seg; b < p.parts; b += kSegs) {
+      const u32x2 v = part[b * pitch + e];
+      S += __builtin_bit_cast(float, (uint32_t)v[0]);
+      count += (int)v[1];
+    }
+  if (tid < p.parts) n = (int)part[tid * pitch + p.E][1];
+  n = lane_reduce<64>(n, OpSum{});
+  sums[seg][e] = S;
+  counts[seg][e] = count;
+  if ((tid & 63) == 0) tokens[tid >> 6] = n;
+  __syncthreads();
+  S = 0.0f;
+  count = n = 0;
+  if (seg == 0) {
+#pragma unroll
+    for (int i = 0; i < kSegs; ++i) {
+      S += sums[i][e];
+      count += counts[i][e];
+    }
+  }
+#pragma unroll
+  for (int w = 0; w < kSumThreads / 64; ++w) n += tokens[w];
+  finish(p, S, count, n, area);
+}
+
+// With d_e = dloss E counts[e] / (sum counts * n), the gradient of share e:
+//   softmax  dx_e = share_e (d_e - sum_j share_j d_j),
+//   sigmoid  dx_e = share_e (1 - s_e) (d_e - sum_j share_j d_j).
+// Bound by memory: reads the logits, writes their gradient.
+template <int DT, int Lanes, int Quads>
+__global__ void __launch_bounds__(kGradThreads) moe_balance_backward_kernel(
+    const BalanceParams p) {
+  constexpr int kTokens = kGradThreads / Lanes;
+  const int lane = threadIdx.x % Lanes, slot = threadIdx.x / Lanes;
+  const bool soft = p.score == SG_SCORE_SOFTMAX;
+  float d[Quads][kHeld];
+  int64_t all = 0;
+#pragma unroll
+  for (int q = 0; q < Quads; ++q)
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      const int e = kHeld * (q * Lanes + lane) + i;
+      const int c = e < p.E ? p.counts[e] : 0;
+      d[q][i] = (float)c;
+      all += c;
+    }
+  all = lane_reduce<Lanes>(all, OpSum{});
+  const int n = p.tokens[0];
+  const float f = all > 0 && n > 0 ? p.dloss[0] * (float)((double)p.E / ((double)all * n)) : 0.0f;
+#pragma unroll
+  for (int q = 0; q < Quads; ++q)
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) d[q][i] *= f;
+
+  const int64_t step = (int64_t)gridDim.x * kTokens;
+  for (int64_t t = (int64_t)blockIdx.x * kTokens + slot; t - slot < p.T; t += step) {
+    float x[Quads][kHeld], rest[Quads][kHeld];
+#pragma unroll
+    for (int q = 0; q < Quads; ++q)
+      load_row4<DT>(p, t, kHeld * (q * Lanes + lane), t < p.T, x[q]);
+    const float total = scores<Lanes, Quads, true>(x, rest, soft);
+    const float over = 1.0f / __builtin_fmaxf(total, kTiny);
+    float dot = 0.0f;
+#pragma unroll
+    for (int q = 0; q < Quads; ++q)
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) {
+        x[q][i] *= over;
+        dot += x[q][i] * d[q][i];
+      }
+    dot = lane_reduce<Lanes>(dot, OpSum{});
+    if (t >= p.T) continue;
+#pragma unroll
+    for (int q = 0; q < Quads; ++q) {
+      const int e0 = kHeld * (q * Lanes + lane);
+      if (e0 >= p.E) break;
+      f32x4 v;
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i)
+        v[i] = x[q][i] * (soft ? 1.0f : rest[q][i]) * (d[q][i] - dot);
+      store_row4<DT>(p, t, e0, v);
+    }
+  }
+}
+
+constexpr const char* type_label(int dt) {
+  return dt == SG_F32 ? "f32" : dt == SG_BF16 ? "bf16" : "f16";
+}
+constexpr const char* digits(int n) {
+  return n == 1 ? "1" : n == 2 ? "2" : n == 4 ? "4" : n == 8 ? "8" : n == 16 ? "16"
+         : n == 32 ? "32" : "64";
+}
+
+template <int DT, int Lanes, int Quads>
+hipError_t go_sum(const BalanceParams& p, hipStream_t s) {
+  static const char* const name =
+      kernel_label("moe_balance_kernel", type_label(DT), digits(Lanes), digits(Quads));
+  last_kernel() = name;
+  if (p.parts == 1) {
+    hipLaunchKernelGGL((moe_balance_kernel<DT, Lanes, Quads, true>), dim3(1), dim3(kSumThreads),
+                       0, s, p);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL((moe_balance_kernel<DT, Lanes, Quads, false>), dim3(p.parts),
+                     dim3(kSumThreads), 0, s, p);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(moe_balance_join_kernel, dim3(1), dim3(kSumThreads), 0, s, p);
+  return hipGetLastError();
+}
+
+template <int DT, int Lanes, int Quads>
+hipError_t go_grad(const BalanceParams& p, hipStream_t s) {
+  static const char* const name =
+      kernel_label("moe_balance_backward_kernel", type_label(DT), digits(Lanes), digits(Quads));
+  last_kernel() = name;
+  constexpr int kTokens = kGradThreads / Lanes;
+  const int64_t blocks = std::min<int64_t>((p.T + kTokens - 1) / kTokens, 2048);
+  hipLaunchKernelGGL((moe_balance_backward_kernel<DT, Lanes, Quads>), dim3((unsigned)blocks),
+                     dim3(kGradThreads), 0, s, p);
+  return hipGetLastError();
+}
+
+template <int DT>
+hipError_t forward(const BalanceParams& p, hipStream_t s) {
+  if (p.E <= 32) return go_sum<DT, 8, 1>(p, s);
+  if (p.E <= 64) return go_sum<DT, 8, 2>(p, s);
+  if (p.E <= 128) return go_sum<DT, 16, 2>(p, s);
+  return go_sum<DT, 16, 4>(p, s);
+}
+
+template <int DT>
+hipError_t backward(const BalanceParams& p, hipStream_t s) {
+  if (p.E <= 32) return go_grad<DT, 8, 1>(p, s);
+  if (p.E <= 64) return go_grad<DT, 8, 2>(p, s);
+  if (p.E <= 128) return go_grad<DT, 16, 2>(p, s);
+  return go_grad<DT, 16, 4>(p, s);
+}
+
+}  // namespace
+
+hipError_t launch_moe_balance(int dtype, const BalanceParams& p, hipStream_t s) {
+  if (dtype == SG_F32) return forward<SG_F32>(p, s);
+  if (dtype == SG_BF16) return forward<SG_BF16>(p, s);
+  return forward<SG_F16>(p, s);
+}
+
+hipError_t launch_moe_balance_backward(int dtype, const BalanceParams& p, hipStream_t s) {
+  if (dtype == SG_F32) return backward<SG_F32>(p, s);
+  if (dtype == SG_BF16) return backward<SG_BF16>(p, s);
+  return backward<SG_F16>(p, s);
+}
+
+}  // namespace sg

@@ -33,7 +33,8 @@
 
 namespace sg {
 
-template <int BM, bool IsBF16, bool AMn, bool BMn>
+// Epi: what is done with the sums instead of storing D (xent.h), or void.
+template <int BM, bool IsBF16, bool AMn, bool BMn, class Epi = void>
 struct DeepTile {
   static_assert(BM == 64 || BM == 128, "64x64 or 128x128 tiles");
   using Base = GemmTile<BM, BM, IsBF16, AMn, BMn, kSwzDefault, 4>;
@@ -266,6 +267,12 @@ struct DeepTile {
     }
     wait_vmem();  // the loads past K
 
+    if constexpr (!std::is_void<Epi>::value) {
+      PingPongTile<IsBF16, kSwzDefault>::barrier();  // every wave's reads are done
+      Epi::template finish32<kFM, kFN, Base::kWM, Base::kWN, 2>(acc, j, smem, D, ldd, lane, wm,
+                                                                wn);
+      return;
+    }
     if (d_dtype == SG_F32 && C == nullptr) {
       PingPongTile<IsBF16, kSwzDefault>::barrier();  // every wave's reads are done
       store_f32_via_lds(acc, j, smem + wave * kWaveBytes, D, ldd, lane, wm, wn);

@@ -43,6 +43,7 @@ struct DenseParams {
   int tiles_m, tiles_n;
   int group_m;
   ClockTrace clk;
+  const float* alpha_dev = nullptr;  // a factor of alpha in device memory, or NULL
 };
 
 struct GroupedParams {
@@ -79,6 +80,19 @@ __device__ __forceinline__ void raster(int t, int tiles_m, int tiles_n,
   tn = local / gm;
 }
 
+// What the epilogues of the cross entropy (xent.h) take besides the tile's
+// sums.
+struct XentJob {
+  const void* targets;  // one per token (row of the product)
+  bool wide;            // 64-bit targets
+  float* part;          // [M][2]: maximum and sum of the tile's columns
+  float* zt;            // [M]: the targets' logits
+  const float* rows;    // [M][4]: a token's terms of the gradient
+  int64_t words;        // words of the vocabulary (targets outside are none)
+  int64_t col0;         // the word of the tile's first column
+  int64_t n_store;      // columns of the gradient that are written (>= n_valid)
+};
+
 // Where one workgroup's operand panels and output tile live.
 struct TileJob {
   const char* a;        // A panel base (see loaders for the addressing)
@@ -100,6 +114,7 @@ struct TileJob {
   int a_total;          // rows of A (with `rows`)
   bool vec;             // D's rows are 16-byte aligned
   bool past;            // a 16-bit D is stored past the caches (256x256 tiles)
+  XentJob x;            // the cross entropy's epilogues only
 };
 
 // Epilogue element work shared by every kernel.  One chunk is 4 consecutive
@@ -634,15 +649,20 @@ __device__ __forceinline__ TileJob dense_tile_job(const DenseParams& p, int wg) 
   j.m_valid = (int)min<int64_t>(BM, p.M - m0);
   j.n_valid = (int)min<int64_t>(BN, p.N - n0);
   // Each buffer covers exactly the bytes the tile may read: up to the end of
-  // its last valid row (K-major) or of row K-1 (MN-major).
+  // its last valid row (K-major) or of row K-1 (MN-major), and for A of the
+  // 16-byte chunk that holds the row's last value: the range check drops a
+  // dword that is not whole.  (The chunk lies in the row's pitch and crosses no
+  // page.  What it holds past M is not stored, past K it has to be zero.)
   if constexpr (AMn) {  // A stored [K][lda], M contiguous
     j.a = static_cast<const char*>(p.A) + m0 * es;
     j.a_pitch = (uint32_t)(p.lda * es);
-    j.a_bytes = p.K > 0 ? (uint32_t)((p.K - 1) * p.lda * es + (p.M - m0) * es) : 0u;
+    j.a_bytes =
+        p.K > 0 ? (uint32_t)((p.K - 1) * p.lda * es + (((p.M - m0) * es + 15) & ~15)) : 0u;
   } else {              // A stored [M][lda], K contiguous
     j.a = static_cast<const char*>(p.A) + m0 * p.lda * es;
     j.a_pitch = (uint32_t)(p.lda * es);
-    j.a_bytes = p.K > 0 ? (uint32_t)((j.m_valid - 1) * p.lda * es + p.K * es) : 0u;
+    j.a_bytes =
+        p.K > 0 ? (uint32_t)((j.m_valid - 1) * p.lda * es + ((p.K * es + 15) & ~15)) : 0u;
   }
   if constexpr (BMn) {  // B stored [K][ldb], N contiguous
     j.b = static_cast<const char*>(p.B) + n0 * es;
@@ -654,7 +674,7 @@ __device__ __forceinline__ TileJob dense_tile_job(const DenseParams& p, int wg) 
     j.b_bytes = p.K > 0 ? (uint32_t)((j.n_valid - 1) * p.ldb * es + p.K * es) : 0u;
   }
   j.ldc = p.ldc;
-  j.alpha = p.alpha;
+  j.alpha = p.alpha_dev ? p.alpha * *p.alpha_dev : p.alpha;
   j.beta = p.beta;
   j.d_row0 = m0;
   j.n0 = n0;

@@ -13,6 +13,27 @@ namespace sg {
 
 // Tile shapes the planner chooses between.
 enum TileShape { kTile256 = 0, kTile128 = 1, kTile64 = 2 };
+
+constexpr int kCUs = 256;  // MI355X compute units
+
+// Dense GEMM: 256x256 tiles when they fill the CUs, else 128x128 tiles when
+// they fill half of them, else 64x64 tiles (small problems: 1024^3 has 64
+// tiles of 128 but 256 of 64).  Between those, when the 256x256 tiles would
+// run on the ping-pong (`pingpong`: K-major operands, or a K that its loaders
+// of MN-major operands take) and the 128x128 tiles would need three or more
+// rounds of the CUs, one partial round of the ping-pong is faster (bf16 on
+// MI355X, TFLOP/s 256 vs 128 tiles: 3072^3 1056 vs 694, 3584^3 1337 vs 911,
+// 3072x3072x1024 846 vs 585), though not against one or two rounds of 128x128
+// tiles (2560^3 753 vs 847, 2048x4096x4096 934 vs 1041).
+// `fits256`: 256-row panels stay within 32-bit buffer offsets.
+inline TileShape pick_dense_tile(int64_t M, int64_t N, bool pingpong, bool fits256) {
+  auto tiles = [&](int64_t side) { return ((M + side - 1) / side) * ((N + side - 1) / side); };
+  if (tiles(256) >= kCUs) return kTile256;
+  if (pingpong && fits256 && (tiles(128) + kCUs - 1) / kCUs >= 3) return kTile256;
+  if (tiles(128) >= kCUs / 2) return kTile128;
+  return kTile64;
+}
+
 // The kernels of the 8-bit products (i8_kernels.h), named by rows x columns of
 // a tile.  kI8Stream32x32: one workgroup a CU with five stages;
 // kI8Stream32x32x2: two with two.
@@ -23,6 +44,7 @@ enum I8Tile {
 struct I8Params;
 struct RouteParams;
 struct PlanParams;
+struct BalanceParams;
 
 // A grid of `blocks` workgroups over x and y: a launch has fewer than 2^32
 // threads along x.  The kernel's block index is block_index().
@@ -56,6 +78,11 @@ const char* kernel_label(const char* name, Parts... parts) {
 // launch status.
 hipError_t launch_dense(TileShape tile, bool bf16, bool a_mn, bool b_mn,
                         const DenseParams& p, hipStream_t s);
+// The same where an operand is MN-major and K any: 256x256 tiles run the
+// ping-pong from K = 65 on.  A K-major A then holds zeros from K up to the next
+// multiple of 64.
+hipError_t launch_dense_any_k(TileShape tile, bool bf16, bool a_mn, bool b_mn,
+                              const DenseParams& p, hipStream_t s);
 // The layout ablation: bf16, K-major operands, 256x256 tiles on the 32x32x16
 // ping-pong kernel with the LDS layout swz (0, 8 or 16 units per line).
 hipError_t launch_layout(int swz, const DenseParams& p, hipStream_t s);
@@ -83,6 +110,9 @@ hipError_t launch_i8_quant(const void* X, int64_t R, int64_t K, int64_t ldx, int
 hipError_t launch_moe_route(int dtype, const RouteParams& p, hipStream_t s);
 hipError_t launch_moe_route_backward(int dtype, const RouteParams& p, hipStream_t s);
 hipError_t launch_moe_plan(const PlanParams& p, hipStream_t s);
+// The routing's balance loss (balance.hip).
+hipError_t launch_moe_balance(int dtype, const BalanceParams& p, hipStream_t s);
+hipError_t launch_moe_balance_backward(int dtype, const BalanceParams& p, hipStream_t s);
 // The MFMA clock probe (diag.hip): one wave per SIMD of 256 CUs.
 int clock_probe_waves();
 hipError_t launch_clock_probe(int64_t iters, void* out, hipStream_t s);

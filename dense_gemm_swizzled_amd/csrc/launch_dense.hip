@@ -136,6 +136,29 @@ hipError_t launch_dense(TileShape tile, bool bf16, bool a_mn, bool b_mn,
   return dense_by_dtype<64, 64, 16>(bf16, a_mn, b_mn, p, s);
 }
 
+namespace {
+
+template <bool BF, bool AMn>
+hipError_t go_tail(const DenseParams& p, hipStream_t s) {
+  static const char* const name =
+      kernel_label("pingpong16_gemm_kernel", dt_name(BF), mj_name(AMn), mj_name(true), "tail");
+  last_kernel() = name;
+  hipLaunchKernelGGL((pingpong16_gemm_kernel<BF, kSwzDefault, AMn, true, true, true>),
+                     dim3(p.tiles_m * p.tiles_n), dim3(512), 0, s, p);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_dense_any_k(TileShape tile, bool bf16, bool a_mn, bool b_mn,
+                              const DenseParams& p, hipStream_t s) {
+  if (tile == kTile256 && b_mn && p.K > 64 && p.K % 64) {
+    if (a_mn) return bf16 ? go_tail<true, true>(p, s) : go_tail<false, true>(p, s);
+    return bf16 ? go_tail<true, false>(p, s) : go_tail<false, false>(p, s);
+  }
+  return launch_dense(tile, bf16, a_mn, b_mn, p, s);
+}
+
 hipError_t launch_layout(int swz, const DenseParams& p, hipStream_t s) {
   if (swz == 16) return go_pingpong32<16>(p, s);
   if (swz == 8) return go_pingpong32<8>(p, s);

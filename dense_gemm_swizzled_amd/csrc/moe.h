@@ -25,6 +25,25 @@ struct RouteParams {
   int64_t lddl;
 };
 
+struct BalanceParams {
+  int64_t T;
+  int E, top_k;
+  const void* logits;       // [T][ldl]
+  int64_t ldl;
+  int score;
+  bool vec, vec_d;          // as above
+  int64_t chunk;            // tokens of one workgroup (forward)
+  const int32_t* ids;       // [T][top_k] (forward)
+  float* loss;              // [1] (forward)
+  int32_t* counts;          // [E]; read by the backward pass
+  int32_t* tokens;          // [1]; read by the backward pass
+  void* part;               // workspace: [workgroups][E + 1] pairs
+  int parts;                // workgroups
+  const float* dloss;       // [1] (backward)
+  void* dlogits;            // [T][lddl] of the logits' type (backward)
+  int64_t lddl;
+};
+
 struct PlanParams {
   int64_t P;                // pairs
   int E, top_k;

@@ -39,9 +39,11 @@ namespace sg {
 // of the layout ablation); Swz is the operands' layout.  Elem: the element
 // type; for kElemI8 K and the offsets along it count pairs of elements, so
 // that a K tile is the same 128 bytes.  Rows: A's rows are gathered (TileJob
-// `rows`).
+// `rows`).  Epi: what is done with the sums instead of storing D (xent.h), or
+// void.  Tail: MN-major operands with any K of two K tiles or more; a K-major
+// operand's rows then hold zeros from K up to the next multiple of 64.
 template <int Elem, int Swz, bool AMn = false, bool BMn = false, bool OutSwz = true,
-          bool Rows = false>
+          bool Rows = false, class Epi = void, bool Tail = false>
 struct PingPong16Tile {
   using PP = PingPongTile<Elem, Swz>;
   using ALoader = typename std::conditional<Rows, RowsHalfLoader<Swz>, HalfLoader<Swz>>::type;
@@ -125,6 +127,19 @@ struct PingPong16Tile {
       const int col = (int)(lbyte >> 1);
       x.voff[q] = col < cols ? k * pitch + 2u * (uint32_t)(128 * g + col) : kOutOfRange;
     }
+  }
+
+  // The loader of the last K tile of an MN-major operand whose K ends inside
+  // it (Tail): the K position `soff` moves from the SGPR offset, which the
+  // range check may leave out, into the lane's own, so that rows past K, which
+  // start past the descriptor's records, read as zero.
+  __device__ __forceinline__ static KExactHalfLoader<Swz> last_tile(
+      const KExactHalfLoader<Swz>& x, uint32_t soff) {
+    KExactHalfLoader<Swz> y;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      y.voff[q] = x.voff[q] == kOutOfRange ? kOutOfRange : x.voff[q] + soff;
+    return y;
   }
 
   __device__ __forceinline__ static void read(Frags& f, const char* at, const char* bt,
@@ -350,13 +365,27 @@ struct PingPong16Tile {
     if (g) PP::barrier();  // group 1 runs one phase behind group 0
     int bs = 0;            // t mod 3
     int t = 0;
-    for (; t + 2 < T; ++t) {
+    for (; t + (Tail ? 3 : 2) < T; ++t) {
       ktile<Active, false>(acc, t, bs, la, ra, (uint32_t)(t + 1) * kstep_a, lb, rb,
                            (uint32_t)(t + 2) * kstep_b, la, ra0, a_ring, b_ring, a_rd, b_rd, o,
                            w4);
       bs = bs == 2 ? 0 : bs + 1;
     }
-    if constexpr (LdsC) {
+    if constexpr (Tail) {  // (without a C in LDS): tile T - 3 loads B of the
+                           // last tile, T - 2 its A
+      const uint32_t ka = (uint32_t)(T - 1) * kstep_a, kb = (uint32_t)(T - 1) * kstep_b;
+      for (; t < T; ++t) {
+        KExactHalfLoader<Swz> ta = la, tb = lb;
+        if (AMn && t + 2 == T) ta = last_tile(la, ka);
+        if (BMn && t + 3 == T) tb = last_tile(lb, kb);
+        const u32x4 rat = t + 1 < T ? ra : ra0, rbt = t + 2 < T ? rb : rb0;
+        ktile<Active, false>(acc, t, bs, ta, rat,
+                             AMn && t + 2 == T ? 0u : (uint32_t)(t + 1) * kstep_a, tb, rbt,
+                             BMn && t + 3 == T ? 0u : (uint32_t)(t + 2) * kstep_b, la, ra0,
+                             a_ring, b_ring, a_rd, b_rd, o, w4);
+        bs = bs == 2 ? 0 : bs + 1;
+      }
+    } else if constexpr (LdsC) {
       CBlock cb;
       cb.init(j, C, g, w4, lane);
       ktile<Active, false>(acc, t, bs, la, ra, (uint32_t)(t + 1) * kstep_a, cb.quarter(0),
@@ -593,7 +622,10 @@ struct PingPong16Tile {
     const bool kexact = AMn || BMn || (K & (kBK - 1)) == 0;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      if constexpr (BMn) {
+      if constexpr (BMn && Tail) {  // (T may be 2: tile 1 may be the last)
+        const KExactHalfLoader<Swz> x = last_tile(xbm, t * kstep_b);
+        load_half(x, rb, b_ring + t * kTileBytes, w4, 0u);
+      } else if constexpr (BMn) {
         xbm.template issue<0>(rb, b_ring + t * kTileBytes, w4, t * kstep_b);
         xbm.template issue<1>(rb, b_ring + t * kTileBytes, w4, t * kstep_b);
         xbm.template issue<2>(rb, b_ring + t * kTileBytes, w4, t * kstep_b);
@@ -635,7 +667,7 @@ struct PingPong16Tile {
     // with at most 128 valid rows) runs the mainloop without its MFMAs.
     // A 16-bit C comes in through the last two K tiles' loads when K is a
     // multiple of 64 and 128 C rows stay within 32-bit buffer offsets.
-    const bool ldsc = kexact && T >= 2 && C != nullptr &&
+    const bool ldsc = !Tail && kexact && T >= 2 && C != nullptr &&
                       (c_dtype == SG_BF16 || c_dtype == SG_F16) && j.ldc <= (int64_t{1} << 22);
     if (kexact) {
       KExactHalfLoader<Swz> xa, xb;
@@ -670,6 +702,11 @@ struct PingPong16Tile {
       epilogue_i8(acc, j, smem, T, D, d_dtype, ldd, lane, g, w4, a_rows > 0, sc);
       return;
     }
+    if constexpr (!std::is_void<Epi>::value) {
+      PP::barrier();  // every fragment read is done: the ring is free
+      Epi::template finish16<PingPong16Tile>(acc, j, smem, T, D, ldd, lane, g, w4);
+      return;
+    }
 
     // Through LDS: a 16-bit C that came in with the last loads, and a 16-bit
     // D.  Every fragment read is done once all waves pass the barrier, and
@@ -687,9 +724,10 @@ struct PingPong16Tile {
   }
 };
 
-template <bool IsBF16, int Swz, bool AMn = false, bool BMn = false, bool OutSwz = true>
+template <bool IsBF16, int Swz, bool AMn = false, bool BMn = false, bool OutSwz = true,
+          bool Tail = false>
 __global__ void __launch_bounds__(512, 1) pingpong16_gemm_kernel(const DenseParams p) {
-  using Tile = PingPong16Tile<IsBF16, Swz, AMn, BMn, OutSwz>;
+  using Tile = PingPong16Tile<IsBF16, Swz, AMn, BMn, OutSwz, false, void, Tail>;
   __shared__ __attribute__((aligned(4096))) char smem[Tile::kLdsBytes];
   const ClockStamp cs = clock_begin(p.clk);
   const TileJob j = dense_tile_job<256, 256, AMn, BMn>(p, blockIdx.x);

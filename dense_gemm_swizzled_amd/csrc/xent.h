@@ -1,0 +1,313 @@
+// xent.h -- softmax cross entropy over a vocabulary as epilogues of the 16-bit
+// product z = alpha * A.B^T (A: tokens, B: one row per word):
+//
+//   lse[m] = log sum_n exp z[m][n],   loss[m] = lse[m] - z[m][t[m]],
+//   g[m][n] = alpha * ((dloss[m] + dlse[m]) exp(z[m][n] - lse[m])
+//                      - dloss[m] [n = t[m]]),   dA = g B,   dB = g^T A.
+//
+// The logits never leave the registers they were summed in.  Forward, a tile
+// reduces each of its rows to the maximum and the sum of exponentials of its
+// columns (XentStats), and a second kernel joins the tiles of a row in a fixed
+// order.  Backward, the product runs again, its epilogue turns the logits into
+// g in 16 bits (XentGrad) a run of words at a time, and two products of the
+// library's own kernels take g to dA and dB.
+#pragma once
+
+#include "deep64.h"
+#include "lane_ops.h"
+#include "pingpong16.h"
+
+namespace sg {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
+struct XentParams {
+  DenseParams d;   // the product (D: the gradient's workspace)
+  XentJob x;       // pointers to row 0, column 0
+  int64_t col0;    // the word of column 0
+};
+
+// What the join of a row's tiles and the gradient's preparation read.
+struct XentRows {
+  int64_t M, N;
+  float alpha;
+  const void* targets;
+  bool wide;
+  const float* part;   // [tiles][M][2]
+  const float* zt;     // [M]
+  int tiles;
+  float* loss;
+  float* lse;          // written by the join, read by the preparation
+  const float* dloss;
+  const float* dlse;   // or NULL
+  float* rows;         // [M][4]
+  float* scale;        // [1]: the factor that undoes the gradient's scale
+  bool scaled;
+};
+
+__device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Token m's target, -1 where it is no word of [0, N).
+__device__ __forceinline__ int target_of(const void* t, bool wide, int64_t m, int64_t N) {
+  const int64_t v = wide ? static_cast<const int64_t*>(t)[m]
+                         : (int64_t) static_cast<const int32_t*>(t)[m];
+  return v >= 0 && v < N ? (int)v : -1;
+}
+
+// (maximum, sum of exp(z - maximum)) of two sets of logits from those of each.
+// A set without a finite logit has the maximum -inf and the sum 0, or NaN.
+__device__ __forceinline__ void join_stats(float& m, float& s, float m2, float s2) {
+  const float top = __builtin_fmaxf(m, m2);
+  const float base = top == -__builtin_inff() ? 0.0f : top;
+  s = s * exp2_of((m - base) * kLog2e) + s2 * exp2_of((m2 - base) * kLog2e);
+  m = top;
+}
+
+// Forward.
+struct XentStats {
+  // The maximum and sum of NV logits that lanes S apart (Steps) share a row of.
+  template <int NV, bool Four>
+  __device__ __forceinline__ static void reduce(const float (&v)[NV], float& m, float& s) {
+    m = v[0];
+#pragma unroll
+    for (int e = 1; e < NV; ++e) m = __builtin_fmaxf(m, v[e]);
+    if constexpr (Four) m = reduce_step<16>(m, OpMax{});
+    m = reduce_step<32>(m, OpMax{});
+    const float base = m == -__builtin_inff() ? 0.0f : m;
+    s = 0.0f;
+#pragma unroll
+    for (int e = 0; e < NV; ++e) s += exp2_of((v[e] - base) * kLog2e);
+    if constexpr (Four) s = reduce_step<16>(s, OpSum{});
+    s = reduce_step<32>(s, OpSum{});
+  }
+
+  // Joins the waves' columns of each row (area: [waves][rows][2] floats) and
+  // writes the tile's pair.
+  template <int Waves, int Rows>
+  __device__ __forceinline__ static void write(const TileJob& j, const float* area) {
+    __syncthreads();
+    const int r = threadIdx.x;
+    if (r >= Rows || r >= j.m_valid) return;
+    float m = area[2 * r], s = area[2 * r + 1];
+#pragma unroll
+    for (int w = 1; w < Waves; ++w)
+      join_stats(m, s, area[2 * (w * Rows + r)], area[2 * (w * Rows + r) + 1]);
+    *reinterpret_cast<float2*>(j.x.part + 2 * (int64_t)r) = make_float2(m, s);
+  }
+
+  // The column, inside the tile, of the target of tile row ml (or below 0, or
+  // past the tile).
+  __device__ __forceinline__ static int column(const TileJob& j, int ml) {
+    const int64_t t = (int64_t)target_of(j.x.targets, j.x.wide, min(ml, j.m_valid - 1),
+                                         j.x.words) - j.x.col0;
+    return t >= 0 && t < 256 ? (int)t : -1;
+  }
+
+  // Lane l of block (i, jn) holds row 128g + 16i + l%16, columns 64 w4 + 16 jn
+  // + 4(l/16) .. +3.
+  template <class Tile>
+  __device__ __forceinline__ static void finish16(f32x4 (&acc)[Tile::kI][Tile::kJ],
+                                                  const TileJob& j, char* smem, int, void*,
+                                                  int64_t, int lane, int g, int w4) {
+    float* area = reinterpret_cast<float*>(smem);
+    const int c0 = 64 * w4 + 4 * (lane >> 4);
+    if (j.m_valid > 128 * g) {
+      int tc[Tile::kI];
+#pragma unroll
+      for (int i = 0; i < Tile::kI; ++i) tc[i] = column(j, 128 * g + 16 * i + (lane & 15));
+#pragma unroll
+      for (int i = 0; i < Tile::kI; ++i) {
+        const int ml = 128 * g + 16 * i + (lane & 15);
+        float v[4 * Tile::kJ];
+#pragma unroll
+        for (int jn = 0; jn < Tile::kJ; ++jn)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[4 * jn + e] = acc[i][jn][e] * j.alpha;
+        if (j.n_valid < 256) {
+#pragma unroll
+          for (int e = 0; e < 4 * Tile::kJ; ++e)
+            if (c0 + 16 * (e >> 2) + (e & 3) >= j.n_valid) v[e] = -__builtin_inff();
+        }
+        const int at = tc[i] - c0;  // 16 jn + e of the target
+        if (at >= 0 && at < 64 && (at & 12) == 0 && ml < j.m_valid) {
+          float z = 0.0f;
+#pragma unroll
+          for (int e = 0; e < 4 * Tile::kJ; ++e)
+            if (at == 16 * (e >> 2) + (e & 3)) z = v[e];
+          j.x.zt[ml] = z;
+        }
+        float m, s;
+        reduce<4 * Tile::kJ, true>(v, m, s);
+        if (lane < 16) *reinterpret_cast<float2*>(area + 2 * (256 * w4 + ml)) = make_float2(m, s);
+      }
+    }
+    write<4, 256>(j, area);
+  }
+
+  // Lane l of block (fm, fn) holds row WM wm + 32 fm + l%32, columns WN wn +
+  // 32 fn + 8q + 4(l/32) .. +3 in registers 4q .. 4q+3.
+  template <int FM, int FN, int WM, int WN, int WavesN>
+  __device__ __forceinline__ static void finish32(f32x16 (&acc)[FM][FN], const TileJob& j,
+                                                  char* smem, void*, int64_t, int lane, int wm,
+                                                  int wn) {
+    constexpr int kRows = 2 * WM;
+    float* area = reinterpret_cast<float*>(smem);
+    const int c0 = WN * wn + 4 * (lane >> 5);
+#pragma unroll
+    for (int fm = 0; fm < FM; ++fm) {
+      const int ml = WM * wm + 32 * fm + (lane & 31);
+      float v[16 * FN];
+#pragma unroll
+      for (int fn = 0; fn < FN; ++fn)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          v[16 * fn + r] = acc[fm][fn][r] * j.alpha;
+          if (c0 + 32 * fn + 8 * (r >> 2) + (r & 3) >= j.n_valid)
+            v[16 * fn + r] = -__builtin_inff();
+        }
+      const int at = column(j, ml) - c0;
+      if (at >= 0 && at < WN && (at & 4) == 0 && ml < j.m_valid) {
+        float z = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 16 * FN; ++e)
+          if (at == 32 * (e >> 4) + 8 * ((e >> 2) & 3) + (e & 3)) z = v[e];
+        j.x.zt[ml] = z;
+      }
+      float m, s;
+      reduce<16 * FN, false>(v, m, s);
+      if (lane < 32)
+        *reinterpret_cast<float2*>(area + 2 * (kRows * wn + ml)) = make_float2(m, s);
+    }
+    write<WavesN, kRows>(j, area);
+  }
+};
+
+// Backward: the logits of a tile become the gradient in 16 bits.  Each value
+// is rounded once, by at most half a step of its own size: what that adds to a
+// sum over the vocabulary or the tokens is below the rounding of dA and dB.
+template <int DD>
+struct XentGrad {
+  // Row terms: log2(e) lse, the factor of the softmax, what the target's column
+  // loses, the target (the factors are zero for a token without a loss).
+  struct Row {
+    float l2, p, t;
+    int at;
+  };
+  __device__ __forceinline__ static Row row_of(const TileJob& j, int ml) {
+    const f32x4 r = *reinterpret_cast<const f32x4*>(j.x.rows + 4 * (int64_t)min(ml, j.m_valid - 1));
+    const int t = __builtin_bit_cast(int, (float)r[3]);
+    const int64_t at = (int64_t)t - j.x.col0;
+    return {r[0], r[1], r[2], t >= 0 && at >= 0 && at < 256 ? (int)at : -1};
+  }
+  __device__ __forceinline__ static float value(float acc, float k, const Row& r) {
+    return r.p * exp2_of(__builtin_fmaf(acc, k, -r.l2));
+  }
+
+  template <class Tile>
+  __device__ __forceinline__ static void finish16(f32x4 (&acc)[Tile::kI][Tile::kJ],
+                                                  const TileJob& j, char* smem, int T, void* D,
+                                                  int64_t ldd, int lane, int g, int w4) {
+    if (j.m_valid <= 128 * g) return;
+    const int c0 = 64 * w4 + 4 * (lane >> 4);
+    const float k = j.alpha * kLog2e;
+    Row r[Tile::kI];
+#pragma unroll
+    for (int i = 0; i < Tile::kI; ++i) r[i] = row_of(j, 128 * g + 16 * i + (lane & 15));
+#pragma unroll
+    for (int i = 0; i < Tile::kI; ++i) {
+#pragma unroll
+      for (int jn = 0; jn < Tile::kJ; ++jn)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][jn][e] = value(acc[i][jn][e], k, r[i]);
+      const int at = r[i].at - c0;
+      if (at >= 0 && at < 64 && (at & 12) == 0) {
+#pragma unroll
+        for (int jn = 0; jn < Tile::kJ; ++jn)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (at == 16 * jn + e) acc[i][jn][e] -= r[i].t;
+      }
+      if (j.n_valid < 256) {
+#pragma unroll
+        for (int jn = 0; jn < Tile::kJ; ++jn)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (c0 + 16 * jn + e >= j.n_valid) acc[i][jn][e] = 0.0f;
+      }
+    }
+    TileJob out = j;
+    out.alpha = 1.0f;
+    out.n_valid = j.x.n_store;
+    char* cq[4];
+    cblock_quarters(cq, smem, T, g, Tile::kTileBytes, Tile::kHalfBytes);
+    Tile::template epilogue_lds_t<SG_NONE, DD>(acc, out, cq, D, ldd, lane, g, w4);
+  }
+
+  template <int FM, int FN, int WM, int WN, int WavesN>
+  __device__ __forceinline__ static void finish32(f32x16 (&acc)[FM][FN], const TileJob& j, char*,
+                                                  void* D, int64_t ldd, int lane, int wm,
+                                                  int wn) {
+    const int c0 = WN * wn + 4 * (lane >> 5);
+    const float k = j.alpha * kLog2e;
+    const u32x2 none{};
+#pragma unroll
+    for (int fm = 0; fm < FM; ++fm) {
+      const int ml = WM * wm + 32 * fm + (lane & 31);
+      if (ml >= j.m_valid) continue;
+      const Row r = row_of(j, ml);
+      const int at = r.at - c0;
+#pragma unroll
+      for (int fn = 0; fn < FN; ++fn)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int n = 32 * fn + 8 * q;
+          if (c0 + n >= j.x.n_store) continue;
+          f32x4 v;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            v[e] = value(acc[fm][fn][4 * q + e], k, r);
+            if (at == n + e) v[e] -= r.t;
+            if (c0 + n + e >= j.n_valid) v[e] = 0.0f;
+          }
+          store_d_chunk<SG_NONE, DD>(v, none, D, (j.d_row0 + ml) * ldd + j.n0 + c0 + n, 1.0f,
+                                     0.0f);
+        }
+    }
+  }
+};
+
+template <int BM>
+__device__ __forceinline__ TileJob xent_job(const XentParams& p, int wg) {
+  TileJob j = dense_tile_job<BM, BM, false, false>(p.d, wg);
+  const int64_t m0 = j.d_row0;
+  j.x = p.x;
+  j.x.col0 = p.col0 + j.n0;
+  j.x.targets = static_cast<const char*>(p.x.targets) + m0 * (p.x.wide ? 8 : 4);
+  j.x.part = p.x.part + 2 * ((j.n0 / BM) * p.d.M + m0);
+  j.x.zt = p.x.zt + m0;
+  j.x.rows = p.x.rows + 4 * m0;
+  j.x.n_store = (int)min<int64_t>(BM, p.x.n_store - j.n0);
+  return j;
+}
+
+template <bool BF, class Epi>
+__global__ void __launch_bounds__(512, 1) xent_pingpong_kernel(const XentParams p) {
+  using Tile = PingPong16Tile<BF, kSwzDefault, false, false, true, false, Epi>;
+  __shared__ __attribute__((aligned(4096))) char smem[Tile::kLdsBytes];
+  const ClockStamp cs = clock_begin(p.d.clk);
+  const TileJob j = xent_job<256>(p, blockIdx.x);
+  Tile::run(smem, j, p.d.K, nullptr, SG_NONE, p.d.D, p.d.d_dtype, p.d.ldd);
+  clock_end(p.d.clk, cs);
+}
+
+template <int BM, bool BF, class Epi>
+__global__ void __launch_bounds__(256, 1) xent_deep_kernel(const XentParams p) {
+  using Tile = DeepTile<BM, BF, false, false, Epi>;
+  __shared__ __attribute__((aligned(4096))) char smem[Tile::kLdsBytes];
+  const ClockStamp cs = clock_begin(p.d.clk);
+  const TileJob j = xent_job<BM>(p, blockIdx.x);
+  Tile::run(smem, j, p.d.K, nullptr, SG_NONE, p.d.D, p.d.d_dtype, p.d.ldd);
+  clock_end(p.d.clk, cs);
+}
+
+}  // namespace sg

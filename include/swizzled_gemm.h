@@ -63,6 +63,9 @@ extern "C" {
 #define SG_E2M3 7 /* OCP FP6 E2M3 (bias 1, max 7.5, no infinity or NaN) */
 #define SG_E3M2 8 /* OCP FP6 E3M2 (bias 3, max 28, no infinity or NaN) */
 
+#define SG_I32 9  /* 32-bit and 64-bit integers (targets of the cross entropy) */
+#define SG_I64 10
+
 /* Layouts of the e8m0 scale arrays of the block-scaled GEMMs. */
 #define SG_SF_ROWS 0   /* [rows][K/32]: row r's byte b at r * (K/32) + b */
 #define SG_SF_BLOCKS 1 /* 1 KiB blocks of 64 rows x 16 bytes, see mx_scales_to_blocks */
@@ -447,6 +450,110 @@ int moe_plan_run(int64_t T, int E, int top_k, const int32_t* ids, int32_t* offse
 /* Bytes of workspace that moe_plan_run needs for P pairs (host only), or
  * SG_ERR_SHAPE (negative). */
 int64_t moe_plan_workspace_bytes(int64_t P, int E);
+
+/*
+ * moe_balance_run -- how evenly a router spreads its tokens over its experts
+ * (the auxiliary loss of its training), and the tokens of each expert:
+ *   share[t][e] = s[t][e] / sum_e s[t][e],  s the scores of moe_route_run (a
+ *                 masked logit scores 0; the sum is at least 2^-126),
+ *   counts[e]   = the pairs of ids that name e,
+ *   loss        = sum_e (E * counts[e] / sum counts) * (1/n) sum_t share[t][e],
+ * n the tokens with a logit that is not masked.  1 for an even load, E where all
+ * goes to one expert; 0 without a token or a pair.
+ *   logits   [T][ldl] of dtype (SG_F32, SG_BF16, SG_F16), any ldl >= E.
+ *   ids      int32 [T][top_k] as moe_route_run writes them; those outside
+ *            [0, E) are not counted.
+ *   loss     fp32 [1];  counts  int32 [E];  tokens  int32 [1]: n.
+ *   workspace  DEVICE, moe_balance_workspace_bytes(T, E) bytes, 16-byte aligned
+ *            (0 bytes up to 256 tokens: may be NULL).  It holds nothing between
+ *            calls; calls that may run at the same time need their own.
+ * Sums are added in a fixed order.  T = 0 writes zeros.  E is 1..SG_MAX_GROUPS,
+ * top_k 1..min(E, SG_MAX_TOP_K), T * top_k below 2^31.  Errors: SG_ERR_NULL,
+ * SG_ERR_ALIGN, SG_ERR_SHAPE, SG_ERR_DTYPE, SG_ERR_HIP.
+ */
+int moe_balance_run(int64_t T, int E, int top_k, const void* logits, int64_t ldl, int dtype,
+                    const int32_t* ids, int score, float* loss, int32_t* counts,
+                    int32_t* tokens, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that moe_balance_run needs (host only), or SG_ERR_SHAPE. */
+int64_t moe_balance_workspace_bytes(int64_t T, int E);
+
+/*
+ * moe_balance_backward_run -- the gradient of the logits from that of
+ * moe_balance_run's loss, the counts held fixed.
+ *   dloss    DEVICE fp32 [1];  counts, tokens  as moe_balance_run wrote them
+ *            (counts added up over several calls, with their tokens, give the
+ *            gradient of the loss over all of them).
+ *   dlogits  [T][lddl] of the logits' type, E values a row: all written, zero
+ *            for masked logits.
+ * score is the forward call's.  Errors as there.
+ */
+int moe_balance_backward_run(int64_t T, int E, const float* dloss, const void* logits,
+                             int64_t ldl, int dtype, const int32_t* counts,
+                             const int32_t* tokens, int score, void* dlogits, int64_t lddl,
+                             void* stream);
+
+/*
+ * gemm_xent_run -- softmax cross entropy over a vocabulary of N words for M
+ * tokens, without keeping the logits z = alpha * A*B:
+ *   z[m][n] = alpha * sum_k A[m][k] * B[n][k]  (fp32 accumulation),
+ *   lse[m]  = log sum_n exp z[m][n],
+ *   loss[m] = lse[m] - z[m][targets[m]], or 0 where targets[m] lies outside
+ *             [0, N) (a token without a target: padding, a prompt).
+ * A token with a logit of NaN or +inf has lse = loss = NaN (0 without a
+ * target); logits of -inf count as probability 0.  N = 0 gives lse = -inf.
+ *   A        ab_dtype (SG_F16, SG_BF16) [M][lda], K values a row.
+ *   B        ab_dtype [N][ldb], K values a row: a word each.
+ *   targets  [M] of target_dtype (SG_I32, SG_I64).
+ *   loss, lse  fp32 [M].
+ *   K        a multiple of 8; lda, ldb multiples of 8 below 2^22; A and B
+ *            16-byte aligned.  N and M may be any.
+ *   workspace  DEVICE, gemm_xent_workspace_bytes(M, N, K) bytes, 16-byte
+ *            aligned: two floats for each token and column tile (8192 tokens,
+ *            131072 words: 34 MB, where the logits would be 4.3 GB).  It holds
+ *            nothing between calls; calls that may run at the same time need
+ *            their own.
+ * The result depends on nothing but the arguments (no atomics).  Errors:
+ * SG_ERR_NULL, SG_ERR_ALIGN, SG_ERR_SHAPE (also 2^23 tiles or more),
+ * SG_ERR_DTYPE, SG_ERR_HIP.
+ */
+int gemm_xent_run(int64_t M, int64_t N, int64_t K, float alpha, const void* A, int64_t lda,
+                  const void* B, int64_t ldb, int ab_dtype, const void* targets, int target_dtype,
+                  float* loss, float* lse, void* workspace, int64_t workspace_bytes,
+                  void* stream);
+
+/* Bytes of workspace that gemm_xent_run needs (host only), or SG_ERR_SHAPE. */
+int64_t gemm_xent_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
+/*
+ * gemm_xent_backward_run -- the gradients of A and B from those of
+ * gemm_xent_run's loss and lse:
+ *   g[m][n] = alpha * ((dl[m] + dlse[m]) * exp(z[m][n] - lse[m])
+ *                      - (n == targets[m] ? dl[m] : 0)),
+ *   dA = g*B,  dB = g^T*A,
+ * dl = dloss, or 0 for a token without a target.  The logits are computed again,
+ * a run of words at a time; g is rounded to ab_dtype (fp16: scaled into its
+ * range first, exactly), the sums are fp32, the results are rounded once.
+ *   dloss    fp32 [M];  dlse  fp32 [M] or NULL (zero).
+ *   lse      fp32 [M] as gemm_xent_run wrote it for the same A, B and alpha.
+ *   dA       ab_dtype [M][ldda], or NULL: not wanted;  dB  ab_dtype [N][lddb],
+ *            or NULL.  16-byte aligned, row pitches too.  Both are overwritten
+ *            whole (zeros where M or N is 0).
+ *   workspace  DEVICE, gemm_xent_backward_workspace_bytes(M, N, K, ldb) bytes,
+ *            16-byte aligned; as above.  It is 2 * M bytes a word of a run (at
+ *            most 512 MB or 256 words), and 4 * M * K with several runs.
+ * M is below 2^22, and with dB the rows of A span less than 2^31 bytes.  The
+ * other arguments and the errors are gemm_xent_run's.
+ */
+int gemm_xent_backward_run(int64_t M, int64_t N, int64_t K, float alpha, const float* dloss,
+                           const float* dlse, const void* A, int64_t lda, const void* B,
+                           int64_t ldb, int ab_dtype, const void* targets, int target_dtype,
+                           const float* lse, void* dA, int64_t ldda, void* dB, int64_t lddb,
+                           void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that gemm_xent_backward_run needs (host only), or
+ * SG_ERR_SHAPE. */
+int64_t gemm_xent_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t ldb);
 
 /* Thread-local text of the last failing call ("" if none).  Never NULL. */
 const char* gemm_last_error(void);
