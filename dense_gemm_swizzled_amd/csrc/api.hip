@@ -675,7 +675,7 @@ int xent_check(const char* who, int64_t M, int64_t N, int64_t K, const void* A, 
   if (!aligned16(A) || !aligned16(B) ||
       reinterpret_cast<uintptr_t>(targets) % (target_dtype == SG_I64 ? 8 : 4))
     return fail(SG_ERR_ALIGN, "%s: A and B must be 16-byte aligned, targets to its elements", who);
-  const int64_t side = sg::tile_side(sg::xent_tile(M, N, K));
+  const int64_t side = sg::tile_side(sg::xent_tile(M, N));
   if (cdiv(M, side) * cdiv(N, side) > sg::kXentMaxTiles)
     return fail(SG_ERR_SHAPE, "%s: more than 2^23 tiles of %lld x %lld", who, (long long)side,
                 (long long)side);

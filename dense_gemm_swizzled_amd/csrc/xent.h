@@ -42,7 +42,19 @@ struct XentRows {
   const float* dlse;   // or NULL
   float* rows;         // [M][4]
   float* scale;        // [1]: the factor that undoes the gradient's scale
-  bool scaled;
+  float2* most;        // [parts]: the largest factors
+  int parts;
+};
+
+// What the sum of dA's parts reads and writes.
+struct XentSum {
+  int64_t M, K, rows;
+  int splits;
+  const float* parts;
+  const float* before;  // [M][K] or NULL
+  const float* scale;
+  void* D;
+  int64_t ldd;
 };
 
 __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }

@@ -2,6 +2,7 @@
 // (gemm_xent_backward_run): instantiations, the kernels around the products,
 // and the plan of both calls.
 #include "xent.h"
+#include "xent_few.h"
 
 #include "launch.h"
 #include "xent_plan.h"
@@ -59,42 +60,81 @@ __global__ void __launch_bounds__(kJoinThreads) xent_join_kernel(const XentRows 
       target_of(p.targets, p.wide, row, p.N) >= 0 ? (m - p.zt[row]) + log_sum : 0.0f;
 }
 
-// The terms of each token's gradient (XentGrad::Row).  fp16 holds 2^-24 to
-// 2^16, less than the factors of a mean over many tokens times the softmax of a
-// large vocabulary span: they are scaled by the power of two that brings the
-// largest to [2^13, 2^14), found by every workgroup for itself, and the
-// products undo it in fp32 (scale[0]).  bf16 has fp32's range.
-__global__ void __launch_bounds__(256) xent_rows_kernel(const XentRows p) {
-  float factor = 1.0f;
-  if (p.scaled) {
-    __shared__ float tops[4];
-    float top = 0.0f;
-    for (int64_t m = threadIdx.x; m < p.M; m += 256) {
-      const float dl = target_of(p.targets, p.wide, m, p.N) >= 0 ? p.dloss[m] : 0.0f;
-      const float whole = p.dlse ? dl + p.dlse[m] : dl;
-      top = __builtin_fmaxf(top, __builtin_fabsf(dl) + __builtin_fabsf(whole));
-    }
-    top = lane_reduce<64>(top, OpMax{});
-    if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
-    __syncthreads();
-    top = __builtin_fmaxf(__builtin_fmaxf(tops[0], tops[1]), __builtin_fmaxf(tops[2], tops[3])) *
-          __builtin_fabsf(p.alpha);
-    int e = 0;
-    if (top > 0.0f && top < __builtin_inff()) {
-      frexpf(top, &e);          // top in [2^(e-1), 2^e)
-      e = min(max(14 - e, -100), 100);
-      factor = ldexpf(1.0f, e);
-    }
-    if (blockIdx.x == 0 && threadIdx.x == 0) p.scale[0] = ldexpf(1.0f, -e * (factor != 1.0f));
+__device__ __forceinline__ float2 over_workgroup(float a, float b, float2 (&area)[4]) {
+  a = lane_reduce<64>(a, OpMax{});
+  b = lane_reduce<64>(b, OpMax{});
+  if ((threadIdx.x & 63) == 0) area[threadIdx.x >> 6] = make_float2(a, b);
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    a = __builtin_fmaxf(a, area[w].x);
+    b = __builtin_fmaxf(b, area[w].y);
   }
+  return make_float2(a, b);
+}
+
+// The factors of token m's gradient: dloss (0 without a target) and with dlse.
+__device__ __forceinline__ float2 factors_of(const XentRows& p, int64_t m, int t) {
+  const float dl = t >= 0 ? p.dloss[m] : 0.0f;
+  return make_float2(dl, p.dlse ? dl + p.dlse[m] : dl);
+}
+
+// The largest |dloss| and the largest sum with the softmax's factor over tokens
+// first, first + step, ..., then over the workgroup.
+__device__ __forceinline__ float2 largest(const XentRows& p, int64_t first, int64_t step,
+                                          float2 (&area)[4]) {
+  float most = 0.0f, top = 0.0f;
+#pragma unroll 4
+  for (int64_t m = first; m < p.M; m += step) {
+    const float2 f = factors_of(p, m, target_of(p.targets, p.wide, m, p.N));
+    most = __builtin_fmaxf(most, __builtin_fabsf(f.x));
+    top = __builtin_fmaxf(top, __builtin_fabsf(f.x) + __builtin_fabsf(f.y));
+  }
+  return over_workgroup(most, top, area);
+}
+
+// Beyond 1024 tokens a launch looks for them first.
+__global__ void __launch_bounds__(256) xent_most_kernel(const XentRows p) {
+  __shared__ float2 area[4];
+  const float2 v = largest(p, (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256,
+                           area);
+  if (threadIdx.x == 0) p.most[blockIdx.x] = v;
+}
+
+// The terms of each token's gradient (XentGrad::Row), scaled by a power of two
+// over the largest |dloss|: a mean's weights become one power of two, so that the
+// gradient of a target whose probability is small rounds to it exactly instead
+// of by the same fraction for every token, and fp16's narrow range (2^-24 to
+// 2^16) is used from 2^14 down.  The products undo the scale in fp32 (scale[0]).
+__global__ void __launch_bounds__(256) xent_rows_kernel(const XentRows p) {
+  __shared__ float2 area[4];
+  float2 found;
+  if (p.parts == 0) {
+    found = largest(p, threadIdx.x, 256, area);
+  } else {
+    const float2 v = (int)threadIdx.x < p.parts ? p.most[threadIdx.x] : make_float2(0.0f, 0.0f);
+    found = over_workgroup(v.x, v.y, area);
+  }
+  float most = found.x;
+  const float top = found.y;
+  // The factors, with alpha, become dloss * up and so on; down undoes it.
+  float up = p.alpha, down = 1.0f;
+  if (!(most > 0x1p-20f * top)) most = top;  // (dlse alone)
+  const float a = __builtin_fabsf(p.alpha) * most;
+  if (a > 0x1p-100f && a < 0x1p100f) {
+    int e;
+    frexpf(top / most, &e);                  // top / most in [2^(e-1), 2^e)
+    const float size = ldexpf(1.0f, 14 - e);
+    up = (p.alpha < 0 ? -size : size) / most;
+    down = a / size;
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) p.scale[0] = down;
   const int64_t m = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (m >= p.M) return;
   const int t = target_of(p.targets, p.wide, m, p.N);
-  const float dl = t >= 0 ? p.dloss[m] : 0.0f;
-  const float whole = p.dlse ? dl + p.dlse[m] : dl;
+  const float2 f = factors_of(p, m, t);
   reinterpret_cast<f32x4*>(p.rows)[m] =
-      f32x4{p.lse[m] * kLog2e, whole * p.alpha * factor, dl * p.alpha * factor,
-            __builtin_bit_cast(float, t)};
+      f32x4{p.lse[m] * kLog2e, f.y * up, f.x * up, __builtin_bit_cast(float, t)};
 }
 
 // Rows of 16-byte chunks set to zero (an empty vocabulary).
@@ -103,6 +143,82 @@ __global__ void __launch_bounds__(256) xent_zero_kernel(char* D, int64_t rows, i
   const int64_t i = block_index() * 256 + threadIdx.x;
   if (i >= rows * chunks) return;
   *reinterpret_cast<u32x4*>(D + i / chunks * pitch + 16 * (i % chunks)) = u32x4{};
+}
+
+// A below itself, [2 M][K]: the tokens of a gradient in two parts.
+__global__ void __launch_bounds__(256) xent_twice_kernel(const char* A, int64_t M, int64_t chunks,
+                                                         int64_t pitch, char* D) {
+  const int64_t i = block_index() * 256 + threadIdx.x;
+  if (i >= M * chunks) return;
+  const u32x4 v = *reinterpret_cast<const u32x4*>(A + i / chunks * pitch + 16 * (i % chunks));
+  *reinterpret_cast<u32x4*>(D + 16 * i) = v;
+  *reinterpret_cast<u32x4*>(D + 16 * (i + M * chunks)) = v;
+}
+
+// dA from its parts [splits][rows][K], rows M + m (with rows = 2 M) belonging to
+// rows m, and the runs before: the last run's sum is rounded to dA's type.
+template <int DD>
+__global__ void __launch_bounds__(256) xent_sum_kernel(const XentSum p) {
+  const int64_t i = (block_index() * 256 + threadIdx.x) * 4;
+  if (i >= p.M * p.K) return;
+  f32x4 v = p.before ? *reinterpret_cast<const f32x4*>(p.before + i) : f32x4{};
+  for (int s = 0; s < p.splits; ++s) {
+    const float* part = p.parts + (int64_t)s * p.rows * p.K + i;
+    v += *reinterpret_cast<const f32x4*>(part);
+    if (p.rows > p.M) v += *reinterpret_cast<const f32x4*>(part + p.M * p.K);
+  }
+  if constexpr (DD == SG_F32) {
+    *reinterpret_cast<f32x4*>(static_cast<float*>(p.D) + i) = v;
+  } else {
+    v *= p.scale[0];
+    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(p.D) + i / p.K * p.ldd + i % p.K) =
+        pack_d16<DD>(v);
+  }
+}
+
+// One tile of dA over a share of the words: workgroup (x, y) takes words [y *
+// share, + share), a multiple of 64.
+template <int BM, bool BF>
+__global__ void __launch_bounds__(256, 1) xent_split_kernel(DenseParams p, int64_t share) {
+  using Tile = DeepTile<BM, BF, false, true>;
+  __shared__ __attribute__((aligned(4096))) char smem[Tile::kLdsBytes];
+  const int64_t n0 = blockIdx.y * share;
+  p.A = static_cast<const char*>(p.A) + 2 * n0;
+  p.B = static_cast<const char*>(p.B) + 2 * n0 * p.ldb;
+  p.D = static_cast<float*>(p.D) + blockIdx.y * p.M * p.N;
+  p.K = max<int64_t>(0, min<int64_t>(share, p.K - n0));
+  const TileJob j = dense_tile_job<BM, BM, false, true>(p, blockIdx.x);
+  Tile::run(smem, j, p.K, nullptr, SG_NONE, p.D, SG_F32, p.N);
+}
+
+template <bool BF, int MT, int CT, bool Grad>
+hipError_t go_few(const XentParams& p, hipStream_t s) {
+  static const char* const name =
+      kernel_label(Grad ? "xent_few_grad_kernel" : "xent_few_stats_kernel", BF ? "bf16" : "f16",
+                   MT == 1 ? "16" : MT == 2 ? "32" : "64",
+                   CT == 1 ? "128" : CT == 2 ? "256" : "512");
+  last_kernel() = name;
+  const dim3 grid((unsigned)cdiv(Grad ? p.x.n_store : p.d.N, 128 * CT));
+  if constexpr (Grad)
+    hipLaunchKernelGGL((xent_few_grad_kernel<BF, MT, CT>), grid, dim3(512), 0, s, p);
+  else
+    hipLaunchKernelGGL((xent_few_stats_kernel<BF, MT, CT>), grid, dim3(512), 0, s, p);
+  return hipGetLastError();
+}
+
+template <bool Grad, bool BF, int MT>
+hipError_t few_by_words(const XentParams& p, hipStream_t s) {
+  const int ct = xent_few_blocks(p.d.N);
+  return ct == 1 ? go_few<BF, MT, 1, Grad>(p, s)
+         : ct == 2 ? go_few<BF, MT, 2, Grad>(p, s)
+                   : go_few<BF, MT, 4, Grad>(p, s);
+}
+
+template <bool Grad, bool BF>
+hipError_t few_tokens(const XentParams& p, hipStream_t s) {
+  return p.d.M <= 16   ? few_by_words<Grad, BF, 1>(p, s)
+         : p.d.M <= 32 ? few_by_words<Grad, BF, 2>(p, s)
+                       : few_by_words<Grad, BF, 4>(p, s);
 }
 
 template <bool BF, class Epi>
@@ -159,7 +275,8 @@ void go_join(const XentRows& r, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_xent(const XentCall& c, hipStream_t s) {
-  const TileShape tile = xent_tile(c.M, c.N, c.K);
+  const bool few = c.M <= kXentFew;
+  const TileShape tile = xent_tile(c.M, c.N);
   XentParams p{};
   set_product(p.d, c.M, c.N, c.K);
   p.d.A = c.A;
@@ -168,20 +285,23 @@ hipError_t launch_xent(const XentCall& c, hipStream_t s) {
   p.d.ldb = c.ldb;
   p.d.alpha = c.alpha;
   set_tiles(p.d, tile);
+  const int64_t tiles = cdiv(c.N, xent_columns(c.M, c.N));
   p.x.targets = c.targets;
   p.x.wide = c.wide;
   p.x.words = c.N;
   p.x.part = static_cast<float*>(c.workspace);
-  p.x.zt = p.x.part + 2 * c.M * p.d.tiles_n;
+  p.x.zt = p.x.part + 2 * c.M * tiles;
   if (c.N > 0) {
-    const hipError_t e = c.bf16 ? go_product<true, XentStats>(tile, p, "stats", s)
-                                : go_product<false, XentStats>(tile, p, "stats", s);
+    const hipError_t e =
+        few ? (c.bf16 ? few_tokens<false, true>(p, s) : few_tokens<false, false>(p, s))
+        : c.bf16 ? go_product<true, XentStats>(tile, p, "stats", s)
+                 : go_product<false, XentStats>(tile, p, "stats", s);
     if (e != hipSuccess) return e;
   }
   XentRows r = rows_of(c);
   r.part = p.x.part;
   r.zt = p.x.zt;
-  r.tiles = p.d.tiles_n;
+  r.tiles = (int)tiles;
   r.loss = c.loss;
   r.lse = c.lse;
   // Tokens of a workgroup: enough workgroups for the CUs, and up to 32 tokens,
@@ -192,14 +312,84 @@ hipError_t launch_xent(const XentCall& c, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_xent_backward(const XentCall& c, hipStream_t s) {
-  const XentPlan plan = xent_plan(c.M, c.N, c.K, c.ldb);
-  char* const w = static_cast<char*>(c.workspace);
-  float* const rows = reinterpret_cast<float*>(w);
-  float* const scale = reinterpret_cast<float*>(w + plan.scale_at);
-  char* const G = w + plan.g_at;
-  float* const sum = reinterpret_cast<float*>(w + plan.sum_at);
+namespace {
 
+template <int BM>
+void go_split(const DenseParams& d, bool bf16, int64_t splits, int64_t share, hipStream_t s) {
+  const dim3 grid((unsigned)(d.tiles_m * d.tiles_n), (unsigned)splits);
+  if (bf16)
+    hipLaunchKernelGGL((xent_split_kernel<BM, true>), grid, dim3(256), 0, s, d, share);
+  else
+    hipLaunchKernelGGL((xent_split_kernel<BM, false>), grid, dim3(256), 0, s, d, share);
+}
+
+// dA of one run of n words from v0 on: g B, in fp32 until the last run.
+hipError_t hidden_gradient(const XentCall& c, const XentPlan& plan, const char* G, const char* B,
+                           int64_t v0, int64_t n, hipStream_t s) {
+  char* const w = static_cast<char*>(c.workspace);
+  float* const sum = reinterpret_cast<float*>(w + plan.sum_at);
+  float* const parts = reinterpret_cast<float*>(w + plan.parts_at);
+  const float* const scale = reinterpret_cast<const float*>(w + plan.scale_at);
+  const bool first = v0 == 0, last = v0 + n == c.N;
+  const int dt = c.bf16 ? SG_BF16 : SG_F16;
+  DenseParams d;
+  set_product(d, plan.rows, c.K, n);
+  d.A = G;
+  d.lda = plan.ldg;
+  d.B = B;
+  d.ldb = c.ldb;
+  set_tiles(d, plan.a_tile);
+  if (plan.splits > 1 || plan.rows > c.M) {
+    d.D = parts;
+    d.d_dtype = SG_F32;
+    d.ldd = c.K;
+    const int64_t share = cdiv(cdiv(n, plan.splits), 64) * 64;
+    if (plan.a_tile == kTile128) go_split<128>(d, c.bf16, plan.splits, share, s);
+    else go_split<64>(d, c.bf16, plan.splits, share, s);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    XentSum q{c.M, c.K, plan.rows, (int)plan.splits, parts, first ? nullptr : sum, scale,
+              last ? c.dA : sum, c.ldda};
+    const dim3 grid = grid_of(cdiv(c.M * c.K, 1024));
+    if (!last) hipLaunchKernelGGL((xent_sum_kernel<SG_F32>), grid, dim3(256), 0, s, q);
+    else if (c.bf16) hipLaunchKernelGGL((xent_sum_kernel<SG_BF16>), grid, dim3(256), 0, s, q);
+    else hipLaunchKernelGGL((xent_sum_kernel<SG_F16>), grid, dim3(256), 0, s, q);
+    return hipGetLastError();
+  }
+  d.C = first ? nullptr : sum;
+  d.c_dtype = first ? SG_NONE : SG_F32;
+  d.ldc = c.K;
+  d.beta = first ? 0.0f : 1.0f;
+  d.D = last ? c.dA : sum;
+  d.d_dtype = last ? dt : SG_F32;
+  d.ldd = last ? c.ldda : c.K;
+  d.alpha_dev = scale;
+  return launch_dense_any_k(plan.a_tile, c.bf16, false, true, d, s);
+}
+
+// dB of the words [v0, v0 + n): g^T A.
+hipError_t head_gradient(const XentCall& c, const XentPlan& plan, const char* G, int64_t v0,
+                         int64_t n, hipStream_t s) {
+  char* const w = static_cast<char*>(c.workspace);
+  DenseParams d;
+  set_product(d, n, c.K, plan.rows);
+  d.A = G;
+  d.lda = plan.ldg;
+  d.B = plan.rows > c.M ? w + plan.twice_at : c.A;
+  d.ldb = plan.rows > c.M ? c.K : c.lda;
+  d.c_dtype = SG_NONE;
+  d.D = static_cast<char*>(c.dB) + v0 * c.lddb * 2;
+  d.d_dtype = c.bf16 ? SG_BF16 : SG_F16;
+  d.ldd = c.lddb;
+  d.alpha_dev = reinterpret_cast<const float*>(w + plan.scale_at);
+  const TileShape t = xent_back_tile(d.M, d.N, d.K);
+  set_tiles(d, t);
+  return launch_dense_any_k(t, c.bf16, true, true, d, s);
+}
+
+}  // namespace
+
+hipError_t launch_xent_backward(const XentCall& c, hipStream_t s) {
   if (c.M == 0 || c.N == 0) {  // sums of nothing
     char* const D = static_cast<char*>(c.N == 0 ? c.dA : c.dB);
     const int64_t n = c.N == 0 ? c.M : c.N, chunks = c.K / 8;
@@ -208,19 +398,28 @@ hipError_t launch_xent_backward(const XentCall& c, hipStream_t s) {
                        chunks, 2 * (c.N == 0 ? c.ldda : c.lddb));
     return hipGetLastError();
   }
+  const XentPlan plan = xent_plan(c.M, c.N, c.K, c.ldb);
+  const bool few = c.M <= kXentFew;
+  char* const w = static_cast<char*>(c.workspace);
+  char* const G = w + plan.g_at;
   XentRows r = rows_of(c);
   r.lse = const_cast<float*>(c.lse);
   r.dloss = c.dloss;
   r.dlse = c.dlse;
-  r.rows = rows;
-  r.scale = scale;
-  r.scaled = !c.bf16;
+  r.rows = reinterpret_cast<float*>(w);
+  r.scale = reinterpret_cast<float*>(w + plan.scale_at);
+  r.most = reinterpret_cast<float2*>(w + plan.most_at);
+  r.parts = c.M > 1024 ? (int)std::min<int64_t>(cdiv(c.M, 256), kXentMostParts) : 0;
+  if (r.parts)
+    hipLaunchKernelGGL(xent_most_kernel, dim3(r.parts), dim3(256), 0, s, r);
   hipLaunchKernelGGL(xent_rows_kernel, dim3((unsigned)cdiv(c.M, 256)), dim3(256), 0, s, r);
+  if (few && c.dB)
+    hipLaunchKernelGGL(xent_twice_kernel, grid_of(cdiv(c.M * c.K / 8, 256)), dim3(256), 0, s,
+                       static_cast<const char*>(c.A), c.M, c.K / 8, 2 * c.lda,
+                       w + plan.twice_at);
   hipError_t e = hipGetLastError();
-  const int dt = c.bf16 ? SG_BF16 : SG_F16;
   for (int64_t v0 = 0; v0 < c.N && e == hipSuccess; v0 += plan.words) {
     const int64_t n = std::min(plan.words, c.N - v0);
-    const bool last = v0 + n == c.N;
     const char* const B = static_cast<const char*>(c.B) + v0 * c.ldb * 2;
     XentParams p{};
     set_product(p.d, c.M, n, c.K);
@@ -231,52 +430,17 @@ hipError_t launch_xent_backward(const XentCall& c, hipStream_t s) {
     p.d.alpha = c.alpha;
     p.d.D = G;
     p.d.ldd = plan.ldg;
-    p.d.d_dtype = dt;
-    p.x.rows = rows;
+    p.d.d_dtype = c.bf16 ? SG_BF16 : SG_F16;
+    p.x.rows = r.rows;
     p.x.n_store = cdiv(n, 64) * 64;
     p.col0 = v0;
-    const TileShape tile = xent_tile(c.M, n, c.K);
+    const TileShape tile = xent_tile(c.M, n);
     set_tiles(p.d, tile);
-    e = c.bf16 ? go_product<true, XentGrad<SG_BF16>>(tile, p, "grad", s)
-               : go_product<false, XentGrad<SG_F16>>(tile, p, "grad", s);
-    if (e != hipSuccess) return e;
-    if (c.dA) {  // dA += g B, in fp32 until the last words
-      DenseParams d;
-      set_product(d, c.M, c.K, n);
-      d.A = G;
-      d.lda = plan.ldg;
-      d.B = B;
-      d.ldb = c.ldb;
-      d.C = v0 > 0 ? sum : nullptr;
-      d.c_dtype = v0 > 0 ? SG_F32 : SG_NONE;
-      d.ldc = c.K;
-      d.beta = v0 > 0 ? 1.0f : 0.0f;
-      d.D = last ? c.dA : sum;
-      d.d_dtype = last ? dt : SG_F32;
-      d.ldd = last ? c.ldda : c.K;
-      d.alpha_dev = c.bf16 ? nullptr : scale;
-      const TileShape t = xent_back_tile(d.M, d.N, n);
-      set_tiles(d, t);
-      e = launch_dense_any_k(t, c.bf16, false, true, d, s);
-      if (e != hipSuccess) return e;
-    }
-    if (c.dB) {
-      DenseParams d;
-      set_product(d, n, c.K, c.M);
-      d.A = G;
-      d.lda = plan.ldg;
-      d.B = c.A;
-      d.ldb = c.lda;
-      d.c_dtype = SG_NONE;
-      d.D = static_cast<char*>(c.dB) + v0 * c.lddb * 2;
-      d.d_dtype = dt;
-      d.ldd = c.lddb;
-      d.alpha_dev = c.bf16 ? nullptr : scale;
-      const TileShape t = xent_back_tile(d.M, d.N, c.M);
-      set_tiles(d, t);
-      e = launch_dense_any_k(t, c.bf16, true, true, d, s);
-      if (e != hipSuccess) return e;
-    }
+    e = few      ? (c.bf16 ? few_tokens<true, true>(p, s) : few_tokens<true, false>(p, s))
+        : c.bf16 ? go_product<true, XentGrad<SG_BF16>>(tile, p, "grad", s)
+                 : go_product<false, XentGrad<SG_F16>>(tile, p, "grad", s);
+    if (e == hipSuccess && c.dA) e = hidden_gradient(c, plan, G, B, v0, n, s);
+    if (e == hipSuccess && c.dB) e = head_gradient(c, plan, G, v0, n, s);
   }
   return e;
 }

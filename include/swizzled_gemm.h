@@ -541,7 +541,9 @@ int64_t gemm_xent_workspace_bytes(int64_t M, int64_t N, int64_t K);
  *            whole (zeros where M or N is 0).
  *   workspace  DEVICE, gemm_xent_backward_workspace_bytes(M, N, K, ldb) bytes,
  *            16-byte aligned; as above.  It is 2 * M bytes a word of a run (at
- *            most 512 MB or 256 words), and 4 * M * K with several runs.
+ *            most 512 MB or 256 words; twice that for up to 64 tokens, whose g
+ *            is kept to twice as many bits), 4 * M * K with several runs, and
+ *            where dA has few tiles up to 16 MB for their partial sums.
  * M is below 2^22, and with dB the rows of A span less than 2^31 bytes.  The
  * other arguments and the errors are gemm_xent_run's.
  */
