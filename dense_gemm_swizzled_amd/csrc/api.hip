@@ -808,7 +808,7 @@ int64_t gemm_xent_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   if (M < 0 || N < 0 || K < 0 || M >= kMaxExtent || N >= kMaxExtent)
     return fail(SG_ERR_SHAPE, "gemm_xent_workspace_bytes: M=%lld N=%lld K=%lld", (long long)M,
                 (long long)N, (long long)K);
-  return sg::xent_workspace(M, N, K);
+  return sg::xent_workspace(M, N);
 }
 
 int64_t gemm_xent_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t ldb) {
@@ -832,7 +832,7 @@ int gemm_xent_run(int64_t M, int64_t N, int64_t K, float alpha, const void* A, i
   if (!aligned4(loss) || !aligned4(lse))
     return fail(SG_ERR_ALIGN, "%s: loss and lse must be 4-byte aligned", who);
   if (const int rc = workspace_check(who, workspace, workspace_bytes,
-                                     sg::xent_workspace(M, N, K)))
+                                     sg::xent_workspace(M, N)))
     return rc;
   sg::XentCall c = xent_call(M, N, K, alpha, A, lda, B, ldb, ab_dtype, targets, target_dtype,
                              workspace);

@@ -91,6 +91,7 @@ struct XentJob {
   int64_t words;        // words of the vocabulary (targets outside are none)
   int64_t col0;         // the word of the tile's first column
   int64_t n_store;      // columns of the gradient that are written (>= n_valid)
+  int64_t low;          // from a value of the gradient to its second part, or 0
 };
 
 // Where one workgroup's operand panels and output tile live.
@@ -327,7 +328,8 @@ __device__ __forceinline__ void epilogue16(const f32x4 (&acc)[NI][NJ], const Til
 // Waves = 4: one wave per SIMD, each wave owns a (BM/2) x (BN/2) block.
 // Waves = 8: two waves per SIMD (the hardware interleaves them, and twice as
 // many waves issue the direct-to-LDS loads), each owning (BM/2) x (BN/4).
-template <int BM, int BN, int Elem, bool AMn, bool BMn, int Swz, int Waves = 4>
+// Epi: what is done with the sums instead of storing D (xent.h), or void.
+template <int BM, int BN, int Elem, bool AMn, bool BMn, int Swz, int Waves = 4, class Epi = void>
 struct GemmTile {
   static constexpr int kBK = 64;            // K elements per stage
   static constexpr int kRowBytes = 128;     // kBK * 2 bytes
@@ -546,6 +548,11 @@ struct GemmTile {
     }
     if (kt < kt_total) k_tile(acc, f0, f1, la, lb, ra, rb, s0, s1, j, tid, o, kt, kt_total, Ki);
 
+    if constexpr (!std::is_void<Epi>::value) {
+      __syncthreads();  // every wave's reads are done
+      Epi::template finish32<kFM, kFN, kWM, kWN, kWavesN>(acc, j, s0, D, ldd, lane, wm, wn);
+      return;
+    }
     epilogue(acc, j, C, c_dtype, D, d_dtype, ldd, lane, wm, wn);
   }
 

@@ -78,9 +78,9 @@ const char* kernel_label(const char* name, Parts... parts) {
 // launch status.
 hipError_t launch_dense(TileShape tile, bool bf16, bool a_mn, bool b_mn,
                         const DenseParams& p, hipStream_t s);
-// The same where an operand is MN-major and K any: 256x256 tiles run the
-// ping-pong from K = 65 on.  A K-major A then holds zeros from K up to the next
-// multiple of 64.
+// The same where B is MN-major, with 256x256 tiles on the ping-pong for any K.
+// A row of a K-major A that ends inside a 16-byte chunk holds zeros in the rest
+// of it.
 hipError_t launch_dense_any_k(TileShape tile, bool bf16, bool a_mn, bool b_mn,
                               const DenseParams& p, hipStream_t s);
 // The layout ablation: bf16, K-major operands, 256x256 tiles on the 32x32x16

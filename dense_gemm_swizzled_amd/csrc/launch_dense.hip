@@ -152,7 +152,7 @@ hipError_t go_tail(const DenseParams& p, hipStream_t s) {
 
 hipError_t launch_dense_any_k(TileShape tile, bool bf16, bool a_mn, bool b_mn,
                               const DenseParams& p, hipStream_t s) {
-  if (tile == kTile256 && b_mn && p.K > 64 && p.K % 64) {
+  if (tile == kTile256 && b_mn && (p.K % 64 || p.K < 128)) {
     if (a_mn) return bf16 ? go_tail<true, true>(p, s) : go_tail<false, true>(p, s);
     return bf16 ? go_tail<true, false>(p, s) : go_tail<false, false>(p, s);
   }

@@ -40,8 +40,9 @@ namespace sg {
 // type; for kElemI8 K and the offsets along it count pairs of elements, so
 // that a K tile is the same 128 bytes.  Rows: A's rows are gathered (TileJob
 // `rows`).  Epi: what is done with the sums instead of storing D (xent.h), or
-// void.  Tail: MN-major operands with any K of two K tiles or more; a K-major
-// operand's rows then hold zeros from K up to the next multiple of 64.
+// void.  Tail: the K-exact mainloop for any K (MN-major operands too), whose last
+// K tile masks what lies past K; a K-major row that ends inside a 16-byte chunk
+// holds zeros in the rest of it.
 template <int Elem, int Swz, bool AMn = false, bool BMn = false, bool OutSwz = true,
           bool Rows = false, class Epi = void, bool Tail = false>
 struct PingPong16Tile {
@@ -129,16 +130,20 @@ struct PingPong16Tile {
     }
   }
 
-  // The loader of the last K tile of an MN-major operand whose K ends inside
-  // it (Tail): the K position `soff` moves from the SGPR offset, which the
-  // range check may leave out, into the lane's own, so that rows past K, which
-  // start past the descriptor's records, read as zero.
+  // The loader of the last K tile, K position `soff`, where K ends inside it
+  // (Tail).  An MN-major operand's position moves from the SGPR offset, which
+  // the range check may leave out, into the lane's own, so that rows past K,
+  // which start past the descriptor's records, read as zero; a K-major operand's
+  // chunks past K (the lane's is `inside` or not, the same one in all its rows)
+  // go out of range.
+  template <bool Mn>
   __device__ __forceinline__ static KExactHalfLoader<Swz> last_tile(
-      const KExactHalfLoader<Swz>& x, uint32_t soff) {
+      const KExactHalfLoader<Swz>& x, uint32_t soff, bool inside) {
     KExactHalfLoader<Swz> y;
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      y.voff[q] = x.voff[q] == kOutOfRange ? kOutOfRange : x.voff[q] + soff;
+      y.voff[q] = x.voff[q] == kOutOfRange || (!Mn && !inside) ? kOutOfRange
+                                                              : x.voff[q] + (Mn ? soff : 0u);
     return y;
   }
 
@@ -361,7 +366,8 @@ struct PingPong16Tile {
       f32x4 (&acc)[kI][kJ], const KExactHalfLoader<Swz>& la, const KExactHalfLoader<Swz>& lb,
       u32x4 ra, u32x4 rb, u32x4 ra0, u32x4 rb0, uint32_t a_ring, uint32_t b_ring,
       const char* a_rd, const char* b_rd, const Offsets& o, int g, int w4, int T,
-      const TileJob& j, const void* C, int lane, uint32_t kstep_a, uint32_t kstep_b) {
+      const TileJob& j, const void* C, int lane, uint32_t kstep_a, uint32_t kstep_b,
+      [[maybe_unused]] bool inside) {
     if (g) PP::barrier();  // group 1 runs one phase behind group 0
     int bs = 0;            // t mod 3
     int t = 0;
@@ -376,8 +382,8 @@ struct PingPong16Tile {
       const uint32_t ka = (uint32_t)(T - 1) * kstep_a, kb = (uint32_t)(T - 1) * kstep_b;
       for (; t < T; ++t) {
         KExactHalfLoader<Swz> ta = la, tb = lb;
-        if (AMn && t + 2 == T) ta = last_tile(la, ka);
-        if (BMn && t + 3 == T) tb = last_tile(lb, kb);
+        if (t + 2 == T) ta = last_tile<AMn>(la, ka, inside);
+        if (t + 3 == T) tb = last_tile<BMn>(lb, kb, inside);
         const u32x4 rat = t + 1 < T ? ra : ra0, rbt = t + 2 < T ? rb : rb0;
         ktile<Active, false>(acc, t, bs, ta, rat,
                              AMn && t + 2 == T ? 0u : (uint32_t)(t + 1) * kstep_a, tb, rbt,
@@ -619,11 +625,12 @@ struct PingPong16Tile {
 
     // Tiles 0 and 1 (B before A, the order the mainloop keeps); the K-exact
     // mainloop loads A of tile 1 itself.
-    const bool kexact = AMn || BMn || (K & (kBK - 1)) == 0;
+    const bool kexact = Tail || AMn || BMn || (K & (kBK - 1)) == 0;
+    const bool inside = (uint32_t)(T - 1) * 128u + lb.chunk < kbytes;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      if constexpr (BMn && Tail) {  // (T may be 2: tile 1 may be the last)
-        const KExactHalfLoader<Swz> x = last_tile(xbm, t * kstep_b);
+      if constexpr (BMn && Tail) {  // (either tile may be the last)
+        const KExactHalfLoader<Swz> x = last_tile<true>(xbm, t * kstep_b, true);
         load_half(x, rb, b_ring + t * kTileBytes, w4, 0u);
       } else if constexpr (BMn) {
         xbm.template issue<0>(rb, b_ring + t * kTileBytes, w4, t * kstep_b);
@@ -682,13 +689,13 @@ struct PingPong16Tile {
       const u32x4 ra0 = rsrc_words(j.a, 0), rb0 = rsrc_words(j.b, 0);
       if (a_rows > 0 && ldsc)
         mainloop_x<true, true>(acc, xa, xb, ra, rb, ra0, rb0, a_ring, b_ring, a_rd, b_rd, o, g,
-                               w4, T, j, C, lane, kstep_a, kstep_b);
+                               w4, T, j, C, lane, kstep_a, kstep_b, inside);
       else if (a_rows > 0)
         mainloop_x<true, false>(acc, xa, xb, ra, rb, ra0, rb0, a_ring, b_ring, a_rd, b_rd, o, g,
-                                w4, T, j, C, lane, kstep_a, kstep_b);
+                                w4, T, j, C, lane, kstep_a, kstep_b, inside);
       else
         mainloop_x<false, false>(acc, xa, xb, ra, rb, ra0, rb0, a_ring, b_ring, a_rd, b_rd, o,
-                                 g, w4, T, j, C, lane, kstep_a, kstep_b);
+                                 g, w4, T, j, C, lane, kstep_a, kstep_b, inside);
     } else if (a_rows > 0) {
       mainloop<true>(acc, la, lb, ra, rb, a_rows, b_rows, a_ring, b_ring, a_rd, b_rd, o, g, w4,
                      T, kbytes);

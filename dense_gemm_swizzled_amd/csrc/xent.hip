@@ -2,7 +2,6 @@
 // (gemm_xent_backward_run): instantiations, the kernels around the products,
 // and the plan of both calls.
 #include "xent.h"
-#include "xent_few.h"
 
 #include "launch.h"
 #include "xent_plan.h"
@@ -106,8 +105,19 @@ __global__ void __launch_bounds__(256) xent_most_kernel(const XentRows p) {
 // gradient of a target whose probability is small rounds to it exactly instead
 // of by the same fraction for every token, and fp16's narrow range (2^-24 to
 // 2^16) is used from 2^14 down.  The products undo the scale in fp32 (scale[0]).
+// For few tokens the workgroups after the first write A below itself, [2 M][K],
+// for the gradient in two parts.
 __global__ void __launch_bounds__(256) xent_rows_kernel(const XentRows p) {
   __shared__ float2 area[4];
+  if (p.twice && blockIdx.x > 0) {
+    const int64_t i = (int64_t)(blockIdx.x - 1) * 256 + threadIdx.x, all = p.M * p.chunks;
+    if (i >= all) return;
+    const u32x4 v =
+        *reinterpret_cast<const u32x4*>(p.A + i / p.chunks * p.pitch + 16 * (i % p.chunks));
+    *reinterpret_cast<u32x4*>(p.twice + 16 * i) = v;
+    *reinterpret_cast<u32x4*>(p.twice + 16 * (i + all)) = v;
+    return;
+  }
   float2 found;
   if (p.parts == 0) {
     found = largest(p, threadIdx.x, 256, area);
@@ -145,27 +155,26 @@ __global__ void __launch_bounds__(256) xent_zero_kernel(char* D, int64_t rows, i
   *reinterpret_cast<u32x4*>(D + i / chunks * pitch + 16 * (i % chunks)) = u32x4{};
 }
 
-// A below itself, [2 M][K]: the tokens of a gradient in two parts.
-__global__ void __launch_bounds__(256) xent_twice_kernel(const char* A, int64_t M, int64_t chunks,
-                                                         int64_t pitch, char* D) {
-  const int64_t i = block_index() * 256 + threadIdx.x;
-  if (i >= M * chunks) return;
-  const u32x4 v = *reinterpret_cast<const u32x4*>(A + i / chunks * pitch + 16 * (i % chunks));
-  *reinterpret_cast<u32x4*>(D + 16 * i) = v;
-  *reinterpret_cast<u32x4*>(D + 16 * (i + M * chunks)) = v;
-}
-
 // dA from its parts [splits][rows][K], rows M + m (with rows = 2 M) belonging to
 // rows m, and the runs before: the last run's sum is rounded to dA's type.
+// Bound by reading the parts: small workgroups, so that all CUs read, and eight
+// loads in flight a thread.
 template <int DD>
-__global__ void __launch_bounds__(256) xent_sum_kernel(const XentSum p) {
-  const int64_t i = (block_index() * 256 + threadIdx.x) * 4;
+__global__ void __launch_bounds__(64) xent_sum_kernel(const XentSum p) {
+  const int64_t i = (block_index() * 64 + threadIdx.x) * 4;
   if (i >= p.M * p.K) return;
   f32x4 v = p.before ? *reinterpret_cast<const f32x4*>(p.before + i) : f32x4{};
-  for (int s = 0; s < p.splits; ++s) {
-    const float* part = p.parts + (int64_t)s * p.rows * p.K + i;
-    v += *reinterpret_cast<const f32x4*>(part);
-    if (p.rows > p.M) v += *reinterpret_cast<const f32x4*>(part + p.M * p.K);
+  const float* const part = p.parts + i;
+  if (p.rows > p.M) {
+#pragma unroll 4
+    for (int s = 0; s < p.splits; ++s) {
+      v += *reinterpret_cast<const f32x4*>(part + (int64_t)(2 * s) * p.M * p.K);
+      v += *reinterpret_cast<const f32x4*>(part + (int64_t)(2 * s + 1) * p.M * p.K);
+    }
+  } else {
+#pragma unroll 8
+    for (int s = 0; s < p.splits; ++s)
+      v += *reinterpret_cast<const f32x4*>(part + (int64_t)s * p.M * p.K);
   }
   if constexpr (DD == SG_F32) {
     *reinterpret_cast<f32x4*>(static_cast<float*>(p.D) + i) = v;
@@ -176,66 +185,58 @@ __global__ void __launch_bounds__(256) xent_sum_kernel(const XentSum p) {
   }
 }
 
-// One tile of dA over a share of the words: workgroup (x, y) takes words [y *
-// share, + share), a multiple of 64.
+// One tile of dA over a share of the words: workgroup (x, y) of gridDim.y takes
+// every share of whole 64 words, the last one to the end.
+__device__ __forceinline__ void take_share(DenseParams& p) {
+  const int64_t units = (p.K + 63) / 64;
+  const int64_t first = 64 * (units * blockIdx.y / gridDim.y);
+  const int64_t end = 64 * (units * (blockIdx.y + 1) / gridDim.y);
+  p.A = static_cast<const char*>(p.A) + 2 * first;
+  p.B = static_cast<const char*>(p.B) + 2 * first * p.ldb;
+  p.D = static_cast<float*>(p.D) + (int64_t)blockIdx.y * p.M * p.N;
+  p.K = min<int64_t>(end, p.K) - first;
+}
+
 template <int BM, bool BF>
-__global__ void __launch_bounds__(256, 1) xent_split_kernel(DenseParams p, int64_t share) {
+__global__ void __launch_bounds__(256, 1) xent_split_kernel(DenseParams p) {
   using Tile = DeepTile<BM, BF, false, true>;
   __shared__ __attribute__((aligned(4096))) char smem[Tile::kLdsBytes];
-  const int64_t n0 = blockIdx.y * share;
-  p.A = static_cast<const char*>(p.A) + 2 * n0;
-  p.B = static_cast<const char*>(p.B) + 2 * n0 * p.ldb;
-  p.D = static_cast<float*>(p.D) + blockIdx.y * p.M * p.N;
-  p.K = max<int64_t>(0, min<int64_t>(share, p.K - n0));
+  take_share(p);
   const TileJob j = dense_tile_job<BM, BM, false, true>(p, blockIdx.x);
   Tile::run(smem, j, p.K, nullptr, SG_NONE, p.D, SG_F32, p.N);
 }
 
-template <bool BF, int MT, int CT, bool Grad>
-hipError_t go_few(const XentParams& p, hipStream_t s) {
-  static const char* const name =
-      kernel_label(Grad ? "xent_few_grad_kernel" : "xent_few_stats_kernel", BF ? "bf16" : "f16",
-                   MT == 1 ? "16" : MT == 2 ? "32" : "64",
-                   CT == 1 ? "128" : CT == 2 ? "256" : "512");
-  last_kernel() = name;
-  const dim3 grid((unsigned)cdiv(Grad ? p.x.n_store : p.d.N, 128 * CT));
-  if constexpr (Grad)
-    hipLaunchKernelGGL((xent_few_grad_kernel<BF, MT, CT>), grid, dim3(512), 0, s, p);
-  else
-    hipLaunchKernelGGL((xent_few_stats_kernel<BF, MT, CT>), grid, dim3(512), 0, s, p);
-  return hipGetLastError();
-}
-
-template <bool Grad, bool BF, int MT>
-hipError_t few_by_words(const XentParams& p, hipStream_t s) {
-  const int ct = xent_few_blocks(p.d.N);
-  return ct == 1 ? go_few<BF, MT, 1, Grad>(p, s)
-         : ct == 2 ? go_few<BF, MT, 2, Grad>(p, s)
-                   : go_few<BF, MT, 4, Grad>(p, s);
-}
-
-template <bool Grad, bool BF>
-hipError_t few_tokens(const XentParams& p, hipStream_t s) {
-  return p.d.M <= 16   ? few_by_words<Grad, BF, 1>(p, s)
-         : p.d.M <= 32 ? few_by_words<Grad, BF, 2>(p, s)
-                       : few_by_words<Grad, BF, 4>(p, s);
+template <bool BF>
+__global__ void __launch_bounds__(512, 1) xent_split_pingpong_kernel(DenseParams p) {
+  using Tile = PingPong16Tile<BF, kSwzDefault, false, true, true, false, void, true>;
+  __shared__ __attribute__((aligned(4096))) char smem[Tile::kLdsBytes];
+  take_share(p);
+  const TileJob j = dense_tile_job<256, 256, false, true>(p, blockIdx.x);
+  Tile::run(smem, j, p.K, nullptr, SG_NONE, p.D, SG_F32, p.N);
 }
 
 template <bool BF, class Epi>
 hipError_t go_product(TileShape tile, const XentParams& p, const char* epi, hipStream_t s) {
   const int grid = p.d.tiles_m * p.d.tiles_n;
-  if (tile == kTile256) {
-    static const char* const name = kernel_label("xent_pingpong_kernel", BF ? "bf16" : "f16", epi);
+  constexpr const char* kType = BF ? "bf16" : "f16";
+  if (tile == kTile256 && p.d.K % 64) {
+    static const char* const name = kernel_label("xent_pingpong_kernel", kType, epi, "tail");
     last_kernel() = name;
-    hipLaunchKernelGGL((xent_pingpong_kernel<BF, Epi>), dim3(grid), dim3(512), 0, s, p);
+    hipLaunchKernelGGL((xent_pingpong_kernel<BF, Epi, true>), dim3(grid), dim3(512), 0, s, p);
+  } else if (tile == kTile256) {
+    static const char* const name = kernel_label("xent_pingpong_kernel", kType, epi);
+    last_kernel() = name;
+    hipLaunchKernelGGL((xent_pingpong_kernel<BF, Epi, false>), dim3(grid), dim3(512), 0, s, p);
+  } else if (tile == kTile128 && grid > kXentCUs) {
+    static const char* const name = kernel_label("xent_dense_kernel", kType, epi);
+    last_kernel() = name;
+    hipLaunchKernelGGL((xent_dense_kernel<BF, Epi>), dim3(grid), dim3(256), 0, s, p);
   } else if (tile == kTile128) {
-    static const char* const name =
-        kernel_label("xent_deep_kernel", "128", BF ? "bf16" : "f16", epi);
+    static const char* const name = kernel_label("xent_deep_kernel", "128", kType, epi);
     last_kernel() = name;
     hipLaunchKernelGGL((xent_deep_kernel<128, BF, Epi>), dim3(grid), dim3(256), 0, s, p);
   } else {
-    static const char* const name =
-        kernel_label("xent_deep_kernel", "64", BF ? "bf16" : "f16", epi);
+    static const char* const name = kernel_label("xent_deep_kernel", "64", kType, epi);
     last_kernel() = name;
     hipLaunchKernelGGL((xent_deep_kernel<64, BF, Epi>), dim3(grid), dim3(256), 0, s, p);
   }
@@ -272,55 +273,12 @@ void go_join(const XentRows& r, hipStream_t s) {
   hipLaunchKernelGGL((xent_join_kernel<R>), grid_of(cdiv(r.M, R)), dim3(kJoinThreads), 0, s, r);
 }
 
-}  // namespace
-
-hipError_t launch_xent(const XentCall& c, hipStream_t s) {
-  const bool few = c.M <= kXentFew;
-  const TileShape tile = xent_tile(c.M, c.N);
-  XentParams p{};
-  set_product(p.d, c.M, c.N, c.K);
-  p.d.A = c.A;
-  p.d.lda = c.lda;
-  p.d.B = c.B;
-  p.d.ldb = c.ldb;
-  p.d.alpha = c.alpha;
-  set_tiles(p.d, tile);
-  const int64_t tiles = cdiv(c.N, xent_columns(c.M, c.N));
-  p.x.targets = c.targets;
-  p.x.wide = c.wide;
-  p.x.words = c.N;
-  p.x.part = static_cast<float*>(c.workspace);
-  p.x.zt = p.x.part + 2 * c.M * tiles;
-  if (c.N > 0) {
-    const hipError_t e =
-        few ? (c.bf16 ? few_tokens<false, true>(p, s) : few_tokens<false, false>(p, s))
-        : c.bf16 ? go_product<true, XentStats>(tile, p, "stats", s)
-                 : go_product<false, XentStats>(tile, p, "stats", s);
-    if (e != hipSuccess) return e;
-  }
-  XentRows r = rows_of(c);
-  r.part = p.x.part;
-  r.zt = p.x.zt;
-  r.tiles = (int)tiles;
-  r.loss = c.loss;
-  r.lse = c.lse;
-  // Tokens of a workgroup: enough workgroups for the CUs, and up to 32 tokens,
-  // whose pairs are one 256-byte piece of each tile's row.
-  if (c.M > 4096) go_join<32>(r, s);
-  else if (c.M > 1024) go_join<8>(r, s);
-  else go_join<2>(r, s);
-  return hipGetLastError();
-}
-
-namespace {
-
 template <int BM>
-void go_split(const DenseParams& d, bool bf16, int64_t splits, int64_t share, hipStream_t s) {
-  const dim3 grid((unsigned)(d.tiles_m * d.tiles_n), (unsigned)splits);
+void go_split(const DenseParams& d, bool bf16, dim3 grid, hipStream_t s) {
   if (bf16)
-    hipLaunchKernelGGL((xent_split_kernel<BM, true>), grid, dim3(256), 0, s, d, share);
+    hipLaunchKernelGGL((xent_split_kernel<BM, true>), grid, dim3(256), 0, s, d);
   else
-    hipLaunchKernelGGL((xent_split_kernel<BM, false>), grid, dim3(256), 0, s, d, share);
+    hipLaunchKernelGGL((xent_split_kernel<BM, false>), grid, dim3(256), 0, s, d);
 }
 
 // dA of one run of n words from v0 on: g B, in fp32 until the last run.
@@ -332,28 +290,35 @@ hipError_t hidden_gradient(const XentCall& c, const XentPlan& plan, const char* 
   const float* const scale = reinterpret_cast<const float*>(w + plan.scale_at);
   const bool first = v0 == 0, last = v0 + n == c.N;
   const int dt = c.bf16 ? SG_BF16 : SG_F16;
+  const TileShape tile = plan.hidden.tile;
   DenseParams d;
   set_product(d, plan.rows, c.K, n);
   d.A = G;
   d.lda = plan.ldg;
   d.B = B;
   d.ldb = c.ldb;
-  set_tiles(d, plan.a_tile);
-  if (plan.splits > 1 || plan.rows > c.M) {
+  set_tiles(d, tile);
+  if (plan.parts) {
+    // (a last run may have fewer words than splits of 64)
+    const int splits = (int)std::min(plan.hidden.splits, cdiv(n, 64));
     d.D = parts;
     d.d_dtype = SG_F32;
     d.ldd = c.K;
-    const int64_t share = cdiv(cdiv(n, plan.splits), 64) * 64;
-    if (plan.a_tile == kTile128) go_split<128>(d, c.bf16, plan.splits, share, s);
-    else go_split<64>(d, c.bf16, plan.splits, share, s);
-    hipError_t e = hipGetLastError();
+    const dim3 grid((unsigned)(d.tiles_m * d.tiles_n), (unsigned)splits);
+    if (tile == kTile128) go_split<128>(d, c.bf16, grid, s);
+    else if (tile == kTile64) go_split<64>(d, c.bf16, grid, s);
+    else if (c.bf16)
+      hipLaunchKernelGGL((xent_split_pingpong_kernel<true>), grid, dim3(512), 0, s, d);
+    else
+      hipLaunchKernelGGL((xent_split_pingpong_kernel<false>), grid, dim3(512), 0, s, d);
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    XentSum q{c.M, c.K, plan.rows, (int)plan.splits, parts, first ? nullptr : sum, scale,
-              last ? c.dA : sum, c.ldda};
-    const dim3 grid = grid_of(cdiv(c.M * c.K, 1024));
-    if (!last) hipLaunchKernelGGL((xent_sum_kernel<SG_F32>), grid, dim3(256), 0, s, q);
-    else if (c.bf16) hipLaunchKernelGGL((xent_sum_kernel<SG_BF16>), grid, dim3(256), 0, s, q);
-    else hipLaunchKernelGGL((xent_sum_kernel<SG_F16>), grid, dim3(256), 0, s, q);
+    const XentSum q{c.M, c.K, plan.rows, splits, parts, first ? nullptr : sum, scale,
+                    last ? c.dA : sum, c.ldda};
+    const dim3 blocks = grid_of(cdiv(c.M * c.K, 256));
+    if (!last) hipLaunchKernelGGL((xent_sum_kernel<SG_F32>), blocks, dim3(64), 0, s, q);
+    else if (c.bf16) hipLaunchKernelGGL((xent_sum_kernel<SG_BF16>), blocks, dim3(64), 0, s, q);
+    else hipLaunchKernelGGL((xent_sum_kernel<SG_F16>), blocks, dim3(64), 0, s, q);
     return hipGetLastError();
   }
   d.C = first ? nullptr : sum;
@@ -363,31 +328,67 @@ hipError_t hidden_gradient(const XentCall& c, const XentPlan& plan, const char* 
   d.D = last ? c.dA : sum;
   d.d_dtype = last ? dt : SG_F32;
   d.ldd = last ? c.ldda : c.K;
+  // (the scale is undone run by run: the sum holds what it stands for)
   d.alpha_dev = scale;
-  return launch_dense_any_k(plan.a_tile, c.bf16, false, true, d, s);
+  return launch_dense_any_k(tile, c.bf16, false, true, d, s);
 }
 
 // dB of the words [v0, v0 + n): g^T A.
 hipError_t head_gradient(const XentCall& c, const XentPlan& plan, const char* G, int64_t v0,
                          int64_t n, hipStream_t s) {
   char* const w = static_cast<char*>(c.workspace);
+  const bool twice = plan.rows > c.M;
   DenseParams d;
   set_product(d, n, c.K, plan.rows);
   d.A = G;
   d.lda = plan.ldg;
-  d.B = plan.rows > c.M ? w + plan.twice_at : c.A;
-  d.ldb = plan.rows > c.M ? c.K : c.lda;
+  d.B = twice ? w + plan.twice_at : c.A;
+  d.ldb = twice ? c.K : c.lda;
   d.c_dtype = SG_NONE;
   d.D = static_cast<char*>(c.dB) + v0 * c.lddb * 2;
   d.d_dtype = c.bf16 ? SG_BF16 : SG_F16;
   d.ldd = c.lddb;
   d.alpha_dev = reinterpret_cast<const float*>(w + plan.scale_at);
-  const TileShape t = xent_back_tile(d.M, d.N, d.K);
+  const TileShape t = xent_back(d.M, d.N, d.K, 1).tile;
   set_tiles(d, t);
   return launch_dense_any_k(t, c.bf16, true, true, d, s);
 }
 
 }  // namespace
+
+hipError_t launch_xent(const XentCall& c, hipStream_t s) {
+  const TileShape tile = xent_tile(c.M, c.N);
+  XentParams p{};
+  set_product(p.d, c.M, c.N, c.K);
+  p.d.A = c.A;
+  p.d.lda = c.lda;
+  p.d.B = c.B;
+  p.d.ldb = c.ldb;
+  p.d.alpha = c.alpha;
+  set_tiles(p.d, tile);
+  p.x.targets = c.targets;
+  p.x.wide = c.wide;
+  p.x.words = c.N;
+  p.x.part = static_cast<float*>(c.workspace);
+  p.x.zt = p.x.part + 2 * c.M * p.d.tiles_n;
+  if (c.N > 0) {
+    const hipError_t e = c.bf16 ? go_product<true, XentStats>(tile, p, "stats", s)
+                                : go_product<false, XentStats>(tile, p, "stats", s);
+    if (e != hipSuccess) return e;
+  }
+  XentRows r = rows_of(c);
+  r.part = p.x.part;
+  r.zt = p.x.zt;
+  r.tiles = p.d.tiles_n;
+  r.loss = c.loss;
+  r.lse = c.lse;
+  // Tokens of a workgroup: enough workgroups for the CUs, and up to 32 tokens,
+  // whose pairs are one 256-byte piece of each tile's row.
+  if (c.M > 4096) go_join<32>(r, s);
+  else if (c.M > 1024) go_join<8>(r, s);
+  else go_join<2>(r, s);
+  return hipGetLastError();
+}
 
 hipError_t launch_xent_backward(const XentCall& c, hipStream_t s) {
   if (c.M == 0 || c.N == 0) {  // sums of nothing
@@ -399,7 +400,6 @@ hipError_t launch_xent_backward(const XentCall& c, hipStream_t s) {
     return hipGetLastError();
   }
   const XentPlan plan = xent_plan(c.M, c.N, c.K, c.ldb);
-  const bool few = c.M <= kXentFew;
   char* const w = static_cast<char*>(c.workspace);
   char* const G = w + plan.g_at;
   XentRows r = rows_of(c);
@@ -410,13 +410,16 @@ hipError_t launch_xent_backward(const XentCall& c, hipStream_t s) {
   r.scale = reinterpret_cast<float*>(w + plan.scale_at);
   r.most = reinterpret_cast<float2*>(w + plan.most_at);
   r.parts = c.M > 1024 ? (int)std::min<int64_t>(cdiv(c.M, 256), kXentMostParts) : 0;
-  if (r.parts)
-    hipLaunchKernelGGL(xent_most_kernel, dim3(r.parts), dim3(256), 0, s, r);
-  hipLaunchKernelGGL(xent_rows_kernel, dim3((unsigned)cdiv(c.M, 256)), dim3(256), 0, s, r);
-  if (few && c.dB)
-    hipLaunchKernelGGL(xent_twice_kernel, grid_of(cdiv(c.M * c.K / 8, 256)), dim3(256), 0, s,
-                       static_cast<const char*>(c.A), c.M, c.K / 8, 2 * c.lda,
-                       w + plan.twice_at);
+  int64_t blocks = cdiv(c.M, 256);
+  if (plan.rows > c.M && c.dB) {
+    r.A = static_cast<const char*>(c.A);
+    r.chunks = c.K / 8;
+    r.pitch = 2 * c.lda;
+    r.twice = w + plan.twice_at;
+    blocks = 1 + cdiv(c.M * r.chunks, 256);
+  }
+  if (r.parts) hipLaunchKernelGGL(xent_most_kernel, dim3(r.parts), dim3(256), 0, s, r);
+  hipLaunchKernelGGL(xent_rows_kernel, dim3((unsigned)blocks), dim3(256), 0, s, r);
   hipError_t e = hipGetLastError();
   for (int64_t v0 = 0; v0 < c.N && e == hipSuccess; v0 += plan.words) {
     const int64_t n = std::min(plan.words, c.N - v0);
@@ -433,12 +436,12 @@ hipError_t launch_xent_backward(const XentCall& c, hipStream_t s) {
     p.d.d_dtype = c.bf16 ? SG_BF16 : SG_F16;
     p.x.rows = r.rows;
     p.x.n_store = cdiv(n, 64) * 64;
+    p.x.low = plan.rows > c.M ? c.M * plan.ldg : 0;
     p.col0 = v0;
     const TileShape tile = xent_tile(c.M, n);
     set_tiles(p.d, tile);
-    e = few      ? (c.bf16 ? few_tokens<true, true>(p, s) : few_tokens<true, false>(p, s))
-        : c.bf16 ? go_product<true, XentGrad<SG_BF16>>(tile, p, "grad", s)
-                 : go_product<false, XentGrad<SG_F16>>(tile, p, "grad", s);
+    e = c.bf16 ? go_product<true, XentGrad<SG_BF16>>(tile, p, "grad", s)
+               : go_product<false, XentGrad<SG_F16>>(tile, p, "grad", s);
     if (e == hipSuccess && c.dA) e = hidden_gradient(c, plan, G, B, v0, n, s);
     if (e == hipSuccess && c.dB) e = head_gradient(c, plan, G, v0, n, s);
   }

@@ -39,42 +39,68 @@ constexpr int64_t kXentMaxLd = int64_t{1} << 22;   // a panel of 256 rows below 
 constexpr int64_t kXentMaxRows = int64_t{1} << 22; // 256 columns of the gradient below 2^31 bytes
 constexpr int64_t kXentMaxTiles = int64_t{1} << 23;
 
-// Up to so many tokens the product streams B past them (xent_few.h).
+// Up to so many tokens the gradient of the logits is kept in two parts.
 constexpr int64_t kXentFew = 64;
-// Words of a workgroup then: 128 while that fills the CUs, up to 512.
-inline int xent_few_blocks(int64_t N) {
-  return N > 2 * 128 * kXentCUs ? 4 : N > 128 * kXentCUs ? 2 : 1;
-}
 
-// The tiles of the product (both operands K-major).
-inline TileShape xent_tile(int64_t M, int64_t N) { return pick_dense_tile(M, N, true, true); }
-// Words of a tile, few tokens or not.
-inline int64_t xent_columns(int64_t M, int64_t N) {
-  return M <= kXentFew ? 128 * xent_few_blocks(N) : tile_side(xent_tile(M, N));
-}
-
-// The tiles of the gradients' products (MN-major operands, K of them).
-inline TileShape xent_back_tile(int64_t M, int64_t N, int64_t K) {
-  return pick_dense_tile(M, N, K > 64, true);
+// The tiles of the product (both operands K-major).  Up to 64 tokens it is bound
+// by reading B: 64x64 tiles, and 128x128 ones from three rounds of the CUs on
+// (4 x 32768 x 2048, us with B in memory, 64 | 128 | 256 tiles: 33.6 | 34.1 |
+// 38.7; 64 x 65536 x 4096 115 | 127 | 130; 64 x 131072 x 4096 201 | 183 | 193).
+inline TileShape xent_tile(int64_t M, int64_t N) {
+  if (M <= 64) return cdiv(N, 128) > 2 * kXentCUs ? kTile128 : kTile64;
+  return pick_dense_tile(M, N, true, true);
 }
 
 // Forward: a pair of floats for each token and column tile, then a float for
 // each token.
-inline int64_t xent_workspace(int64_t M, int64_t N, int64_t K) {
-  return M * cdiv(N, xent_columns(M, N)) * 8 + M * 4;
+inline int64_t xent_workspace(int64_t M, int64_t N) {
+  return M * cdiv(N, tile_side(xent_tile(M, N))) * 8 + M * 4;
+}
+
+// The tiles of a gradient's product of rows x cols over `terms`, and how many
+// workgroups share a tile's terms (`most` at most), whose sums a launch more
+// adds up.  From measured times (us, all CUs busy): a workgroup takes 5, 4 or
+// 2.5 and 0.95, 0.45 or 0.25 for 64 terms with 256x256, 128x128 and 64x64 tiles
+// (1021 x 2056 over 32003, K- and MN-major operand, 256 | 128 | 64 alone: 476 |
+// 222 | 358; 8192 x 1024 over 128, both MN-major: 10.2 | 14.3 | 24.3), the sums
+// 3 and 4 MB a microsecond.
+struct XentBack {
+  TileShape tile;
+  int64_t splits;
+};
+inline XentBack xent_back(int64_t rows, int64_t cols, int64_t terms, int64_t most) {
+  static const double start[3] = {5.0, 4.0, 2.5}, step[3] = {0.95, 0.45, 0.25};
+  const int64_t units = cdiv(terms, 64);
+  XentBack best{kTile256, 1};
+  double least = 0;
+  for (int t = 0; t < 3; ++t) {
+    const int64_t side = tile_side((TileShape)t);
+    const int64_t tiles = cdiv(rows, side) * cdiv(cols, side);
+    for (int64_t s = 1; s <= most && (s == 1 || 4 * s <= units); ++s) {
+      double us = (double)cdiv(tiles * s, kXentCUs) *
+                  (start[t] + step[t] * (double)cdiv(units, s));
+      if (s > 1) us += 3.0 + (double)s * (double)rows * (double)cols * 2e-6;
+      if (least == 0 || us < least) {
+        least = us;
+        best = {(TileShape)t, s};
+      }
+    }
+  }
+  return best;
 }
 
 // Backward: the words go in runs of `words`, for which the gradient of the
 // logits, 16 bits each (twice for few tokens), takes up to 512 MB and an operand
-// of a product stays below 2^31 bytes.  Where dA has too few tiles for the CUs,
-// `splits` workgroups a tile share a run's words.  Workspace: the tokens' terms,
-// the scale, the gradient of one run, A twice for few tokens, and the sums of
-// dA: one for each split, and with several runs one more.
+// of a product stays below 2^31 bytes.  Workspace: the tokens' terms, the scale,
+// the gradient of one run, A twice for few tokens, and the sums of dA: one for
+// each split, and with several runs one more.
 constexpr int kXentMostParts = 256;  // workgroups that look for the largest |dloss|
+constexpr int64_t kXentMostSplits = 32;
 struct XentPlan {
-  int64_t words, ldg, rows, splits;
+  int64_t words, ldg, rows;
+  XentBack hidden;  // the product of dA
+  bool parts;       // dA comes from parts that are added up
   int64_t scale_at, most_at, g_at, twice_at, sum_at, parts_at, bytes;
-  TileShape a_tile;
 };
 
 inline XentPlan xent_plan(int64_t M, int64_t N, int64_t K, int64_t ldb) {
@@ -86,21 +112,19 @@ inline XentPlan xent_plan(int64_t M, int64_t N, int64_t K, int64_t ldb) {
   most = std::max<int64_t>(most / 256 * 256, 256);
   p.words = cdiv(cdiv(N, cdiv(N, most)), 256) * 256;
   const int64_t run = std::min(p.words, N);
+  // (a pitch of many KiB would put the rows of a tile on the same few memory
+  // channels: 256 bytes more, 8192 x 4096 over 32768 1431 -> 1416 us)
   p.ldg = cdiv(run, 64) * 64;
-  // (for few tokens one tile holds them all, so that B is read once)
-  p.a_tile = few ? (p.rows > 64 ? kTile128 : kTile64) : xent_back_tile(M, K, run);
-  const int64_t side = tile_side(p.a_tile), tiles = cdiv(p.rows, side) * cdiv(K, side);
-  p.splits = p.a_tile == kTile256
-                 ? 1
-                 : std::max<int64_t>(1, std::min(kXentCUs / tiles, cdiv(run, 512)));
-  const bool parts = few || p.splits > 1, several = p.words < N;
+  if (p.ldg % 2048 == 0) p.ldg += 128;
+  p.hidden = xent_back(p.rows, K, run, kXentMostSplits);
+  p.parts = few || p.hidden.splits > 1;
   p.scale_at = 16 * M;
   p.most_at = p.scale_at + 16;
   p.g_at = cdiv(p.most_at + 8 * kXentMostParts, 256) * 256;
   p.twice_at = p.g_at + 2 * p.rows * p.ldg;
   p.sum_at = p.twice_at + (few ? 2 * p.rows * K : 0);
-  p.parts_at = p.sum_at + (several ? 4 * M * K : 0);
-  p.bytes = p.parts_at + (parts ? 4 * p.splits * p.rows * K : 0);
+  p.parts_at = p.sum_at + (p.words < N ? 4 * M * K : 0);
+  p.bytes = p.parts_at + (p.parts ? 4 * p.hidden.splits * p.rows * K : 0);
   return p;
 }
 
