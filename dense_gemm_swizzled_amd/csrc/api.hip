@@ -736,8 +736,10 @@ bool rows_of_four(const void* p, int64_t ld, int dtype) {
 }
 
 // Tokens that a workgroup of the balance loss adds up: one workgroup up to 256
-// tokens, beyond that up to 256 workgroups.
-int64_t balance_chunk(int64_t T, int E) {
+// tokens, beyond that up to 256 workgroups (us in a graph, 128 | 256 of them:
+// 16384 x 256 fp32 17.6 | 17.6, 65536 x 256 46 | 33, 65521 x 128 bf16 21 | 16;
+// the more there are the longer the join reads).
+int64_t balance_chunk(int64_t T) {
   return T <= 256 ? 256 : std::max<int64_t>(64, cdiv(cdiv(T, 256), 64) * 64);
 }
 
@@ -958,8 +960,8 @@ int moe_route_backward_run(int64_t T, int E, int top_k, const float* dweights, c
 int64_t moe_balance_workspace_bytes(int64_t T, int E) {
   if (T < 0 || T >= kMaxExtent || E < 1 || E > SG_MAX_GROUPS)
     return fail(SG_ERR_SHAPE, "moe_balance_workspace_bytes: T=%lld E=%d", (long long)T, E);
-  const int64_t parts = cdiv(T, balance_chunk(T, E));
-  return parts <= 1 ? 0 : parts * (E + 1) * 8;
+  const int64_t parts = cdiv(T, balance_chunk(T));
+  return parts <= 1 ? 0 : parts * ((E + 2) & ~1) * 8;
 }
 
 int moe_balance_run(int64_t T, int E, int top_k, const void* logits, int64_t ldl, int dtype,
@@ -985,7 +987,7 @@ int moe_balance_run(int64_t T, int E, int top_k, const void* logits, int64_t ldl
   p.ldl = ldl;
   p.score = score;
   p.vec = rows_of_four(logits, ldl, dtype);
-  p.chunk = balance_chunk(T, E);
+  p.chunk = balance_chunk(T);
   p.ids = ids;
   p.loss = loss;
   p.counts = counts;

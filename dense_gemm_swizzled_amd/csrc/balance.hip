@@ -23,6 +23,10 @@ constexpr int kGradThreads = 256;
 // A token's scores over Lanes lanes with Quads quads of experts each (quad q of
 // the lane: experts from 4 * (q * Lanes + lane)), their sum, and for a sigmoid
 // 1 - s.  A masked logit scores zero; a token with all masked has the sum zero.
+// Nine instructions a logit for the loss, which with many tokens bounds it as
+// much as memory does (expf, a division and the masks of moe_rows.h made 16384 x
+// 256 fp32 take 1 us more): the exponentials are off by |x - top|, or |x| for a
+// sigmoid, units of 2^-24 of themselves, the rounding of their arguments.
 template <int Lanes, int Quads, bool Rest>
 __device__ __forceinline__ float scores(float (&x)[Quads][kHeld], float (&rest)[Quads][kHeld],
                                         bool soft) {
@@ -45,14 +49,18 @@ __device__ __forceinline__ float scores(float (&x)[Quads][kHeld], float (&rest)[
     for (int q = 0; q < Quads; ++q)
 #pragma unroll
       for (int i = 0; i < kHeld; ++i) {
-        const float v = x[q][i], z = expf(-__builtin_fabsf(v)), under = 1.0f / (1.0f + z);
-        x[q][i] = (v < 0 ? z : 1.0f) * under;  // (of -inf: z is zero)
-        if constexpr (Rest) rest[q][i] = (v < 0 ? 1.0f : z) * under;
+        const float z = __builtin_amdgcn_exp2f(x[q][i] * -kLog2e);  // (of -inf: +inf)
+        x[q][i] = __builtin_amdgcn_rcpf(1.0f + z);
+        if constexpr (Rest) rest[q][i] = __builtin_fminf(z, FLT_MAX) * x[q][i];
         part += x[q][i];
       }
   }
   return lane_reduce<Lanes>(part, OpSum{});
 }
+
+// The workspace: for each workgroup E pairs of a sum and a count, a pair (0,
+// tokens), and one more where that makes the rows multiples of 16 bytes.
+__host__ __device__ constexpr int part_pitch(int E) { return (E + 2) & ~1; }
 
 // The loss from the sums S and counts of the experts, one thread each (none
 // from E on); n: the tokens.  In 64 bits, added in a fixed order.
@@ -96,21 +104,20 @@ __global__ void __launch_bounds__(kSumThreads) moe_balance_kernel(const BalanceP
   const int tid = threadIdx.x, lane = tid % Lanes, slot = tid / Lanes;
   const bool soft = p.score == SG_SCORE_SOFTMAX;
   const int64_t first = (int64_t)blockIdx.x * p.chunk, end = min(first + p.chunk, p.T);
-  if (tid <= SG_MAX_GROUPS) counts[tid] = 0;
-  __syncthreads();
-
-  for (int64_t i = first * p.top_k + tid; i < end * p.top_k; i += kSumThreads) {
-    const int id = p.ids[i];
-    if ((uint32_t)id < (uint32_t)p.E) atomicAdd(&counts[id], 1);
-  }
   float sum[Quads][kHeld] = {}, next[Quads][kHeld];
   int live = 0;
   auto load = [&](int64_t t) {
 #pragma unroll
     for (int q = 0; q < Quads; ++q)
-      load_row4<DT>(p, t, kHeld * (q * Lanes + lane), t < end, next[q]);
+      load_row4<DT, true>(p, t, kHeld * (q * Lanes + lane), t < end, next[q]);
   };
   load(first + slot);
+  if (tid <= SG_MAX_GROUPS) counts[tid] = 0;
+  __syncthreads();
+  for (int64_t i = first * p.top_k + tid; i < end * p.top_k; i += kSumThreads) {
+    const int id = p.ids[i];
+    if ((uint32_t)id < (uint32_t)p.E) atomicAdd(&counts[id], 1);
+  }
   for (int64_t t = first + slot; t - slot < end; t += kTokens) {  // (whole waves go round)
     float x[Quads][kHeld], none[Quads][kHeld];
 #pragma unroll
@@ -154,50 +161,67 @@ __global__ void __launch_bounds__(kSumThreads) moe_balance_kernel(const BalanceP
   if constexpr (Alone) {
     finish(p, tid < p.E ? S : 0.0f, tid < p.E ? counts[tid] : 0, counts[SG_MAX_GROUPS], area);
   } else {
-    // Pairs (sum, count), then (0, tokens).
-    u32x2* const out = static_cast<u32x2*>(p.part) + (int64_t)blockIdx.x * (p.E + 1);
+    u32x2* const out = static_cast<u32x2*>(p.part) + (int64_t)blockIdx.x * part_pitch(p.E);
     if (tid < p.E) out[tid] = u32x2{__builtin_bit_cast(uint32_t, S), (uint32_t)counts[tid]};
     if (tid == p.E) out[tid] = u32x2{0u, (uint32_t)counts[SG_MAX_GROUPS]};
   }
 }
 
-// Adds up the workgroups' pairs, a fixed share of them for each of four threads
-// an expert, and finishes the loss.
+// Adds up the workgroups' pairs and finishes the loss: one workgroup, a thread for
+// two experts and a fixed share of the rows, 16 loads of 16 bytes in flight.  What
+// a CU can read bounds it (256 experts of 256 workgroups, 0.5 MB).  (Sixteen
+// workgroups and a last one that waits for them took 7 us for any number of
+// experts: their fences and the count of those that are done.)
+template <int Wide>
 __global__ void __launch_bounds__(kSumThreads) moe_balance_join_kernel(const BalanceParams p) {
-  constexpr int kWide = SG_MAX_GROUPS, kSegs = kSumThreads / kWide;
-  __shared__ float sums[kSegs][kWide];
-  __shared__ int counts[kSegs][kWide], tokens[kSumThreads / 64];
+  constexpr int kCols = Wide / 2, kSegs = kSumThreads / kCols, kBatch = 16;
+  __shared__ float sums[kSegs][Wide];
+  __shared__ int counts[kSegs][Wide], tokens[kSumThreads / 64];
   __shared__ double area[2][4];
-  const int tid = threadIdx.x, e = tid % kWide, seg = tid / kWide;
+  const int tid = threadIdx.x, c = tid % kCols, seg = tid / kCols;
+  const int pitch = part_pitch(p.E);
   const u32x2* const part = static_cast<const u32x2*>(p.part);
-  const int pitch = p.E + 1;
-  float S = 0.0f;
-  int count = 0, n = 0;
-  if (e < p.E)
-#pragma unroll 8
-    for (int b = seg; b < p.parts; b += kSegs) {
-      const u32x2 v = part[b * pitch + e];
-      S += __builtin_bit_cast(float, (uint32_t)v[0]);
-      count += (int)v[1];
-    }
+  float S[2] = {};
+  int count[2] = {}, n = 0;
   if (tid < p.parts) n = (int)part[tid * pitch + p.E][1];
+  for (int b0 = seg; b0 < p.parts; b0 += kBatch * kSegs) {
+    u32x4 v[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      v[i] = *reinterpret_cast<const u32x4*>(part + min(b0 + i * kSegs, p.parts - 1) * pitch +
+                                             min(2 * c, pitch - 2));
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const bool on = b0 + i * kSegs < p.parts;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t bits = v[i][2 * h], number = v[i][2 * h + 1];
+        S[h] += on ? __builtin_bit_cast(float, bits) : 0.0f;
+        count[h] += on ? (int)number : 0;
+      }
+    }
+  }
   n = lane_reduce<64>(n, OpSum{});
-  sums[seg][e] = S;
-  counts[seg][e] = count;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    sums[seg][2 * c + h] = S[h];
+    counts[seg][2 * c + h] = count[h];
+  }
   if ((tid & 63) == 0) tokens[tid >> 6] = n;
   __syncthreads();
-  S = 0.0f;
-  count = n = 0;
-  if (seg == 0) {
+  float all = 0.0f;
+  int number = 0;
+  n = 0;
+  if (tid < p.E) {
 #pragma unroll
     for (int i = 0; i < kSegs; ++i) {
-      S += sums[i][e];
-      count += counts[i][e];
+      all += sums[i][tid];
+      number += counts[i][tid];
     }
   }
 #pragma unroll
   for (int w = 0; w < kSumThreads / 64; ++w) n += tokens[w];
-  finish(p, S, count, n, area);
+  finish(p, all, number, n, area);
 }
 
 // With d_e = dloss E counts[e] / (sum counts * n), the gradient of share e:
@@ -210,31 +234,40 @@ __global__ void __launch_bounds__(kGradThreads) moe_balance_backward_kernel(
   constexpr int kTokens = kGradThreads / Lanes;
   const int lane = threadIdx.x % Lanes, slot = threadIdx.x / Lanes;
   const bool soft = p.score == SG_SCORE_SOFTMAX;
-  float d[Quads][kHeld];
-  int64_t all = 0;
+  const int64_t step = (int64_t)gridDim.x * kTokens;
+  const int64_t first = (int64_t)blockIdx.x * kTokens;
+  float next[Quads][kHeld];
+  auto load = [&](int64_t t) {
+#pragma unroll
+    for (int q = 0; q < Quads; ++q)
+      load_row4<DT, true>(p, t, kHeld * (q * Lanes + lane), t < p.T, next[q]);
+  };
+  load(first + slot);
+  // (sums of counts in fp32: off by a unit of 2^-24 a step)
+  float d[Quads][kHeld], all = 0.0f;
 #pragma unroll
   for (int q = 0; q < Quads; ++q)
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {
       const int e = kHeld * (q * Lanes + lane) + i;
-      const int c = e < p.E ? p.counts[e] : 0;
-      d[q][i] = (float)c;
-      all += c;
+      d[q][i] = e < p.E ? (float)p.counts[e] : 0.0f;
+      all += d[q][i];
     }
   all = lane_reduce<Lanes>(all, OpSum{});
-  const int n = p.tokens[0];
-  const float f = all > 0 && n > 0 ? p.dloss[0] * (float)((double)p.E / ((double)all * n)) : 0.0f;
+  const float n = (float)p.tokens[0];
+  const float f = all > 0 && n > 0 ? p.dloss[0] * ((float)p.E / all / n) : 0.0f;
 #pragma unroll
   for (int q = 0; q < Quads; ++q)
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) d[q][i] *= f;
 
-  const int64_t step = (int64_t)gridDim.x * kTokens;
-  for (int64_t t = (int64_t)blockIdx.x * kTokens + slot; t - slot < p.T; t += step) {
+  for (int64_t t = first + slot; t - slot < p.T; t += step) {
     float x[Quads][kHeld], rest[Quads][kHeld];
 #pragma unroll
     for (int q = 0; q < Quads; ++q)
-      load_row4<DT>(p, t, kHeld * (q * Lanes + lane), t < p.T, x[q]);
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) x[q][i] = next[q][i];
+    if (t - slot + step < p.T) load(t + step);
     const float total = scores<Lanes, Quads, true>(x, rest, soft);
     const float over = 1.0f / __builtin_fmaxf(total, kTiny);
     float dot = 0.0f;
@@ -282,7 +315,8 @@ hipError_t go_sum(const BalanceParams& p, hipStream_t s) {
                      dim3(kSumThreads), 0, s, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(moe_balance_join_kernel, dim3(1), dim3(kSumThreads), 0, s, p);
+  constexpr int kWide = Lanes * Quads * kHeld <= 64 ? 64 : Lanes * Quads * kHeld;
+  hipLaunchKernelGGL((moe_balance_join_kernel<kWide>), dim3(1), dim3(kSumThreads), 0, s, p);
   return hipGetLastError();
 }
 
@@ -292,18 +326,27 @@ hipError_t go_grad(const BalanceParams& p, hipStream_t s) {
       kernel_label("moe_balance_backward_kernel", type_label(DT), digits(Lanes), digits(Quads));
   last_kernel() = name;
   constexpr int kTokens = kGradThreads / Lanes;
-  const int64_t blocks = std::min<int64_t>((p.T + kTokens - 1) / kTokens, 2048);
+  // Three or four workgroups a CU that go on to their next tokens, whose logits
+  // load meanwhile (us in a graph, 16384 x 256 fp32 with 512 | 768 | 1024 | one
+  // for each 8 tokens: 11.5 | 10.6 | 11.8 | 13.5; 65521 x 128 bf16 14.8 | 12.8 |
+  // 12.4 | 15.9).
+  constexpr int64_t kMost = Lanes > 16 ? 768 : 1024;
+  const int64_t blocks = std::min<int64_t>((p.T + kTokens - 1) / kTokens, kMost);
   hipLaunchKernelGGL((moe_balance_backward_kernel<DT, Lanes, Quads>), dim3((unsigned)blocks),
                      dim3(kGradThreads), 0, s, p);
   return hipGetLastError();
 }
 
+// Lanes and quads by measured times (us in a graph, 16 x 4 | 32 x 2 | 64 x 1:
+// 16384 x 256 fp32 sigmoid 18.2 | 17.5 | 16.9, its gradient 13.2 | 10.6 | 10.8;
+// 8 x 4 | 16 x 2 | 32 x 1: 65521 x 128 bf16 15.9 | 15.3 | 16.4, its gradient
+// 12.7 | 12.4 | 13.7).
 template <int DT>
 hipError_t forward(const BalanceParams& p, hipStream_t s) {
   if (p.E <= 32) return go_sum<DT, 8, 1>(p, s);
   if (p.E <= 64) return go_sum<DT, 8, 2>(p, s);
   if (p.E <= 128) return go_sum<DT, 16, 2>(p, s);
-  return go_sum<DT, 16, 4>(p, s);
+  return go_sum<DT, 64, 1>(p, s);
 }
 
 template <int DT>
@@ -311,7 +354,7 @@ hipError_t backward(const BalanceParams& p, hipStream_t s) {
   if (p.E <= 32) return go_grad<DT, 8, 1>(p, s);
   if (p.E <= 64) return go_grad<DT, 8, 2>(p, s);
   if (p.E <= 128) return go_grad<DT, 16, 2>(p, s);
-  return go_grad<DT, 16, 4>(p, s);
+  return go_grad<DT, 32, 2>(p, s);
 }
 
 }  // namespace

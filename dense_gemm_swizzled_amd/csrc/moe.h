@@ -37,7 +37,7 @@ struct BalanceParams {
   float* loss;              // [1] (forward)
   int32_t* counts;          // [E]; read by the backward pass
   int32_t* tokens;          // [1]; read by the backward pass
-  void* part;               // workspace: [workgroups][E + 1] pairs
+  void* part;               // workspace: pairs, see balance.hip
   int parts;                // workgroups
   const float* dloss;       // [1] (backward)
   void* dlogits;            // [T][lddl] of the logits' type (backward)

@@ -59,13 +59,17 @@ __global__ void __launch_bounds__(kJoinThreads) xent_join_kernel(const XentRows 
       target_of(p.targets, p.wide, row, p.N) >= 0 ? (m - p.zt[row]) + log_sum : 0.0f;
 }
 
-__device__ __forceinline__ float2 over_workgroup(float a, float b, float2 (&area)[4]) {
+constexpr int kRowsThreads = 1024;
+
+// The largest a and b of a workgroup.
+__device__ __forceinline__ float2 over_workgroup(float a, float b,
+                                                 float2 (&area)[kRowsThreads / 64]) {
   a = lane_reduce<64>(a, OpMax{});
   b = lane_reduce<64>(b, OpMax{});
   if ((threadIdx.x & 63) == 0) area[threadIdx.x >> 6] = make_float2(a, b);
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
+  for (int w = 0; w < kRowsThreads / 64; ++w) {
     a = __builtin_fmaxf(a, area[w].x);
     b = __builtin_fmaxf(b, area[w].y);
   }
@@ -74,14 +78,14 @@ __device__ __forceinline__ float2 over_workgroup(float a, float b, float2 (&area
 
 // The factors of token m's gradient: dloss (0 without a target) and with dlse.
 __device__ __forceinline__ float2 factors_of(const XentRows& p, int64_t m, int t) {
-  const float dl = t >= 0 ? p.dloss[m] : 0.0f;
+  const float given = p.dloss[m], dl = t >= 0 ? given : 0.0f;
   return make_float2(dl, p.dlse ? dl + p.dlse[m] : dl);
 }
 
 // The largest |dloss| and the largest sum with the softmax's factor over tokens
 // first, first + step, ..., then over the workgroup.
 __device__ __forceinline__ float2 largest(const XentRows& p, int64_t first, int64_t step,
-                                          float2 (&area)[4]) {
+                                          float2 (&area)[kRowsThreads / 64]) {
   float most = 0.0f, top = 0.0f;
 #pragma unroll 4
   for (int64_t m = first; m < p.M; m += step) {
@@ -92,11 +96,12 @@ __device__ __forceinline__ float2 largest(const XentRows& p, int64_t first, int6
   return over_workgroup(most, top, area);
 }
 
-// Beyond 1024 tokens a launch looks for them first.
-__global__ void __launch_bounds__(256) xent_most_kernel(const XentRows p) {
-  __shared__ float2 area[4];
-  const float2 v = largest(p, (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256,
-                           area);
+// Beyond 8192 tokens a launch looks for them first; each workgroup for itself
+// takes as long until then.
+__global__ void __launch_bounds__(kRowsThreads) xent_most_kernel(const XentRows p) {
+  __shared__ float2 area[kRowsThreads / 64];
+  const float2 v = largest(p, (int64_t)blockIdx.x * kRowsThreads + threadIdx.x,
+                           (int64_t)gridDim.x * kRowsThreads, area);
   if (threadIdx.x == 0) p.most[blockIdx.x] = v;
 }
 
@@ -107,10 +112,11 @@ __global__ void __launch_bounds__(256) xent_most_kernel(const XentRows p) {
 // 2^16) is used from 2^14 down.  The products undo the scale in fp32 (scale[0]).
 // For few tokens the workgroups after the first write A below itself, [2 M][K],
 // for the gradient in two parts.
-__global__ void __launch_bounds__(256) xent_rows_kernel(const XentRows p) {
-  __shared__ float2 area[4];
+__global__ void __launch_bounds__(kRowsThreads) xent_rows_kernel(const XentRows p) {
+  __shared__ float2 area[kRowsThreads / 64];
   if (p.twice && blockIdx.x > 0) {
-    const int64_t i = (int64_t)(blockIdx.x - 1) * 256 + threadIdx.x, all = p.M * p.chunks;
+    const int64_t i = (int64_t)(blockIdx.x - 1) * kRowsThreads + threadIdx.x;
+    const int64_t all = p.M * p.chunks;
     if (i >= all) return;
     const u32x4 v =
         *reinterpret_cast<const u32x4*>(p.A + i / p.chunks * p.pitch + 16 * (i % p.chunks));
@@ -120,7 +126,7 @@ __global__ void __launch_bounds__(256) xent_rows_kernel(const XentRows p) {
   }
   float2 found;
   if (p.parts == 0) {
-    found = largest(p, threadIdx.x, 256, area);
+    found = largest(p, threadIdx.x, kRowsThreads, area);
   } else {
     const float2 v = (int)threadIdx.x < p.parts ? p.most[threadIdx.x] : make_float2(0.0f, 0.0f);
     found = over_workgroup(v.x, v.y, area);
@@ -139,7 +145,7 @@ __global__ void __launch_bounds__(256) xent_rows_kernel(const XentRows p) {
     down = a / size;
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) p.scale[0] = down;
-  const int64_t m = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t m = (int64_t)blockIdx.x * kRowsThreads + threadIdx.x;
   if (m >= p.M) return;
   const int t = target_of(p.targets, p.wide, m, p.N);
   const float2 f = factors_of(p, m, t);
@@ -409,17 +415,17 @@ hipError_t launch_xent_backward(const XentCall& c, hipStream_t s) {
   r.rows = reinterpret_cast<float*>(w);
   r.scale = reinterpret_cast<float*>(w + plan.scale_at);
   r.most = reinterpret_cast<float2*>(w + plan.most_at);
-  r.parts = c.M > 1024 ? (int)std::min<int64_t>(cdiv(c.M, 256), kXentMostParts) : 0;
-  int64_t blocks = cdiv(c.M, 256);
+  r.parts = c.M > 8192 ? (int)std::min<int64_t>(cdiv(c.M, kRowsThreads), kXentMostParts) : 0;
+  int64_t blocks = cdiv(c.M, kRowsThreads);
   if (plan.rows > c.M && c.dB) {
     r.A = static_cast<const char*>(c.A);
     r.chunks = c.K / 8;
     r.pitch = 2 * c.lda;
     r.twice = w + plan.twice_at;
-    blocks = 1 + cdiv(c.M * r.chunks, 256);
+    blocks = 1 + cdiv(c.M * r.chunks, kRowsThreads);
   }
-  if (r.parts) hipLaunchKernelGGL(xent_most_kernel, dim3(r.parts), dim3(256), 0, s, r);
-  hipLaunchKernelGGL(xent_rows_kernel, dim3((unsigned)blocks), dim3(256), 0, s, r);
+  if (r.parts) hipLaunchKernelGGL(xent_most_kernel, dim3(r.parts), dim3(kRowsThreads), 0, s, r);
+  hipLaunchKernelGGL(xent_rows_kernel, dim3((unsigned)blocks), dim3(kRowsThreads), 0, s, r);
   hipError_t e = hipGetLastError();
   for (int64_t v0 = 0; v0 < c.N && e == hipSuccess; v0 += plan.words) {
     const int64_t n = std::min(plan.words, c.N - v0);

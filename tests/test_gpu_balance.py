@@ -2,10 +2,13 @@
 
 u = 2^-24.  A score is off by a few u: softmax by u |x - top| log2 e for the
 rounded difference and product (at most 3u (1 + |x - top|), which weighs e^-|x -
-top|: 4u of the row's sum) and u of 2^x; sigmoid by 4u (expf, a sum, a
-reciprocal, a product).  A row's sum of E adds log2 E u.  So a share is off by
-at most rel = (4 * (2 + spread) + log2 E + 4) u of itself, where spread is the
-largest |x - top| (0 for sigmoid), and 2^-126 where a result underflows."""
+top|: 4u of the row's sum) and u of 2^x; sigmoid by |x| u of
+e^-x (its argument's rounding is half a step of |x| log2 e, 2^a changes by ln 2 a
+unit of a: |x| u), then 4u (2^x, a sum, a reciprocal of one step, a product).  A
+row's sum of E adds log2 E u.  So a share is off by at most rel = (4 * (2 +
+spread) + log2 E + 4) u of itself, where spread is the largest |x - top| (|x| for
+sigmoid, up to 88 where scores underflow), and 2^-126 where a result
+underflows."""
 import math
 
 import pytest
@@ -44,7 +47,7 @@ def shares(x, score):
         spread = torch.where(on, top - x, 0).clamp(max=104.0)
     else:
         s = torch.where(on, torch.sigmoid(x), 0)
-        spread = torch.zeros_like(x)
+        spread = torch.where(on, x.abs(), 0).clamp(max=88.0)
     total = s.sum(1, keepdim=True).clamp_min(2.0 ** -126)
     rel = (4 * (2 + spread) + math.log2(x.shape[1]) + 4 + 12) * U
     return live, s, total, s / total, rel
