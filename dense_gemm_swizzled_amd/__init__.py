@@ -1208,14 +1208,16 @@ def moe_balance(logits, ids, *, score: str = "softmax", out=None, workspace=None
         _packed("tokens", tokens, (), T.int32)
         _on_one_device(logits, ids, loss, counts, tokens, workspace)
     dev = logits.device
-    workspace = _workspace(workspace, lib.moe_balance_workspace_bytes(n, E), dev)
+    need = lib.moe_balance_workspace_bytes(n, E)
+    if need or workspace is not None:
+        workspace = _workspace(workspace, need, dev)
     if out is None:
         loss = T.empty((), dtype=T.float32, device=dev)
         counts = T.empty(E, dtype=T.int32, device=dev)
         tokens = T.empty((), dtype=T.int32, device=dev)
     _launch(lib.moe_balance_run, dev, n, E, top_k, logits.data_ptr(), ldl, dt, ids.data_ptr(),
-            code, loss.data_ptr(), counts.data_ptr(), tokens.data_ptr(), workspace.data_ptr(),
-            workspace.numel())
+            code, loss.data_ptr(), counts.data_ptr(), tokens.data_ptr(),
+            workspace.data_ptr() if need else None, need)
     return loss, counts, tokens
 
 
@@ -1341,7 +1343,8 @@ def gemm_xent(A, B, targets, *, alpha: float = 1.0, out=None, workspace=None):
     dev = A.device
     workspace = _workspace(workspace, lib.gemm_xent_workspace_bytes(M, N, K), dev)
     if out is None:
-        loss, lse = T.empty(2, M, dtype=T.float32, device=dev).unbind(0)
+        loss = T.empty(M, dtype=T.float32, device=dev)
+        lse = T.empty_like(loss)
     _launch(lib.gemm_xent_run, dev, M, N, K, alpha, A.data_ptr(), lda, B.data_ptr(), ldb, dt,
             targets.data_ptr(), tt, loss.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
             workspace.numel())

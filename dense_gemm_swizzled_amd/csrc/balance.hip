@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kSumThreads) moe_balance_kernel(const BalanceP
     const float total = scores<Lanes, Quads, false>(x, none, soft);
     const uint64_t who = __ballot(any) >> (tid & 63 & ~(Lanes - 1));
     live += lane == 0 && (Lanes == 64 ? who : who & ((1ull << (Lanes & 63)) - 1)) ? 1 : 0;
-    const float over = 1.0f / __builtin_fmaxf(total, kTiny);
+    const float over = __builtin_amdgcn_rcpf(__builtin_fmaxf(total, kTiny));
 #pragma unroll
     for (int q = 0; q < Quads; ++q)
 #pragma unroll
@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(kGradThreads) moe_balance_backward_kernel(
       for (int i = 0; i < kHeld; ++i) x[q][i] = next[q][i];
     if (t - slot + step < p.T) load(t + step);
     const float total = scores<Lanes, Quads, true>(x, rest, soft);
-    const float over = 1.0f / __builtin_fmaxf(total, kTiny);
+    const float over = __builtin_amdgcn_rcpf(__builtin_fmaxf(total, kTiny));
     float dot = 0.0f;
 #pragma unroll
     for (int q = 0; q < Quads; ++q)

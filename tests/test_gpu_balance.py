@@ -275,3 +275,43 @@ def test_in_a_graph_and_on_a_side_stream():
         now = [t.detach().clone() for t in got]
         for a, b in zip(now, step()):
             assert torch.equal(a, b)
+
+
+def test_more_than_2_31_logits():
+    T, E, k = (1 << 23) + 77, 256, 2
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.empty(T, E, dtype=BF, device="cuda")
+    step = 1 << 20
+    for i in range(0, T, step):
+        n = min(step, T - i)
+        x[i:i + n] = torch.randn(n, E, generator=gen, device="cuda").to(BF)
+    assert x.numel() > 2 ** 31
+    x[:, 7] += 1.0
+    x[T - 3] = -math.inf
+    ids = torch.randint(0, E, (T, k), generator=gen, device="cuda", dtype=torch.int32)
+    ids[T - 3] = -1
+    loss, counts, tokens = sg.moe_balance(x, ids)
+    flat = ids.reshape(-1).long()
+    assert torch.equal(counts.long(), torch.bincount(flat[flat >= 0], minlength=E))
+    assert int(tokens) == T - 1
+    total = torch.zeros(E, dtype=torch.float64, device="cuda")
+    for i in range(0, T, step):
+        y = x[i:i + step].double()
+        total += torch.softmax(y[y[:, 0] > -math.inf], 1).sum(0)
+    load = E * counts.double() / counts.sum()
+    want = float((load * total).sum() / (T - 1))
+    # A lane adds T / (256 * 16) tokens one after another, half a step of the sum
+    # so far each time: at most T / 4096 / 2 steps of the sum; shares by 1e-5.
+    assert abs(float(loss) - want) <= (T / 8192 * 2 * U + 1e-5) * want
+    d = torch.tensor(float(T), device="cuda")
+    dx = sg.moe_balance_backward(d, x, counts, tokens)
+    for rows in (slice(0, 50), slice(T - 50, T), slice(T // 2, T // 2 + 50)):
+        y = x[rows].double()
+        p = torch.where(y > -math.inf, torch.softmax(y, 1), 0).nan_to_num(0.0)
+        coef = T * load / (T - 1)
+        dot = (p * coef).sum(1, keepdim=True)
+        exact = p * (coef - dot)
+        size = p * (coef + dot)
+        assert bool(((dx[rows].double() - exact).abs()
+                     <= HALF[BF] * exact.abs() + 1e-5 * size + 1e-30).all())
+    torch.cuda.empty_cache()
