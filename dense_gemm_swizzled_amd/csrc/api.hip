@@ -867,6 +867,8 @@ int gemm_xent_backward_run(int64_t M, int64_t N, int64_t K, float alpha, const f
   if (!aligned4(dloss) || !aligned4(dlse) || !aligned4(lse))
     return fail(SG_ERR_ALIGN, "%s: dloss, dlse and lse must be 4-byte aligned", who);
   if (K == 0 || (!dA && !dB)) return ok();
+  if (M > 0 && N > 0 && !sg::xent_plan(M, N, K, ldb).fits)
+    return fail(SG_ERR_SHAPE, "%s: a gradient of more than 2^23 tiles of 256 x 256", who);
   if (const int rc = workspace_check(who, workspace, workspace_bytes,
                                      gemm_xent_backward_workspace_bytes(M, N, K, ldb)))
     return rc;

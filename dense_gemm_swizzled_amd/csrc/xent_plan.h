@@ -67,22 +67,24 @@ inline int64_t xent_workspace(int64_t M, int64_t N) {
 struct XentBack {
   TileShape tile;
   int64_t splits;
+  bool fits;  // at most 2^23 workgroups
 };
 inline XentBack xent_back(int64_t rows, int64_t cols, int64_t terms, int64_t most) {
   static const double start[3] = {5.0, 4.0, 2.5}, step[3] = {0.95, 0.45, 0.25};
   const int64_t units = cdiv(terms, 64);
-  XentBack best{kTile256, 1};
+  XentBack best{kTile256, 1, false};
   double least = 0;
   for (int t = 0; t < 3; ++t) {
     const int64_t side = tile_side((TileShape)t);
     const int64_t tiles = cdiv(rows, side) * cdiv(cols, side);
     for (int64_t s = 1; s <= most && (s == 1 || 4 * s <= units); ++s) {
+      if (tiles * s > kXentMaxTiles) break;
       double us = (double)cdiv(tiles * s, kXentCUs) *
                   (start[t] + step[t] * (double)cdiv(units, s));
       if (s > 1) us += 3.0 + (double)s * (double)rows * (double)cols * 2e-6;
       if (least == 0 || us < least) {
         least = us;
-        best = {(TileShape)t, s};
+        best = {(TileShape)t, s, true};
       }
     }
   }
@@ -100,6 +102,7 @@ struct XentPlan {
   int64_t words, ldg, rows;
   XentBack hidden;  // the product of dA
   bool parts;       // dA comes from parts that are added up
+  bool fits;        // every product is one launch
   int64_t scale_at, most_at, g_at, twice_at, sum_at, parts_at, bytes;
 };
 
@@ -117,6 +120,7 @@ inline XentPlan xent_plan(int64_t M, int64_t N, int64_t K, int64_t ldb) {
   p.ldg = cdiv(run, 64) * 64;
   if (p.ldg % 2048 == 0) p.ldg += 128;
   p.hidden = xent_back(p.rows, K, run, kXentMostSplits);
+  p.fits = p.hidden.fits && xent_back(run, K, p.rows, 1).fits;
   p.parts = few || p.hidden.splits > 1;
   p.scale_at = 16 * M;
   p.most_at = p.scale_at + 16;
