@@ -34,12 +34,14 @@
 namespace sg {
 
 // Epi: what is done with the sums instead of storing D (xent.h), or void.
-template <int BM, bool IsBF16, bool AMn, bool BMn, class Epi = void>
+// Stages: of the ring.
+template <int BM, bool IsBF16, bool AMn, bool BMn, class Epi = void,
+          int Stages = (BM == 64 ? 8 : 5)>
 struct DeepTile {
   static_assert(BM == 64 || BM == 128, "64x64 or 128x128 tiles");
   using Base = GemmTile<BM, BM, IsBF16, AMn, BMn, kSwzDefault, 4>;
   static constexpr int kFM = Base::kFM, kFN = Base::kFN;   // 32x32 blocks per wave
-  static constexpr int kStages = BM == 64 ? 8 : 5;
+  static constexpr int kStages = Stages;
   static constexpr int kBK = 64;
   static constexpr int kOpBytes = BM * 128;                // one operand's K tile
   static constexpr int kStageBytes = 2 * kOpBytes;         // A, then B
@@ -48,7 +50,7 @@ struct DeepTile {
   // A wave's loads newer than those of K tile 0 at the first wait, and than
   // those of K tile t+1 in iteration t.
   static constexpr int kFirst = (kStages - 2) * kLoads, kLoop = (kStages - 3) * kLoads;
-  static_assert(kFirst == 24 && (kLoop == 20 || kLoop == 16), "vmcnt immediates");
+  static_assert(kLoop >= 0 && kFirst < 64, "vmcnt immediates");
 
   // Byte offset, in an MN-major operand's stage, of byte `byte` of k-row k.
   // 64x64 tiles: 128-byte rows, rows with bit 1 of k rotated by 64 bytes.
@@ -186,7 +188,7 @@ struct DeepTile {
     // t-1, whose fragments were read in iteration t-2, for the loads of tile
     // t + kStages - 1.
     Frags f0, f1;
-    asm volatile("s_waitcnt vmcnt(24)" ::: "memory");
+    asm volatile("s_waitcnt vmcnt(%0)" ::"i"(kFirst) : "memory");
     PingPongTile<IsBF16, kSwzDefault>::barrier();
     read(f0, 0);
     // The reads of K step kk of tile t.
@@ -217,10 +219,7 @@ struct DeepTile {
     // `steps`: the 16-wide K steps of the tile that hold any of K (4 but in
     // the last tile), so no MFMA multiplies only the zero fill past K.
     auto iteration = [&](int t, Frags& cur, Frags& nxt, int steps) {
-      if constexpr (kLoop == 20)
-        asm volatile("s_waitcnt vmcnt(20) lgkmcnt(0)" ::: "memory");
-      else
-        asm volatile("s_waitcnt vmcnt(16) lgkmcnt(0)" ::: "memory");
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"i"(kLoop) : "memory");
       PingPongTile<IsBF16, kSwzDefault>::barrier();
       if constexpr (BM != 64) {
         issue(t + kStages - 1);

@@ -329,10 +329,13 @@ __global__ void __launch_bounds__(512, 1) xent_pingpong_kernel(const XentParams 
   clock_end(p.d.clk, cs);
 }
 
-// 64x64 and 128x128 tiles, one workgroup a CU with a deep ring.
+// 64x64 and 128x128 tiles with a ring of five stages: 80 KiB of LDS, two
+// workgroups a CU, or 160.  (The eight stages that plain products of 64x64 tiles
+// run, one workgroup a CU: 4 x 32768 x 2048 with B in memory 37.9 us against
+// 34.9, 4 x 65536 x 2048 69 against 60; four stages 36.4 and 68.)
 template <int BM, bool BF, class Epi>
 __global__ void __launch_bounds__(256, 1) xent_deep_kernel(const XentParams p) {
-  using Tile = DeepTile<BM, BF, false, false, Epi>;
+  using Tile = DeepTile<BM, BF, false, false, Epi, 5>;
   __shared__ __attribute__((aligned(4096))) char smem[Tile::kLdsBytes];
   const ClockStamp cs = clock_begin(p.d.clk);
   const TileJob j = xent_job<BM>(p, blockIdx.x);

@@ -43,11 +43,11 @@ constexpr int64_t kXentMaxTiles = int64_t{1} << 23;
 constexpr int64_t kXentFew = 64;
 
 // The tiles of the product (both operands K-major).  Up to 64 tokens it is bound
-// by reading B: 64x64 tiles, and 128x128 ones from three rounds of the CUs on
-// (4 x 32768 x 2048, us with B in memory, 64 | 128 | 256 tiles: 33.6 | 34.1 |
-// 38.7; 64 x 65536 x 4096 115 | 127 | 130; 64 x 131072 x 4096 201 | 183 | 193).
+// by reading B: 64x64 tiles with two workgroups a CU (us with B in memory, 64 |
+// 128 | 256 tiles: 4 x 32768 x 2048 34.9 | 34.1 | 38.7; 64 x 65536 x 4096 110 |
+// 127 | 130; 4 x 70000 x 2048 66 | 97; 64 x 131072 x 4096 207 | 210, 5.2 TB/s).
 inline TileShape xent_tile(int64_t M, int64_t N) {
-  if (M <= 64) return cdiv(N, 128) > 2 * kXentCUs ? kTile128 : kTile64;
+  if (M <= 64) return kTile64;
   return pick_dense_tile(M, N, true, true);
 }
 

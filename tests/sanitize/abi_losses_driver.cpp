@@ -118,7 +118,7 @@ static void choices() {
   const Choice list[] = {{17, 129, 40, C, C, 1, C},         {65, 257, 200, C, C, 1, C},
                          {130, 8190, 320, B, C, 16, B},     {700, 7001, 64, B, C, 16, C},
                          {2000, 8200, 192, A, B, 8, B},     {4099, 4100, 200, A, B, 3, B},
-                         {40, 66001, 72, B, C, 32, A},      {2049, 20000, 1032, A, A, 5, A},
+                         {40, 66001, 72, C, C, 32, A},      {2049, 20000, 1032, A, A, 5, A},
                          {2048, 20032, 1024, A, A, 8, A},   {8192, 300, 1032, B, A, 1, C},
                          {3000, 70, 520, C, B, 1, C},       {100, 300, 4096, C, C, 1, B},
                          {5000, 100003, 72, A, B, 6, B}};
