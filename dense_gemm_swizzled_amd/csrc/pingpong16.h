@@ -31,6 +31,16 @@
 
 namespace sg {
 
+// What an Epi takes from memory before the mainloop (nothing without one).
+template <class Epi>
+struct EpiPre {
+  using type = typename Epi::Rows16;
+};
+template <>
+struct EpiPre<void> {
+  struct type {};
+};
+
 // AMn / BMn: A is [K][M] / B is [K][N] (MN-major); such an operand's half
 // tiles hold one 256-byte row per k (mn256_lds_offset) and its fragments
 // come from transposing reads.  Only for K a multiple of 64 with at least
@@ -622,6 +632,8 @@ struct PingPong16Tile {
 
     [[maybe_unused]] Scales sc;
     if constexpr (Elem == kElemI8) load_scales(sc, j, lane, g, w4);
+    [[maybe_unused]] typename EpiPre<Epi>::type pre;
+    if constexpr (!std::is_void<Epi>::value) pre = Epi::fetch16(j, lane, g);
 
     // Tiles 0 and 1 (B before A, the order the mainloop keeps); the K-exact
     // mainloop loads A of tile 1 itself.
@@ -711,7 +723,7 @@ struct PingPong16Tile {
     }
     if constexpr (!std::is_void<Epi>::value) {
       PP::barrier();  // every fragment read is done: the ring is free
-      Epi::template finish16<PingPong16Tile>(acc, j, smem, T, D, ldd, lane, g, w4);
+      Epi::template finish16<PingPong16Tile>(acc, j, pre, smem, T, D, ldd, lane, g, w4);
       return;
     }
 

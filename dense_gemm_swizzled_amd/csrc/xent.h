@@ -118,18 +118,27 @@ struct XentStats {
     return t >= 0 && t < 256 ? (int)t : -1;
   }
 
+  // The targets' columns of a lane's rows, loaded before the mainloop so that
+  // their latency is not the tile's last.
+  struct Rows16 {
+    int at[8];
+  };
+  __device__ __forceinline__ static Rows16 fetch16(const TileJob& j, int lane, int g) {
+    Rows16 r;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.at[i] = column(j, 128 * g + 16 * i + (lane & 15));
+    return r;
+  }
+
   // Lane l of block (i, jn) holds row 128g + 16i + l%16, columns 64 w4 + 16 jn
   // + 4(l/16) .. +3.
   template <class Tile>
   __device__ __forceinline__ static void finish16(f32x4 (&acc)[Tile::kI][Tile::kJ],
-                                                  const TileJob& j, char* smem, int, void*,
-                                                  int64_t, int lane, int g, int w4) {
+                                                  const TileJob& j, const Rows16& rows, char* smem,
+                                                  int, void*, int64_t, int lane, int g, int w4) {
     float* area = reinterpret_cast<float*>(smem);
     const int c0 = 64 * w4 + 4 * (lane >> 4);
     if (j.m_valid > 128 * g) {
-      int tc[Tile::kI];
-#pragma unroll
-      for (int i = 0; i < Tile::kI; ++i) tc[i] = column(j, 128 * g + 16 * i + (lane & 15));
 #pragma unroll
       for (int i = 0; i < Tile::kI; ++i) {
         const int ml = 128 * g + 16 * i + (lane & 15);
@@ -143,7 +152,7 @@ struct XentStats {
           for (int e = 0; e < 4 * Tile::kJ; ++e)
             if (c0 + 16 * (e >> 2) + (e & 3) >= j.n_valid) v[e] = -__builtin_inff();
         }
-        const int at = tc[i] - c0;  // 16 jn + e of the target
+        const int at = rows.at[i] - c0;  // 16 jn + e of the target
         if (at >= 0 && at < 64 && (at & 12) == 0 && ml < j.m_valid) {
           float z = 0.0f;
 #pragma unroll
@@ -222,16 +231,26 @@ struct XentGrad {
     return r.p * exp2_of(__builtin_fmaf(acc, k, -r.l2));
   }
 
+  // A lane's rows, loaded before the mainloop.
+  struct Rows16 {
+    Row row[8];
+  };
+  __device__ __forceinline__ static Rows16 fetch16(const TileJob& j, int lane, int g) {
+    Rows16 r;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.row[i] = row_of(j, 128 * g + 16 * i + (lane & 15));
+    return r;
+  }
+
   template <class Tile>
   __device__ __forceinline__ static void finish16(f32x4 (&acc)[Tile::kI][Tile::kJ],
-                                                  const TileJob& j, char* smem, int T, void* D,
-                                                  int64_t ldd, int lane, int g, int w4) {
+                                                  const TileJob& j, const Rows16& rows, char* smem,
+                                                  int T, void* D, int64_t ldd, int lane, int g,
+                                                  int w4) {
     if (j.m_valid <= 128 * g) return;
     const int c0 = 64 * w4 + 4 * (lane >> 4);
     const float k = j.alpha * kLog2e;
-    Row r[Tile::kI];
-#pragma unroll
-    for (int i = 0; i < Tile::kI; ++i) r[i] = row_of(j, 128 * g + 16 * i + (lane & 15));
+    const Row (&r)[8] = rows.row;
 #pragma unroll
     for (int i = 0; i < Tile::kI; ++i) {
 #pragma unroll

@@ -355,6 +355,8 @@ hipError_t head_gradient(const XentCall& c, const XentPlan& plan, const char* G,
   d.d_dtype = c.bf16 ? SG_BF16 : SG_F16;
   d.ldd = c.lddb;
   d.alpha_dev = reinterpret_cast<const float*>(w + plan.scale_at);
+  d.group_m = 4;  // (8192 x 65536 x 4096, all gradients with 2 | 4 | 8 | 16 tile rows
+                  // a group: 9080 | 9069 | 9150 | 9340 us; the others like 8 as well)
   const TileShape t = xent_back(d.M, d.N, d.K, 1).tile;
   set_tiles(d, t);
   return launch_dense_any_k(t, c.bf16, true, true, d, s);
