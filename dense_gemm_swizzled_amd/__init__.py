@@ -1212,9 +1212,8 @@ def moe_balance(logits, ids, *, score: str = "softmax", out=None, workspace=None
     if need or workspace is not None:
         workspace = _workspace(workspace, need, dev)
     if out is None:
-        loss = T.empty((), dtype=T.float32, device=dev)
-        counts = T.empty(E, dtype=T.int32, device=dev)
-        tokens = T.empty((), dtype=T.int32, device=dev)
+        loss = logits.new_empty((), dtype=T.float32)
+        counts, tokens = ids.new_empty(E), ids.new_empty(())
     _launch(lib.moe_balance_run, dev, n, E, top_k, logits.data_ptr(), ldl, dt, ids.data_ptr(),
             code, loss.data_ptr(), counts.data_ptr(), tokens.data_ptr(),
             workspace.data_ptr() if need else None, need)

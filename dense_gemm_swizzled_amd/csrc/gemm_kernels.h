@@ -91,7 +91,13 @@ struct XentJob {
   int64_t words;        // words of the vocabulary (targets outside are none)
   int64_t col0;         // the word of the tile's first column
   int64_t n_store;      // columns of the gradient that are written (>= n_valid)
-  int64_t low;          // from a value of the gradient to its second part, or 0
+  // Few tokens: the terms are made from these by every wave, and the gradient
+  // is written in two parts.
+  const float* dloss;   // [M]
+  const float* dlse;    // [M], or NULL
+  const float* lse;     // [M]
+  float* scale;         // [1]
+  int64_t low;          // from a value of the gradient to its second part
 };
 
 // Where one workgroup's operand panels and output tile live.

@@ -44,9 +44,13 @@ struct XentRows {
   float* scale;        // [1]: the factor that undoes the gradient's scale
   float2* most;        // [parts]: the largest factors
   int parts;
-  const char* A;       // few tokens: A, its chunks of 16 bytes a row, its pitch
-  int64_t chunks, pitch;
-  char* twice;         // and where it is written twice, or NULL
+};
+
+// A below itself, [2 M][K]: the tokens of a gradient in two parts.
+struct XentTwice {
+  const char* A;
+  int64_t M, chunks, pitch;  // chunks of 16 bytes a row
+  char* D;                   // or NULL: not wanted
 };
 
 // What the sum of dA's parts reads and writes.
@@ -76,6 +80,25 @@ __device__ __forceinline__ void join_stats(float& m, float& s, float m2, float s
   const float base = top == -__builtin_inff() ? 0.0f : top;
   s = s * exp2_of((m - base) * kLog2e) + s2 * exp2_of((m2 - base) * kLog2e);
   m = top;
+}
+
+// The scale of a gradient's terms: a power of two over the largest |dloss|
+// (`most`; `top`: the largest |dloss| + |dloss + dlse|).  A mean's weights become
+// one power of two, so that the gradient of a target whose probability is small
+// rounds to it exactly instead of by the same fraction for every token, and
+// fp16's narrow range (2^-24 to 2^16) is used from 2^14 down.  The terms, with
+// alpha, become dloss * up and so on; the products undo it by `down` in fp32.
+struct XentScale {
+  float up, down;
+};
+__device__ __forceinline__ XentScale scale_of(float alpha, float most, float top) {
+  if (!(most > 0x1p-20f * top)) most = top;  // (dlse alone)
+  const float a = __builtin_fabsf(alpha) * most;
+  if (!(a > 0x1p-100f && a < 0x1p100f)) return {alpha, 1.0f};
+  int e;
+  frexpf(top / most, &e);  // top / most in [2^(e-1), 2^e)
+  const float size = ldexpf(1.0f, 14 - e);
+  return {(alpha < 0 ? -size : size) / most, a / size};
 }
 
 // Forward.
@@ -210,9 +233,7 @@ struct XentStats {
 // rounded once, by at most half a step of its own size.  In dA and dB, sums over
 // many of them, that is less than their own rounding to 16 bits (measured
 // against 64 bits, 8192 x 65536 x 4096 bf16: 0.0018 of the norm, 0.0017 of it
-// that rounding).  With few tokens it would not average out (0.0028): finish32
-// then keeps what the rounding took away as a second 16-bit number, `low`
-// further on, and the products add both.
+// that rounding).
 template <int DD>
 struct XentGrad {
   // Row terms: log2(e) lse, the factor of the softmax, what the target's column
@@ -281,44 +302,91 @@ struct XentGrad {
     Tile::template epilogue_lds_t<SG_NONE, DD>(acc, out, cq, D, ldd, lane, g, w4);
   }
 
+  // Four columns, from c on, of tile row ml: the gradient in place of the sums
+  // (zero past the words).
+  __device__ __forceinline__ static f32x4 values(const f32x16& acc, int q, float k, const Row& r,
+                                                 const TileJob& j, int c) {
+    f32x4 v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[e] = value(acc[4 * q + e], k, r);
+      if (r.at == c + e) v[e] -= r.t;
+      if (c + e >= j.n_valid) v[e] = 0.0f;
+    }
+    return v;
+  }
+
   template <int FM, int FN, int WM, int WN, int WavesN>
   __device__ __forceinline__ static void finish32(f32x16 (&acc)[FM][FN], const TileJob& j, char*,
                                                   void* D, int64_t ldd, int lane, int wm,
                                                   int wn) {
     const int c0 = WN * wn + 4 * (lane >> 5);
     const float k = j.alpha * kLog2e;
+    const u32x2 none{};
 #pragma unroll
     for (int fm = 0; fm < FM; ++fm) {
       const int ml = WM * wm + 32 * fm + (lane & 31);
       if (ml >= j.m_valid) continue;
       const Row r = row_of(j, ml);
-      const int at = r.at - c0;
 #pragma unroll
       for (int fn = 0; fn < FN; ++fn)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const int n = 32 * fn + 8 * q;
-          if (c0 + n >= j.x.n_store) continue;
-          f32x4 v;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            v[e] = value(acc[fm][fn][4 * q + e], k, r);
-            if (at == n + e) v[e] -= r.t;
-            if (c0 + n + e >= j.n_valid) v[e] = 0.0f;
-          }
-          uint16_t* const d =
-              static_cast<uint16_t*>(D) + (j.d_row0 + ml) * ldd + j.n0 + c0 + n;
-          const u32x2 high = pack_d16<DD>(v);
-          *reinterpret_cast<u32x2*>(d) = high;
-          if (j.x.low) {  // what the rounding took away
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t h = (e & 1) ? high[e / 2] >> 16 : high[e / 2] & 0xffffu;
-              v[e] -= DD == SG_BF16 ? bf16_to_f32(h) : f16_to_f32(h);
-            }
-            *reinterpret_cast<u32x2*>(d + j.x.low) = pack_d16<DD>(v);
-          }
+          const int c = c0 + 32 * fn + 8 * q;
+          if (c >= j.x.n_store) continue;
+          store_d_chunk<SG_NONE, DD>(values(acc[fm][fn], q, k, r, j, c), none, D,
+                                     (j.d_row0 + ml) * ldd + j.n0 + c, 1.0f, 0.0f);
         }
+    }
+  }
+};
+
+// The same for up to 64 tokens, all in one tile: with few of them the rounding
+// would not average out (0.0028 of the norm), so what it took away is kept as a
+// second 16-bit number, `low` further on, and the products add both.  Every wave
+// makes the tokens' terms for itself, lane l those of token l.
+template <int DD>
+struct XentGradFew {
+  using Grad = XentGrad<DD>;
+  __device__ __forceinline__ static typename Grad::Row row_of(const TileJob& j, int lane, int ml) {
+    const int m = min(lane, j.m_valid - 1);
+    const int t = target_of(j.x.targets, j.x.wide, m, j.x.words);
+    const float given = j.x.dloss[m], dl = t >= 0 ? given : 0.0f;
+    const float whole = j.x.dlse ? dl + j.x.dlse[m] : dl;
+    const float most = lane_reduce<64>(__builtin_fabsf(dl), OpMax{});
+    const float top =
+        lane_reduce<64>(__builtin_fabsf(dl) + __builtin_fabsf(whole), OpMax{});
+    const XentScale f = scale_of(j.alpha, most, top);
+    if (j.x.col0 == 0 && threadIdx.x == 0) j.x.scale[0] = f.down;
+    const int64_t at = (int64_t)t - j.x.col0;
+    const int in = t >= 0 && at >= 0 && at < 256 ? (int)at : -1;
+    return {__shfl(j.x.lse[m] * kLog2e, ml), __shfl(whole * f.up, ml), __shfl(dl * f.up, ml),
+            __shfl(in, ml)};
+  }
+
+  template <int FM, int FN, int WM, int WN, int WavesN>
+  __device__ __forceinline__ static void finish32(f32x16 (&acc)[FM][FN], const TileJob& j, char*,
+                                                  void* D, int64_t ldd, int lane, int wm,
+                                                  int wn) {
+    static_assert(FM == 1 && FN == 1 && 2 * WM == kWaveSize, "a row for each lane");
+    const int ml = WM * wm + (lane & 31), c0 = WN * wn + 4 * (lane >> 5);
+    const float k = j.alpha * kLog2e;
+    const typename Grad::Row r = row_of(j, lane, ml);
+    if (ml >= j.m_valid) return;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int c = c0 + 8 * q;
+      if (c >= j.x.n_store) continue;
+      f32x4 v = Grad::values(acc[0][0], q, k, r, j, c);
+      uint16_t* const d = static_cast<uint16_t*>(D) + (j.d_row0 + ml) * ldd + j.n0 + c;
+      const u32x2 high = pack_d16<DD>(v);
+      *reinterpret_cast<u32x2*>(d) = high;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t h = (e & 1) ? high[e / 2] >> 16 : high[e / 2] & 0xffffu;
+        v[e] -= DD == SG_BF16 ? bf16_to_f32(h) : f16_to_f32(h);
+      }
+      *reinterpret_cast<u32x2*>(d + j.x.low) = pack_d16<DD>(v);
     }
   }
 };

@@ -105,25 +105,9 @@ __global__ void __launch_bounds__(kRowsThreads) xent_most_kernel(const XentRows 
   if (threadIdx.x == 0) p.most[blockIdx.x] = v;
 }
 
-// The terms of each token's gradient (XentGrad::Row), scaled by a power of two
-// over the largest |dloss|: a mean's weights become one power of two, so that the
-// gradient of a target whose probability is small rounds to it exactly instead
-// of by the same fraction for every token, and fp16's narrow range (2^-24 to
-// 2^16) is used from 2^14 down.  The products undo the scale in fp32 (scale[0]).
-// For few tokens the workgroups after the first write A below itself, [2 M][K],
-// for the gradient in two parts.
+// The terms of each token's gradient (XentGrad::Row).
 __global__ void __launch_bounds__(kRowsThreads) xent_rows_kernel(const XentRows p) {
   __shared__ float2 area[kRowsThreads / 64];
-  if (p.twice && blockIdx.x > 0) {
-    const int64_t i = (int64_t)(blockIdx.x - 1) * kRowsThreads + threadIdx.x;
-    const int64_t all = p.M * p.chunks;
-    if (i >= all) return;
-    const u32x4 v =
-        *reinterpret_cast<const u32x4*>(p.A + i / p.chunks * p.pitch + 16 * (i % p.chunks));
-    *reinterpret_cast<u32x4*>(p.twice + 16 * i) = v;
-    *reinterpret_cast<u32x4*>(p.twice + 16 * (i + all)) = v;
-    return;
-  }
   float2 found;
   if (p.parts == 0) {
     found = largest(p, threadIdx.x, kRowsThreads, area);
@@ -131,26 +115,14 @@ __global__ void __launch_bounds__(kRowsThreads) xent_rows_kernel(const XentRows 
     const float2 v = (int)threadIdx.x < p.parts ? p.most[threadIdx.x] : make_float2(0.0f, 0.0f);
     found = over_workgroup(v.x, v.y, area);
   }
-  float most = found.x;
-  const float top = found.y;
-  // The factors, with alpha, become dloss * up and so on; down undoes it.
-  float up = p.alpha, down = 1.0f;
-  if (!(most > 0x1p-20f * top)) most = top;  // (dlse alone)
-  const float a = __builtin_fabsf(p.alpha) * most;
-  if (a > 0x1p-100f && a < 0x1p100f) {
-    int e;
-    frexpf(top / most, &e);                  // top / most in [2^(e-1), 2^e)
-    const float size = ldexpf(1.0f, 14 - e);
-    up = (p.alpha < 0 ? -size : size) / most;
-    down = a / size;
-  }
-  if (blockIdx.x == 0 && threadIdx.x == 0) p.scale[0] = down;
+  const XentScale f = scale_of(p.alpha, found.x, found.y);
+  if (blockIdx.x == 0 && threadIdx.x == 0) p.scale[0] = f.down;
   const int64_t m = (int64_t)blockIdx.x * kRowsThreads + threadIdx.x;
   if (m >= p.M) return;
   const int t = target_of(p.targets, p.wide, m, p.N);
-  const float2 f = factors_of(p, m, t);
+  const float2 w = factors_of(p, m, t);
   reinterpret_cast<f32x4*>(p.rows)[m] =
-      f32x4{p.lse[m] * kLog2e, f.y * up, f.x * up, __builtin_bit_cast(float, t)};
+      f32x4{p.lse[m] * kLog2e, w.y * f.up, w.x * f.up, __builtin_bit_cast(float, t)};
 }
 
 // Rows of 16-byte chunks set to zero (an empty vocabulary).
@@ -161,13 +133,11 @@ __global__ void __launch_bounds__(256) xent_zero_kernel(char* D, int64_t rows, i
   *reinterpret_cast<u32x4*>(D + i / chunks * pitch + 16 * (i % chunks)) = u32x4{};
 }
 
-// dA from its parts [splits][rows][K], rows M + m (with rows = 2 M) belonging to
-// rows m, and the runs before: the last run's sum is rounded to dA's type.
-// Bound by reading the parts: small workgroups, so that all CUs read, and eight
-// loads in flight a thread.
+// Four values of dA, from i on, from its parts [splits][rows][K], rows M + m (with
+// rows = 2 M) belonging to rows m, and the runs before: the last run's sum is
+// rounded to dA's type.  Eight loads in flight a thread.
 template <int DD>
-__global__ void __launch_bounds__(64) xent_sum_kernel(const XentSum p) {
-  const int64_t i = (block_index() * 64 + threadIdx.x) * 4;
+__device__ __forceinline__ void sum_parts(const XentSum& p, int64_t i) {
   if (i >= p.M * p.K) return;
   f32x4 v = p.before ? *reinterpret_cast<const f32x4*>(p.before + i) : f32x4{};
   const float* const part = p.parts + i;
@@ -189,6 +159,49 @@ __global__ void __launch_bounds__(64) xent_sum_kernel(const XentSum p) {
     *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(p.D) + i / p.K * p.ldd + i % p.K) =
         pack_d16<DD>(v);
   }
+}
+
+// Bound by reading the parts: small workgroups, so that all CUs read.
+template <int DD>
+__global__ void __launch_bounds__(64) xent_sum_kernel(const XentSum p) {
+  sum_parts<DD>(p, (block_index() * 64 + threadIdx.x) * 4);
+}
+
+// dB on 256x256 tiles, and behind its tiles' workgroups those that add up dA's
+// parts, which then overlap (64 x 8192 x 1024: 11 us and 4 behind it).
+template <bool BF>
+__global__ void __launch_bounds__(512, 1) xent_head_kernel(const DenseParams p, const XentSum q) {
+  using Tile = PingPong16Tile<BF, kSwzDefault, true, true, true, false, void, true>;
+  __shared__ __attribute__((aligned(4096))) char smem[Tile::kLdsBytes];
+  const int tiles = p.tiles_m * p.tiles_n;
+  if ((int)blockIdx.x >= tiles) {
+    sum_parts<BF ? SG_BF16 : SG_F16>(q, ((int64_t)(blockIdx.x - tiles) * 512 + threadIdx.x) * 4);
+    return;
+  }
+  const TileJob j = dense_tile_job<256, 256, true, true>(p, blockIdx.x);
+  Tile::run(smem, j, p.K, nullptr, SG_NONE, p.D, p.d_dtype, p.ldd);
+}
+
+// The gradient of the logits of few tokens, on 64x64 tiles; behind the tiles'
+// workgroups those that write A twice.  One launch for what takes two otherwise
+// (with the tokens' terms): a launch of them alone is 4 us of 33 (64 x 8192 x
+// 1024).
+template <bool BF>
+__global__ void __launch_bounds__(256, 1) xent_few_kernel(const XentParams p, const XentTwice q) {
+  using Tile = DeepTile<64, BF, false, false, XentGradFew<BF ? SG_BF16 : SG_F16>, 5>;
+  __shared__ __attribute__((aligned(4096))) char smem[Tile::kLdsBytes];
+  const int tiles = p.d.tiles_m * p.d.tiles_n;
+  if ((int)blockIdx.x >= tiles) {
+    const int64_t i = (int64_t)(blockIdx.x - tiles) * 256 + threadIdx.x, all = q.M * q.chunks;
+    if (i >= all) return;
+    const u32x4 v =
+        *reinterpret_cast<const u32x4*>(q.A + i / q.chunks * q.pitch + 16 * (i % q.chunks));
+    *reinterpret_cast<u32x4*>(q.D + 16 * i) = v;
+    *reinterpret_cast<u32x4*>(q.D + 16 * (i + all)) = v;
+    return;
+  }
+  const TileJob j = xent_job<64>(p, blockIdx.x);
+  Tile::run(smem, j, p.d.K, nullptr, SG_NONE, p.d.D, p.d.d_dtype, p.d.ldd);
 }
 
 // One tile of dA over a share of the words: workgroup (x, y) of gridDim.y takes
@@ -287,13 +300,44 @@ void go_split(const DenseParams& d, bool bf16, dim3 grid, hipStream_t s) {
     hipLaunchKernelGGL((xent_split_kernel<BM, false>), grid, dim3(256), 0, s, d);
 }
 
-// dA of one run of n words from v0 on: g B, in fp32 until the last run.
-hipError_t hidden_gradient(const XentCall& c, const XentPlan& plan, const char* G, const char* B,
-                           int64_t v0, int64_t n, hipStream_t s) {
+hipError_t go_head(const DenseParams& d, const XentSum& q, bool bf16, hipStream_t s) {
+  static const char* const names[2] = {kernel_label("xent_head_kernel", "f16"),
+                                       kernel_label("xent_head_kernel", "bf16")};
+  last_kernel() = names[bf16];
+  const dim3 grid((unsigned)(d.tiles_m * d.tiles_n + cdiv(q.M * q.K, 4 * 512)));
+  if (bf16) hipLaunchKernelGGL((xent_head_kernel<true>), grid, dim3(512), 0, s, d, q);
+  else hipLaunchKernelGGL((xent_head_kernel<false>), grid, dim3(512), 0, s, d, q);
+  return hipGetLastError();
+}
+
+hipError_t go_few(const XentParams& p, const XentCall& c, char* twice, hipStream_t s) {
+  static const char* const names[2] = {kernel_label("xent_few_kernel", "f16"),
+                                       kernel_label("xent_few_kernel", "bf16")};
+  last_kernel() = names[c.bf16];
+  const XentTwice q{static_cast<const char*>(c.A), c.M, c.K / 8, 2 * c.lda, twice};
+  const dim3 grid((unsigned)(p.d.tiles_m * p.d.tiles_n + (twice ? cdiv(q.M * q.chunks, 256) : 0)));
+  if (c.bf16) hipLaunchKernelGGL((xent_few_kernel<true>), grid, dim3(256), 0, s, p, q);
+  else hipLaunchKernelGGL((xent_few_kernel<false>), grid, dim3(256), 0, s, p, q);
+  return hipGetLastError();
+}
+
+// The sum of dA's parts over one run of words.
+XentSum sum_of(const XentCall& c, const XentPlan& plan, int64_t v0, int64_t n) {
   char* const w = static_cast<char*>(c.workspace);
   float* const sum = reinterpret_cast<float*>(w + plan.sum_at);
-  float* const parts = reinterpret_cast<float*>(w + plan.parts_at);
-  const float* const scale = reinterpret_cast<const float*>(w + plan.scale_at);
+  // (a last run may have fewer words than splits of 64)
+  const int splits = (int)std::min(plan.hidden.splits, cdiv(n, 64));
+  return {c.M, c.K, plan.rows, splits, reinterpret_cast<float*>(w + plan.parts_at),
+          v0 == 0 ? nullptr : sum, reinterpret_cast<const float*>(w + plan.scale_at),
+          v0 + n == c.N ? c.dA : sum, c.ldda};
+}
+
+// dA of one run of n words from v0 on: g B, in fp32 until the last run.  `alone`:
+// with the sum of its parts.
+hipError_t hidden_gradient(const XentCall& c, const XentPlan& plan, const char* G, const char* B,
+                           int64_t v0, int64_t n, bool alone, hipStream_t s) {
+  char* const w = static_cast<char*>(c.workspace);
+  float* const sum = reinterpret_cast<float*>(w + plan.sum_at);
   const bool first = v0 == 0, last = v0 + n == c.N;
   const int dt = c.bf16 ? SG_BF16 : SG_F16;
   const TileShape tile = plan.hidden.tile;
@@ -305,12 +349,11 @@ hipError_t hidden_gradient(const XentCall& c, const XentPlan& plan, const char* 
   d.ldb = c.ldb;
   set_tiles(d, tile);
   if (plan.parts) {
-    // (a last run may have fewer words than splits of 64)
-    const int splits = (int)std::min(plan.hidden.splits, cdiv(n, 64));
-    d.D = parts;
+    const XentSum q = sum_of(c, plan, v0, n);
+    d.D = w + plan.parts_at;
     d.d_dtype = SG_F32;
     d.ldd = c.K;
-    const dim3 grid((unsigned)(d.tiles_m * d.tiles_n), (unsigned)splits);
+    const dim3 grid((unsigned)(d.tiles_m * d.tiles_n), (unsigned)q.splits);
     if (tile == kTile128) go_split<128>(d, c.bf16, grid, s);
     else if (tile == kTile64) go_split<64>(d, c.bf16, grid, s);
     else if (c.bf16)
@@ -318,9 +361,7 @@ hipError_t hidden_gradient(const XentCall& c, const XentPlan& plan, const char* 
     else
       hipLaunchKernelGGL((xent_split_pingpong_kernel<false>), grid, dim3(512), 0, s, d);
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    const XentSum q{c.M, c.K, plan.rows, splits, parts, first ? nullptr : sum, scale,
-                    last ? c.dA : sum, c.ldda};
+    if (e != hipSuccess || !alone) return e;
     const dim3 blocks = grid_of(cdiv(c.M * c.K, 256));
     if (!last) hipLaunchKernelGGL((xent_sum_kernel<SG_F32>), blocks, dim3(64), 0, s, q);
     else if (c.bf16) hipLaunchKernelGGL((xent_sum_kernel<SG_BF16>), blocks, dim3(64), 0, s, q);
@@ -335,16 +376,21 @@ hipError_t hidden_gradient(const XentCall& c, const XentPlan& plan, const char* 
   d.d_dtype = last ? dt : SG_F32;
   d.ldd = last ? c.ldda : c.K;
   // (the scale is undone run by run: the sum holds what it stands for)
-  d.alpha_dev = scale;
+  d.alpha_dev = reinterpret_cast<const float*>(w + plan.scale_at);
   return launch_dense_any_k(tile, c.bf16, false, true, d, s);
 }
 
 // dB of the words [v0, v0 + n): g^T A.
-hipError_t head_gradient(const XentCall& c, const XentPlan& plan, const char* G, int64_t v0,
-                         int64_t n, hipStream_t s) {
+struct HeadProduct {
+  DenseParams d;
+  TileShape tile;
+};
+HeadProduct head_product(const XentCall& c, const XentPlan& plan, const char* G, int64_t v0,
+                         int64_t n) {
   char* const w = static_cast<char*>(c.workspace);
   const bool twice = plan.rows > c.M;
-  DenseParams d;
+  HeadProduct h;
+  DenseParams& d = h.d;
   set_product(d, n, c.K, plan.rows);
   d.A = G;
   d.lda = plan.ldg;
@@ -357,9 +403,9 @@ hipError_t head_gradient(const XentCall& c, const XentPlan& plan, const char* G,
   d.alpha_dev = reinterpret_cast<const float*>(w + plan.scale_at);
   d.group_m = 4;  // (8192 x 65536 x 4096, all gradients with 2 | 4 | 8 | 16 tile rows
                   // a group: 9080 | 9069 | 9150 | 9340 us; the others like 8 as well)
-  const TileShape t = xent_back(d.M, d.N, d.K, 1).tile;
-  set_tiles(d, t);
-  return launch_dense_any_k(t, c.bf16, true, true, d, s);
+  h.tile = xent_back(d.M, d.N, d.K, 1).tile;
+  set_tiles(d, h.tile);
+  return h;
 }
 
 }  // namespace
@@ -408,6 +454,7 @@ hipError_t launch_xent_backward(const XentCall& c, hipStream_t s) {
     return hipGetLastError();
   }
   const XentPlan plan = xent_plan(c.M, c.N, c.K, c.ldb);
+  const bool few = plan.rows > c.M;
   char* const w = static_cast<char*>(c.workspace);
   char* const G = w + plan.g_at;
   XentRows r = rows_of(c);
@@ -418,19 +465,17 @@ hipError_t launch_xent_backward(const XentCall& c, hipStream_t s) {
   r.scale = reinterpret_cast<float*>(w + plan.scale_at);
   r.most = reinterpret_cast<float2*>(w + plan.most_at);
   r.parts = c.M > 8192 ? (int)std::min<int64_t>(cdiv(c.M, kRowsThreads), kXentMostParts) : 0;
-  int64_t blocks = cdiv(c.M, kRowsThreads);
-  if (plan.rows > c.M && c.dB) {
-    r.A = static_cast<const char*>(c.A);
-    r.chunks = c.K / 8;
-    r.pitch = 2 * c.lda;
-    r.twice = w + plan.twice_at;
-    blocks = 1 + cdiv(c.M * r.chunks, kRowsThreads);
+  hipError_t e = hipSuccess;
+  if (!few) {
+    if (r.parts)
+      hipLaunchKernelGGL(xent_most_kernel, dim3(r.parts), dim3(kRowsThreads), 0, s, r);
+    hipLaunchKernelGGL(xent_rows_kernel, dim3((unsigned)cdiv(c.M, kRowsThreads)),
+                       dim3(kRowsThreads), 0, s, r);
+    e = hipGetLastError();
   }
-  if (r.parts) hipLaunchKernelGGL(xent_most_kernel, dim3(r.parts), dim3(kRowsThreads), 0, s, r);
-  hipLaunchKernelGGL(xent_rows_kernel, dim3((unsigned)blocks), dim3(kRowsThreads), 0, s, r);
-  hipError_t e = hipGetLastError();
   for (int64_t v0 = 0; v0 < c.N && e == hipSuccess; v0 += plan.words) {
     const int64_t n = std::min(plan.words, c.N - v0);
+    const bool last = v0 + n == c.N;
     const char* const B = static_cast<const char*>(c.B) + v0 * c.ldb * 2;
     XentParams p{};
     set_product(p.d, c.M, n, c.K);
@@ -442,16 +487,34 @@ hipError_t launch_xent_backward(const XentCall& c, hipStream_t s) {
     p.d.D = G;
     p.d.ldd = plan.ldg;
     p.d.d_dtype = c.bf16 ? SG_BF16 : SG_F16;
-    p.x.rows = r.rows;
     p.x.n_store = cdiv(n, 64) * 64;
-    p.x.low = plan.rows > c.M ? c.M * plan.ldg : 0;
+    p.x.words = c.N;
     p.col0 = v0;
     const TileShape tile = xent_tile(c.M, n);
     set_tiles(p.d, tile);
-    e = c.bf16 ? go_product<true, XentGrad<SG_BF16>>(tile, p, "grad", s)
-               : go_product<false, XentGrad<SG_F16>>(tile, p, "grad", s);
-    if (e == hipSuccess && c.dA) e = hidden_gradient(c, plan, G, B, v0, n, s);
-    if (e == hipSuccess && c.dB) e = head_gradient(c, plan, G, v0, n, s);
+    if (few) {
+      p.x.targets = c.targets;
+      p.x.wide = c.wide;
+      p.x.dloss = c.dloss;
+      p.x.dlse = c.dlse;
+      p.x.lse = c.lse;
+      p.x.scale = r.scale;
+      p.x.low = c.M * plan.ldg;
+      e = go_few(p, c, v0 == 0 && c.dB ? w + plan.twice_at : nullptr, s);
+    } else {
+      p.x.rows = r.rows;
+      e = c.bf16 ? go_product<true, XentGrad<SG_BF16>>(tile, p, "grad", s)
+                 : go_product<false, XentGrad<SG_F16>>(tile, p, "grad", s);
+    }
+    HeadProduct h{};
+    if (c.dB) h = head_product(c, plan, G, v0, n);
+    const bool both = c.dA && c.dB && plan.parts && last && h.tile == kTile256;
+    if (e == hipSuccess && c.dA) e = hidden_gradient(c, plan, G, B, v0, n, !both, s);
+    if (e != hipSuccess) break;
+    if (both)
+      e = go_head(h.d, sum_of(c, plan, v0, n), c.bf16, s);
+    else if (c.dB)
+      e = launch_dense_any_k(h.tile, c.bf16, true, true, h.d, s);
   }
   return e;
 }
