@@ -736,11 +736,13 @@ bool rows_of_four(const void* p, int64_t ld, int dtype) {
 }
 
 // Tokens that a workgroup of the balance loss adds up: one workgroup up to 256
-// tokens, beyond that up to 256 workgroups (us in a graph, 128 | 256 of them:
-// 16384 x 256 fp32 17.6 | 17.6, 65536 x 256 46 | 33, 65521 x 128 bf16 21 | 16;
-// the more there are the longer the join reads).
+// tokens, up to 128 workgroups for 8192 tokens, beyond that 256 (us in a graph, 64
+// | 128 | 256 of them: 1024 x 256 fp32 7.5 | 7.5 | 7.5 and 9.1 for 16 of them,
+// 4096 x 256 9.7 | 9.3 | 11.6, 16384 x 256 18.5 | 13.6 | 13.6, 16384 x 128 bf16
+// 12.8 | 10.8 | 10.0, 65536 x 256 64 | 37 | 27; the more there are the longer the
+// join reads).
 int64_t balance_chunk(int64_t T) {
-  return T <= 256 ? 256 : std::max<int64_t>(64, cdiv(cdiv(T, 256), 64) * 64);
+  return T <= 256 ? 256 : cdiv(cdiv(T, T <= 8192 ? 128 : 256), 16) * 16;
 }
 
 // Up to so many pairs the plan is one launch (us, one launch / two, 256

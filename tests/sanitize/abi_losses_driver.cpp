@@ -162,7 +162,7 @@ static void balance() {
   EXPECT_RC(moe_balance_workspace_bytes(kBig, 8), SG_ERR_SHAPE);
   for (int64_t T = 1; T < kMaxExtent; T += 1 + T / 2) {
     const int64_t chunk = balance_chunk(T), parts = cdiv(T, chunk);
-    EXPECT_RC(chunk % 64 == 0 && parts >= 1 && parts <= 256 && (T > 256 || parts == 1), 1);
+    EXPECT_RC(chunk % 16 == 0 && parts >= 1 && parts <= 256 && (T > 256 || parts == 1), 1);
   }
 }
 
