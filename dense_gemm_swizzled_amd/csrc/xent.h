@@ -13,6 +13,8 @@
 // library's own kernels take g to dA and dB.
 #pragma once
 
+#include <cfloat>
+
 #include "deep64.h"
 #include "lane_ops.h"
 #include "pingpong16.h"
@@ -99,6 +101,14 @@ __device__ __forceinline__ XentScale scale_of(float alpha, float most, float top
   frexpf(top / most, &e);  // top / most in [2^(e-1), 2^e)
   const float size = ldexpf(1.0f, 14 - e);
   return {(alpha < 0 ? -size : size) / most, a / size};
+}
+
+// The softmax's factor of a token's gradient: 0 where neither loss nor lse has a
+// weight, whatever the token's logits are (padding may hold anything), else NaN
+// where lse is no number.
+__device__ __forceinline__ float softmax_factor(float dl, float whole, float up, float lse) {
+  if (dl == 0.0f && whole == 0.0f) return 0.0f;
+  return __builtin_fabsf(lse) < __builtin_inff() ? whole * up : __builtin_nanf("");
 }
 
 // Forward.
@@ -248,8 +258,10 @@ struct XentGrad {
     const int64_t at = (int64_t)t - j.x.col0;
     return {r[0], r[1], r[2], t >= 0 && at >= 0 && at < 256 ? (int)at : -1};
   }
+  // (A logit of NaN counts as probability 0 here: its row has no weight, or the
+  // factor NaN.)
   __device__ __forceinline__ static float value(float acc, float k, const Row& r) {
-    return r.p * exp2_of(__builtin_fmaf(acc, k, -r.l2));
+    return r.p * exp2_of(__builtin_fmaxf(__builtin_fmaf(acc, k, -r.l2), -FLT_MAX));
   }
 
   // A lane's rows, loaded before the mainloop.
@@ -360,8 +372,9 @@ struct XentGradFew {
     if (j.x.col0 == 0 && threadIdx.x == 0) j.x.scale[0] = f.down;
     const int64_t at = (int64_t)t - j.x.col0;
     const int in = t >= 0 && at >= 0 && at < 256 ? (int)at : -1;
-    return {__shfl(j.x.lse[m] * kLog2e, ml), __shfl(whole * f.up, ml), __shfl(dl * f.up, ml),
-            __shfl(in, ml)};
+    const float lse = j.x.lse[m];
+    return {__shfl(lse * kLog2e, ml), __shfl(softmax_factor(dl, whole, f.up, lse), ml),
+            __shfl(dl * f.up, ml), __shfl(in, ml)};
   }
 
   template <int FM, int FN, int WM, int WN, int WavesN>

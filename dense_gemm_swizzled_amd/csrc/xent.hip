@@ -121,8 +121,10 @@ __global__ void __launch_bounds__(kRowsThreads) xent_rows_kernel(const XentRows 
   if (m >= p.M) return;
   const int t = target_of(p.targets, p.wide, m, p.N);
   const float2 w = factors_of(p, m, t);
+  const float lse = p.lse[m];
   reinterpret_cast<f32x4*>(p.rows)[m] =
-      f32x4{p.lse[m] * kLog2e, w.y * f.up, w.x * f.up, __builtin_bit_cast(float, t)};
+      f32x4{lse * kLog2e, softmax_factor(w.x, w.y, f.up, lse), w.x * f.up,
+            __builtin_bit_cast(float, t)};
 }
 
 // Rows of 16-byte chunks set to zero (an empty vocabulary).
@@ -508,7 +510,8 @@ hipError_t launch_xent_backward(const XentCall& c, hipStream_t s) {
     }
     HeadProduct h{};
     if (c.dB) h = head_product(c, plan, G, v0, n);
-    const bool both = c.dA && c.dB && plan.parts && last && h.tile == kTile256;
+    const bool both = c.dA && c.dB && plan.parts && last && h.tile == kTile256 &&
+                      c.M * c.K <= kXentMaxTiles * 1024;  // (half a launch's workgroups)
     if (e == hipSuccess && c.dA) e = hidden_gradient(c, plan, G, B, v0, n, !both, s);
     if (e != hipSuccess) break;
     if (both)

@@ -531,7 +531,9 @@ int64_t gemm_xent_workspace_bytes(int64_t M, int64_t N, int64_t K);
  *   g[m][n] = alpha * ((dl[m] + dlse[m]) * exp(z[m][n] - lse[m])
  *                      - (n == targets[m] ? dl[m] : 0)),
  *   dA = g*B,  dB = g^T*A,
- * dl = dloss, or 0 for a token without a target.  The logits are computed again,
+ * dl = dloss, or 0 for a token without a target; g is 0 for a token whose dl and
+ * dlse are 0, whatever its A holds (its row of dA is 0; dB adds 0 * A, so that A
+ * has to be finite there).  The logits are computed again,
  * a run of words at a time; g is rounded to ab_dtype (fp16: scaled into its
  * range first, exactly), the sums are fp32, the results are rounded once.
  *   dloss    fp32 [M];  dlse  fp32 [M] or NULL (zero).
@@ -543,7 +545,8 @@ int64_t gemm_xent_workspace_bytes(int64_t M, int64_t N, int64_t K);
  *            16-byte aligned; as above.  It is 2 * M bytes a word of a run (at
  *            most 512 MB or 256 words; twice that for up to 64 tokens, whose g
  *            is kept to twice as many bits), 4 * M * K with several runs, and
- *            where dA has few tiles up to 16 MB for their partial sums.
+ *            where dA has few tiles 4 * M * K for each of up to 32 shares of the
+ *            words, so many that they fill the CUs.
  * M is below 2^22, and with dB the rows of A span less than 2^31 bytes.  The
  * other arguments and the errors are gemm_xent_run's.
  */

@@ -96,6 +96,32 @@ def test_weights_of_any_size(weights, dtype):
     close(dB, wB, bB, "dB")
 
 
+@pytest.mark.parametrize("M,N,K", [(50, 300, 64), (150, 9001, 72), (2100, 8200, 192)])
+def test_padding_holds_anything(M, N, K):
+    """Tokens without a weight have no part in dA, NaN or not; others that are NaN
+    have NaN."""
+    A, B, t = ref.inputs(M, N, K, BF, 35, ignored=0.0)
+    t[::4] = -100
+    want, lse0 = sg.gemm_xent(A, B, t)
+    d = torch.full((M,), 1.0 / M, device="cuda")
+    clean, _ = sg.gemm_xent_backward(d, A, B, t, lse0)
+    a = A.clone()
+    a[::4] = math.nan
+    a[4, :] = math.inf
+    loss, lse = sg.gemm_xent(a, B, t)
+    assert torch.equal(loss, want)
+    dA, none = sg.gemm_xent_backward(d, a, B, t, lse, need=(True, False))
+    assert none is None and torch.equal(dA, clean) and bool((dA[::4] == 0).all())
+    d[::4] = math.nan                       # (a mean over no tokens)
+    dA, _ = sg.gemm_xent_backward(d, a, B, t, lse, need=(True, False))
+    assert torch.equal(dA, clean)
+    # (the largest weight, which scales the gradients, is not theirs either)
+    a[1] = math.nan
+    loss, lse = sg.gemm_xent(a, B, t)
+    dA, _ = sg.gemm_xent_backward(d, a, B, t, lse, need=(True, False))
+    assert bool(torch.isnan(dA[1]).all()) and torch.equal(dA[2:], clean[2:])
+
+
 def test_losses_may_be_changed_in_place():
     A, B, t = ref.inputs(50, 300, 64, BF, 32)
     a = A.clone().requires_grad_()
