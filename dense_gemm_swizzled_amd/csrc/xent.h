@@ -103,6 +103,12 @@ __device__ __forceinline__ XentScale scale_of(float alpha, float most, float top
   return {(alpha < 0 ? -size : size) / most, a / size};
 }
 
+// log2(e) lse, or +inf where that is no number: exp(z - lse) is then 0 for every
+// logit, so that a factor of 0 stays 0 (lse is -inf where all logits are).
+__device__ __forceinline__ float base_of(float lse) {
+  return __builtin_fabsf(lse) < __builtin_inff() ? lse * kLog2e : __builtin_inff();
+}
+
 // The softmax's factor of a token's gradient: 0 where neither loss nor lse has a
 // weight, whatever the token's logits are (padding may hold anything), else NaN
 // where lse is no number.
@@ -258,8 +264,8 @@ struct XentGrad {
     const int64_t at = (int64_t)t - j.x.col0;
     return {r[0], r[1], r[2], t >= 0 && at >= 0 && at < 256 ? (int)at : -1};
   }
-  // (A logit of NaN counts as probability 0 here: its row has no weight, or the
-  // factor NaN.)
+  // (A logit of NaN counts as probability 0 here, and so do those of a row whose
+  // lse is no number: the row has no weight, or the factor NaN.)
   __device__ __forceinline__ static float value(float acc, float k, const Row& r) {
     return r.p * exp2_of(__builtin_fmaxf(__builtin_fmaf(acc, k, -r.l2), -FLT_MAX));
   }
@@ -373,7 +379,7 @@ struct XentGradFew {
     const int64_t at = (int64_t)t - j.x.col0;
     const int in = t >= 0 && at >= 0 && at < 256 ? (int)at : -1;
     const float lse = j.x.lse[m];
-    return {__shfl(lse * kLog2e, ml), __shfl(softmax_factor(dl, whole, f.up, lse), ml),
+    return {__shfl(base_of(lse), ml), __shfl(softmax_factor(dl, whole, f.up, lse), ml),
             __shfl(dl * f.up, ml), __shfl(in, ml)};
   }
 

@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kRowsThreads) xent_rows_kernel(const XentRows 
   const float2 w = factors_of(p, m, t);
   const float lse = p.lse[m];
   reinterpret_cast<f32x4*>(p.rows)[m] =
-      f32x4{lse * kLog2e, softmax_factor(w.x, w.y, f.up, lse), w.x * f.up,
+      f32x4{base_of(lse), softmax_factor(w.x, w.y, f.up, lse), w.x * f.up,
             __builtin_bit_cast(float, t)};
 }
 

@@ -122,6 +122,25 @@ def test_padding_holds_anything(M, N, K):
     assert bool(torch.isnan(dA[1]).all()) and torch.equal(dA[2:], clean[2:])
 
 
+@pytest.mark.parametrize("M,N", [(300, 5000), (2049, 20000), (40, 3000)])
+def test_padding_of_minus_infinity(M, N):
+    """A token without a weight whose logits are all -inf, lse too: its row of dA
+    is 0.  One with a weight has NaN."""
+    A, B, t = ref.inputs(M, N, 64, BF, M, ignored=0.0)
+    B[:, 0] = 1.0
+    A[3, 0] = A[4, 0] = -math.inf
+    t[3] = -1
+    t[4] = 7
+    loss, lse = sg.gemm_xent(A, B, t)
+    assert bool((lse[3:5] == -math.inf).all()) and float(loss[3]) == 0.0
+    d = torch.full((M,), 1.0 / M, device="cuda")
+    dA, _ = sg.gemm_xent_backward(d, A, B, t, lse, need=(True, False))
+    assert bool((dA[3] == 0).all()) and bool(torch.isnan(dA[4]).all())
+    d[4] = 0.0
+    dA, _ = sg.gemm_xent_backward(d, A, B, t, lse, need=(True, False))
+    assert bool((dA[3:5] == 0).all()) and bool(torch.isfinite(dA).all())
+
+
 def test_losses_may_be_changed_in_place():
     A, B, t = ref.inputs(50, 300, 64, BF, 32)
     a = A.clone().requires_grad_()
