@@ -869,11 +869,13 @@ int gemm_xent_backward_run(int64_t M, int64_t N, int64_t K, float alpha, const f
   if (!aligned4(dloss) || !aligned4(dlse) || !aligned4(lse))
     return fail(SG_ERR_ALIGN, "%s: dloss, dlse and lse must be 4-byte aligned", who);
   if (K == 0 || (!dA && !dB)) return ok();
-  if (M > 0 && N > 0 && !sg::xent_plan(M, N, K, ldb).fits)
-    return fail(SG_ERR_SHAPE, "%s: a gradient of more than 2^23 tiles of 256 x 256", who);
-  if (const int rc = workspace_check(who, workspace, workspace_bytes,
-                                     gemm_xent_backward_workspace_bytes(M, N, K, ldb)))
-    return rc;
+  sg::XentPlan plan{};  // (half a microsecond: made once)
+  if (M > 0 && N > 0) {
+    plan = sg::xent_plan(M, N, K, ldb);
+    if (!plan.fits)
+      return fail(SG_ERR_SHAPE, "%s: a gradient of more than 2^23 tiles of 256 x 256", who);
+  }
+  if (const int rc = workspace_check(who, workspace, workspace_bytes, plan.bytes)) return rc;
   sg::XentCall c = xent_call(M, N, K, alpha, A, lda, B, ldb, ab_dtype, targets, target_dtype,
                              workspace);
   c.lse = const_cast<float*>(lse);
@@ -883,7 +885,7 @@ int gemm_xent_backward_run(int64_t M, int64_t N, int64_t K, float alpha, const f
   c.ldda = ldda;
   c.dB = dB;
   c.lddb = lddb;
-  const hipError_t e = sg::launch_xent_backward(c, static_cast<hipStream_t>(stream));
+  const hipError_t e = sg::launch_xent_backward(c, plan, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail(e, who);
   return ok();
 }

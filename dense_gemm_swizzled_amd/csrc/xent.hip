@@ -446,7 +446,7 @@ hipError_t launch_xent(const XentCall& c, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_xent_backward(const XentCall& c, hipStream_t s) {
+hipError_t launch_xent_backward(const XentCall& c, const XentPlan& plan, hipStream_t s) {
   if (c.M == 0 || c.N == 0) {  // sums of nothing
     char* const D = static_cast<char*>(c.N == 0 ? c.dA : c.dB);
     const int64_t n = c.N == 0 ? c.M : c.N, chunks = c.K / 8;
@@ -455,7 +455,6 @@ hipError_t launch_xent_backward(const XentCall& c, hipStream_t s) {
                        chunks, 2 * (c.N == 0 ? c.ldda : c.lddb));
     return hipGetLastError();
   }
-  const XentPlan plan = xent_plan(c.M, c.N, c.K, c.ldb);
   const bool few = plan.rows > c.M;
   char* const w = static_cast<char*>(c.workspace);
   char* const G = w + plan.g_at;

@@ -133,6 +133,7 @@ inline XentPlan xent_plan(int64_t M, int64_t N, int64_t K, int64_t ldb) {
 }
 
 hipError_t launch_xent(const XentCall& c, hipStream_t s);
-hipError_t launch_xent_backward(const XentCall& c, hipStream_t s);
+// `plan`: xent_plan's, not used where M or N is 0.
+hipError_t launch_xent_backward(const XentCall& c, const XentPlan& plan, hipStream_t s);
 
 }  // namespace sg
