@@ -1187,7 +1187,7 @@ def moe_balance(logits, ids, *, score: str = "softmax", out=None, workspace=None
     fixed).  out: (loss, counts, tokens) to write, which carry no history: their
     gradient is a call of moe_balance_backward.  workspace: a uint8 tensor of at
     least moe_balance_workspace_bytes(T, E) bytes; by default one is allocated
-    for the call."""
+    for the call.  (A captured step with its backward: as for gemm_xent.)"""
     lib, T = _lib_torch()
     if out is None and logits.requires_grad and T.is_grad_enabled():
         return _balanced(logits, ids, score, workspace)
@@ -1326,7 +1326,11 @@ def gemm_xent(A, B, targets, *, alpha: float = 1.0, out=None, workspace=None):
     to write, which carry no history: their gradient is a call of
     gemm_xent_backward.  workspace: a uint8 tensor of at least
     gemm_xent_workspace_bytes(M, N, K) bytes; by default one is allocated for
-    the call."""
+    the call.
+
+    To capture a step with its backward into a graph, let no autograd graph of A
+    or B from outside the capture live: torch would accumulate their gradients on
+    the stream of that one."""
     lib, T = _lib_torch()
     alpha = float(alpha)
     if out is None and (A.requires_grad or B.requires_grad) and T.is_grad_enabled():
