@@ -676,8 +676,8 @@ int xent_check(const char* who, int64_t M, int64_t N, int64_t K, const void* A, 
       reinterpret_cast<uintptr_t>(targets) % (target_dtype == SG_I64 ? 8 : 4))
     return fail(SG_ERR_ALIGN, "%s: A and B must be 16-byte aligned, targets to its elements", who);
   const int64_t side = sg::tile_side(sg::xent_tile(M, N));
-  if (cdiv(M, side) * cdiv(N, side) > sg::kXentMaxTiles)
-    return fail(SG_ERR_SHAPE, "%s: more than 2^23 tiles of %lld x %lld", who, (long long)side,
+  if (cdiv(M, side) * cdiv(N, side) >= sg::kXentMaxTiles)
+    return fail(SG_ERR_SHAPE, "%s: 2^23 or more tiles of %lld x %lld", who, (long long)side,
                 (long long)side);
   return SG_OK;
 }
@@ -873,7 +873,7 @@ int gemm_xent_backward_run(int64_t M, int64_t N, int64_t K, float alpha, const f
   if (M > 0 && N > 0) {
     plan = sg::xent_plan(M, N, K, ldb);
     if (!plan.fits)
-      return fail(SG_ERR_SHAPE, "%s: a gradient of more than 2^23 tiles of 256 x 256", who);
+      return fail(SG_ERR_SHAPE, "%s: a gradient of 2^23 or more tiles of 256 x 256", who);
   }
   if (const int rc = workspace_check(who, workspace, workspace_bytes, plan.bytes)) return rc;
   sg::XentCall c = xent_call(M, N, K, alpha, A, lda, B, ldb, ab_dtype, targets, target_dtype,

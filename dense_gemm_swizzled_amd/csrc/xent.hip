@@ -4,6 +4,7 @@
 #include "xent.h"
 
 #include "launch.h"
+#include "twin16.h"
 #include "xent_plan.h"
 
 namespace sg {
@@ -170,7 +171,7 @@ __global__ void __launch_bounds__(64) xent_sum_kernel(const XentSum p) {
 }
 
 // dB on 256x256 tiles, and behind its tiles' workgroups those that add up dA's
-// parts, which then overlap (64 x 8192 x 1024: 11 us and 4 behind it).
+// parts, which then overlap (a launch of them alone takes 4 us or more).
 template <bool BF>
 __global__ void __launch_bounds__(512, 1) xent_head_kernel(const DenseParams p, const XentSum q) {
   using Tile = PingPong16Tile<BF, kSwzDefault, true, true, true, false, void, true>;
@@ -182,6 +183,20 @@ __global__ void __launch_bounds__(512, 1) xent_head_kernel(const DenseParams p, 
   }
   const TileJob j = dense_tile_job<256, 256, true, true>(p, blockIdx.x);
   Tile::run(smem, j, p.K, nullptr, SG_NONE, p.D, p.d_dtype, p.ldd);
+}
+
+// The same on the 256x128 tiles of few tokens.  (Without a sum q.M is 0.)
+template <bool BF>
+__global__ void __launch_bounds__(256, 2) xent_twin_kernel(const DenseParams p, const XentSum q) {
+  using Tile = TwinTile<BF>;
+  __shared__ __attribute__((aligned(4096))) char smem[Tile::kLdsBytes];
+  const int tiles = p.tiles_m * p.tiles_n;
+  if ((int)blockIdx.x >= tiles) {
+    sum_parts<BF ? SG_BF16 : SG_F16>(q, ((int64_t)(blockIdx.x - tiles) * 256 + threadIdx.x) * 4);
+    return;
+  }
+  const TileJob j = dense_tile_job<256, 128, true, true>(p, blockIdx.x);
+  Tile::run(smem, j, p.K, p.D, p.ldd);
 }
 
 // The gradient of the logits of few tokens, on 64x64 tiles; behind the tiles'
@@ -323,6 +338,16 @@ hipError_t go_few(const XentParams& p, const XentCall& c, char* twice, hipStream
   return hipGetLastError();
 }
 
+hipError_t go_twin(const DenseParams& d, const XentSum& q, bool bf16, hipStream_t s) {
+  static const char* const names[2] = {kernel_label("xent_twin_kernel", "f16"),
+                                       kernel_label("xent_twin_kernel", "bf16")};
+  last_kernel() = names[bf16];
+  const dim3 grid((unsigned)(d.tiles_m * d.tiles_n + cdiv(q.M * q.K, 4 * 256)));
+  if (bf16) hipLaunchKernelGGL((xent_twin_kernel<true>), grid, dim3(256), 0, s, d, q);
+  else hipLaunchKernelGGL((xent_twin_kernel<false>), grid, dim3(256), 0, s, d, q);
+  return hipGetLastError();
+}
+
 // The sum of dA's parts over one run of words.
 XentSum sum_of(const XentCall& c, const XentPlan& plan, int64_t v0, int64_t n) {
   char* const w = static_cast<char*>(c.workspace);
@@ -386,6 +411,7 @@ hipError_t hidden_gradient(const XentCall& c, const XentPlan& plan, const char* 
 struct HeadProduct {
   DenseParams d;
   TileShape tile;
+  bool twin;  // 256x128 tiles instead of 256x256
 };
 HeadProduct head_product(const XentCall& c, const XentPlan& plan, const char* G, int64_t v0,
                          int64_t n) {
@@ -407,6 +433,11 @@ HeadProduct head_product(const XentCall& c, const XentPlan& plan, const char* G,
                   // a group: 9080 | 9069 | 9150 | 9340 us; the others like 8 as well)
   h.tile = xent_back(d.M, d.N, d.K, 1).tile;
   set_tiles(d, h.tile);
+  h.twin = xent_twin(h.tile, d.K);
+  if (h.twin) {
+    d.tiles_n = (int)cdiv(d.N, 128);
+    d.group_m = 8;  // (128 x 32000 x 4096, all gradients: 222 us, 227 with 4)
+  }
   return h;
 }
 
@@ -510,10 +541,13 @@ hipError_t launch_xent_backward(const XentCall& c, const XentPlan& plan, hipStre
     HeadProduct h{};
     if (c.dB) h = head_product(c, plan, G, v0, n);
     const bool both = c.dA && c.dB && plan.parts && last && h.tile == kTile256 &&
-                      c.M * c.K <= kXentMaxTiles * 1024;  // (half a launch's workgroups)
+                      xent_joins((int64_t)h.d.tiles_m * h.d.tiles_n, h.twin ? 256 : 512,
+                                 c.M * c.K);
     if (e == hipSuccess && c.dA) e = hidden_gradient(c, plan, G, B, v0, n, !both, s);
     if (e != hipSuccess) break;
-    if (both)
+    if (h.twin)
+      e = go_twin(h.d, both ? sum_of(c, plan, v0, n) : XentSum{}, c.bf16, s);
+    else if (both)
       e = go_head(h.d, sum_of(c, plan, v0, n), c.bf16, s);
     else if (c.dB)
       e = launch_dense_any_k(h.tile, c.bf16, true, true, h.d, s);

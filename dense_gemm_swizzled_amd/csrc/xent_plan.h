@@ -37,7 +37,7 @@ inline int64_t tile_side(TileShape t) { return t == kTile256 ? 256 : t == kTile1
 constexpr int64_t kXentCUs = 256;
 constexpr int64_t kXentMaxLd = int64_t{1} << 22;   // a panel of 256 rows below 2^31 bytes
 constexpr int64_t kXentMaxRows = int64_t{1} << 22; // 256 columns of the gradient below 2^31 bytes
-constexpr int64_t kXentMaxTiles = int64_t{1} << 23;
+constexpr int64_t kXentMaxTiles = int64_t{1} << 23;  // (of 512 threads: 2^32)
 
 // Up to so many tokens the gradient of the logits is kept in two parts.
 constexpr int64_t kXentFew = 64;
@@ -67,7 +67,7 @@ inline int64_t xent_workspace(int64_t M, int64_t N) {
 struct XentBack {
   TileShape tile;
   int64_t splits;
-  bool fits;  // at most 2^23 workgroups
+  bool fits;  // fewer than 2^23 workgroups
 };
 inline XentBack xent_back(int64_t rows, int64_t cols, int64_t terms, int64_t most) {
   static const double start[3] = {5.0, 4.0, 2.5}, step[3] = {0.95, 0.45, 0.25};
@@ -78,7 +78,7 @@ inline XentBack xent_back(int64_t rows, int64_t cols, int64_t terms, int64_t mos
     const int64_t side = tile_side((TileShape)t);
     const int64_t tiles = cdiv(rows, side) * cdiv(cols, side);
     for (int64_t s = 1; s <= most && (s == 1 || 4 * s <= units); ++s) {
-      if (tiles * s > kXentMaxTiles) break;
+      if (tiles * s >= kXentMaxTiles) break;
       double us = (double)cdiv(tiles * s, kXentCUs) *
                   (start[t] + step[t] * (double)cdiv(units, s));
       if (s > 1) us += 3.0 + (double)s * (double)rows * (double)cols * 2e-6;
@@ -89,6 +89,19 @@ inline XentBack xent_back(int64_t rows, int64_t cols, int64_t terms, int64_t mos
     }
   }
   return best;
+}
+
+// dB of up to 512 terms: 256x128 tiles, two workgroups a CU, where the model says
+// 256x256, one (us of all gradients, twin | one: 8 tokens of 131072 x 2048 357 |
+// 398, 64 of 8192 x 1024 27.4 | 29.4, 128 of 32000 x 4096 222 | 237, 256 292 |
+// 306, 384 of 50257 x 768 152 | 163, 512 of 32000 x 4096 383 | 390, 1024 678 |
+// 668).
+inline bool xent_twin(TileShape tile, int64_t terms) { return tile == kTile256 && terms <= 512; }
+
+// Whether dA's `values` may be added up in the launch of dB's tiles, four a
+// thread: a launch has fewer than 2^32 threads.
+inline bool xent_joins(int64_t tiles, int64_t threads, int64_t values) {
+  return (tiles + cdiv(values, 4 * threads)) * threads < (int64_t{1} << 32);
 }
 
 // Backward: the words go in runs of `words`, for which the gradient of the

@@ -51,6 +51,14 @@ static void cross_entropy() {
   EXPECT_RC(run(33, 50, 64, P, 64, P, 64, SG_F16, P, SG_I32, F, Pc + 8, kBig), SG_ERR_ALIGN);
   EXPECT_RC(run(1 << 22, 1 << 30, 64, P, 64, P, 64, SG_F16, P, SG_I32, F, P, kBig),
             SG_ERR_SHAPE);
+  // 2^23 tiles, whose threads no launch counts
+  EXPECT_RC(run(1 << 20, 1 << 19, 64, P, 64, P, 64, SG_F16, P, SG_I32, F, P, kBig), SG_ERR_SHAPE);
+  EXPECT_RC(sg::xent_joins((1 << 23) - 1, 512, 2048), 0);
+  EXPECT_RC(sg::xent_joins((1 << 23) - 2, 512, 2048), 1);
+  EXPECT_RC(sg::xent_joins(1 << 22, 512, int64_t{1} << 33), 0);
+  EXPECT_RC(sg::xent_twin(sg::kTile256, 512), 1);
+  EXPECT_RC(sg::xent_twin(sg::kTile256, 513), 0);
+  EXPECT_RC(sg::xent_twin(sg::kTile128, 64), 0);
   EXPECT_RC(run(0, 50, 64, nullptr, 64, P, 64, SG_F16, nullptr, SG_I32, nullptr, nullptr, 0),
             SG_OK);
   auto back = [](int64_t M, int64_t lda, const float* dl, const float* dlse, void* dA,
@@ -75,7 +83,7 @@ static void cross_entropy() {
 }
 
 // The plan of the gradient: runs that cover the words, operands below 2^31
-// bytes, areas that follow each other on 16-byte borders, launches of at most
+// bytes, areas that follow each other on 16-byte borders, launches of fewer than
 // 2^23 workgroups.
 static void plans() {
   for (int64_t M = 1; M < sg::kXentMaxRows; M = 3 * M + 5)
@@ -96,8 +104,10 @@ static void plans() {
         const int64_t side = sg::tile_side(p.hidden.tile);
         const int64_t d = sg::tile_side(sg::xent_back(run, K, p.rows, 1).tile);
         // (a gradient of more tiles than a launch has is refused)
-        EXPECT_RC(cdiv(p.rows, side) * cdiv(K, side) * p.hidden.splits <= sg::kXentMaxTiles &&
-                      cdiv(run, d) * cdiv(K, d) <= sg::kXentMaxTiles, p.fits);
+        EXPECT_RC(cdiv(p.rows, side) * cdiv(K, side) * p.hidden.splits < sg::kXentMaxTiles &&
+                      cdiv(run, d) * cdiv(K, d) < sg::kXentMaxTiles, p.fits);
+        // (fewer than 2^32 threads, with half the width of a tile too)
+        if (p.fits && d == 256) EXPECT_RC(cdiv(run, 256) * cdiv(K, 128) * 256 < kMaxExtent * 2, 1);
         if (!p.fits)
           EXPECT_RC(gemm_xent_backward_run(M, N, K, 1.0f, F, nullptr, P, K, P, ldb, SG_BF16, P,
                                            SG_I64, F, P, K, nullptr, K, P, kBig, nullptr),

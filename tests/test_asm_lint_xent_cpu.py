@@ -44,6 +44,15 @@ def test_kernels_keep_their_m0(listing):
         assert not bad, f"{name}: {bad[:5]}"
 
 
+def test_joined_kernels_keep_their_m0(listing):
+    """Products whose launch does something else as well."""
+    found = {n: b for n, b in kernels(listing) if re.search(r"xent_(head|twin|few)_kernel", n)}
+    assert len(found) == 6, sorted(found)
+    for name, body in found.items():
+        bad, n = lint(body)
+        assert n > 0 and not bad, f"{name}: {n} loads, {bad[:5]}"
+
+
 def test_no_kernel_spills(listing):
     spills = re.findall(r"\.vgpr_spill_count:\s*(\d+)", listing)
     assert len(spills) >= 30 and set(spills) == {"0"}
