@@ -178,6 +178,9 @@ struct DeepTile {
       }
     };
 
+    [[maybe_unused]] typename EpiPre32<Epi, kFM>::type pre;
+    if constexpr (!std::is_void<Epi>::value)
+      pre = Epi::template fetch32<kFM, Base::kWM>(j, lane, wm);
 #pragma unroll
     for (int t = 0; t < kStages - 1; ++t) issue(t);
 
@@ -268,8 +271,8 @@ struct DeepTile {
 
     if constexpr (!std::is_void<Epi>::value) {
       PingPongTile<IsBF16, kSwzDefault>::barrier();  // every wave's reads are done
-      Epi::template finish32<kFM, kFN, Base::kWM, Base::kWN, 2>(acc, j, smem, D, ldd, lane, wm,
-                                                                wn);
+      Epi::template finish32<kFM, kFN, Base::kWM, Base::kWN, 2>(acc, j, pre, smem, D, ldd, lane,
+                                                                wm, wn);
       return;
     }
     if (d_dtype == SG_F32 && C == nullptr) {

@@ -334,6 +334,17 @@ __device__ __forceinline__ void epilogue16(const f32x4 (&acc)[NI][NJ], const Til
 // Waves = 4: one wave per SIMD, each wave owns a (BM/2) x (BN/2) block.
 // Waves = 8: two waves per SIMD (the hardware interleaves them, and twice as
 // many waves issue the direct-to-LDS loads), each owning (BM/2) x (BN/4).
+// What an Epi takes from memory before the mainloop, so that its latency is not
+// the tile's last (nothing without one).
+template <class Epi, int FM>
+struct EpiPre32 {
+  using type = typename Epi::template Rows32<FM>;
+};
+template <int FM>
+struct EpiPre32<void, FM> {
+  struct type {};
+};
+
 // Epi: what is done with the sums instead of storing D (xent.h), or void.
 template <int BM, int BN, int Elem, bool AMn, bool BMn, int Swz, int Waves = 4, class Epi = void>
 struct GemmTile {
@@ -525,6 +536,9 @@ struct GemmTile {
 #pragma unroll
       for (int k = 0; k < kFN; ++k) acc[i][k] = f32x16{};
 
+    [[maybe_unused]] typename EpiPre32<Epi, kFM>::type pre;
+    if constexpr (!std::is_void<Epi>::value) pre = Epi::template fetch32<kFM, kWM>(j, lane, wm);
+
     const int Ki = (int)K;
     const int kt_total = (Ki + kBK - 1) / kBK;
     ALoader la;
@@ -556,7 +570,8 @@ struct GemmTile {
 
     if constexpr (!std::is_void<Epi>::value) {
       __syncthreads();  // every wave's reads are done
-      Epi::template finish32<kFM, kFN, kWM, kWN, kWavesN>(acc, j, s0, D, ldd, lane, wm, wn);
+      Epi::template finish32<kFM, kFN, kWM, kWN, kWavesN>(acc, j, pre, s0, D, ldd, lane, wm,
+                                                               wn);
       return;
     }
     epilogue(acc, j, C, c_dtype, D, d_dtype, ldd, lane, wm, wn);
@@ -687,7 +702,9 @@ __device__ __forceinline__ TileJob dense_tile_job(const DenseParams& p, int wg) 
     j.b_bytes = p.K > 0 ? (uint32_t)((j.n_valid - 1) * p.ldb * es + p.K * es) : 0u;
   }
   j.ldc = p.ldc;
-  j.alpha = p.alpha_dev ? p.alpha * *p.alpha_dev : p.alpha;
+  // (a scalar load: a vector load's latency would be waited for here)
+  using Scalar = const __attribute__((address_space(4))) float;
+  j.alpha = p.alpha_dev ? p.alpha * *(Scalar*)(uintptr_t)p.alpha_dev : p.alpha;
   j.beta = p.beta;
   j.d_row0 = m0;
   j.n0 = n0;

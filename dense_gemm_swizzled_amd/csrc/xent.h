@@ -68,11 +68,23 @@ struct XentSum {
 
 __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// Token m's target, -1 where it is no word of [0, N).
-__device__ __forceinline__ int target_of(const void* t, bool wide, int64_t m, int64_t N) {
-  const int64_t v = wide ? static_cast<const int64_t*>(t)[m]
-                         : (int64_t) static_cast<const int32_t*>(t)[m];
+// Token m's target as it lies in memory.  Two loads whatever its type: a branch
+// would wait for each token's load before the next.
+struct TargetWords {
+  uint32_t low, high;  // (high: low again for 32-bit targets)
+};
+__device__ __forceinline__ TargetWords load_target(const void* t, bool wide, int64_t m) {
+  const uint32_t* const p = static_cast<const uint32_t*>(t) + (wide ? 2 * m : m);
+  return {p[0], p[wide ? 1 : 0]};
+}
+
+// The target, -1 where it is no word of [0, N).
+__device__ __forceinline__ int target_of(const TargetWords& w, bool wide, int64_t N) {
+  const int64_t v = wide ? (int64_t)((uint64_t)w.high << 32 | w.low) : (int64_t)(int32_t)w.low;
   return v >= 0 && v < N ? (int)v : -1;
+}
+__device__ __forceinline__ int target_of(const void* t, bool wide, int64_t m, int64_t N) {
+  return target_of(load_target(t, wide, m), wide, N);
 }
 
 // (maximum, sum of exp(z - maximum)) of two sets of logits from those of each.
@@ -149,23 +161,36 @@ struct XentStats {
     *reinterpret_cast<float2*>(j.x.part + 2 * (int64_t)r) = make_float2(m, s);
   }
 
-  // The column, inside the tile, of the target of tile row ml (or below 0, or
-  // past the tile).
-  __device__ __forceinline__ static int column(const TileJob& j, int ml) {
-    const int64_t t = (int64_t)target_of(j.x.targets, j.x.wide, min(ml, j.m_valid - 1),
-                                         j.x.words) - j.x.col0;
+  // The column, inside the tile, of a target (or below 0, or past the tile).
+  __device__ __forceinline__ static int column(const TileJob& j, const TargetWords& w) {
+    const int64_t t = (int64_t)target_of(w, j.x.wide, j.x.words) - j.x.col0;
     return t >= 0 && t < 256 ? (int)t : -1;
   }
+  // The target of tile row ml.
+  __device__ __forceinline__ static TargetWords fetch(const TileJob& j, int ml) {
+    return load_target(j.x.targets, j.x.wide, min(ml, j.m_valid - 1));
+  }
 
-  // The targets' columns of a lane's rows, loaded before the mainloop so that
-  // their latency is not the tile's last.
+  // The targets of a lane's rows, loaded before the mainloop so that their latency
+  // is not the tile's last, and first looked at behind it.
   struct Rows16 {
-    int at[8];
+    TargetWords t[8];
   };
   __device__ __forceinline__ static Rows16 fetch16(const TileJob& j, int lane, int g) {
     Rows16 r;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r.at[i] = column(j, 128 * g + 16 * i + (lane & 15));
+    for (int i = 0; i < 8; ++i) r.t[i] = fetch(j, 128 * g + 16 * i + (lane & 15));
+    return r;
+  }
+  template <int FM>
+  struct Rows32 {
+    TargetWords t[FM];
+  };
+  template <int FM, int WM>
+  __device__ __forceinline__ static Rows32<FM> fetch32(const TileJob& j, int lane, int wm) {
+    Rows32<FM> r;
+#pragma unroll
+    for (int fm = 0; fm < FM; ++fm) r.t[fm] = fetch(j, WM * wm + 32 * fm + (lane & 31));
     return r;
   }
 
@@ -191,7 +216,7 @@ struct XentStats {
           for (int e = 0; e < 4 * Tile::kJ; ++e)
             if (c0 + 16 * (e >> 2) + (e & 3) >= j.n_valid) v[e] = -__builtin_inff();
         }
-        const int at = rows.at[i] - c0;  // 16 jn + e of the target
+        const int at = column(j, rows.t[i]) - c0;  // 16 jn + e of the target
         if (at >= 0 && at < 64 && (at & 12) == 0 && ml < j.m_valid) {
           float z = 0.0f;
 #pragma unroll
@@ -211,8 +236,8 @@ struct XentStats {
   // 32 fn + 8q + 4(l/32) .. +3 in registers 4q .. 4q+3.
   template <int FM, int FN, int WM, int WN, int WavesN>
   __device__ __forceinline__ static void finish32(f32x16 (&acc)[FM][FN], const TileJob& j,
-                                                  char* smem, void*, int64_t, int lane, int wm,
-                                                  int wn) {
+                                                  const Rows32<FM>& rows, char* smem, void*,
+                                                  int64_t, int lane, int wm, int wn) {
     constexpr int kRows = 2 * WM;
     float* area = reinterpret_cast<float*>(smem);
     const int c0 = WN * wn + 4 * (lane >> 5);
@@ -228,7 +253,7 @@ struct XentStats {
           if (c0 + 32 * fn + 8 * (r >> 2) + (r & 3) >= j.n_valid)
             v[16 * fn + r] = -__builtin_inff();
         }
-      const int at = column(j, ml) - c0;
+      const int at = column(j, rows.t[fm]) - c0;
       if (at >= 0 && at < WN && (at & 4) == 0 && ml < j.m_valid) {
         float z = 0.0f;
 #pragma unroll
@@ -258,8 +283,10 @@ struct XentGrad {
     float l2, p, t;
     int at;
   };
-  __device__ __forceinline__ static Row row_of(const TileJob& j, int ml) {
-    const f32x4 r = *reinterpret_cast<const f32x4*>(j.x.rows + 4 * (int64_t)min(ml, j.m_valid - 1));
+  __device__ __forceinline__ static f32x4 fetch(const TileJob& j, int ml) {
+    return *reinterpret_cast<const f32x4*>(j.x.rows + 4 * (int64_t)min(ml, j.m_valid - 1));
+  }
+  __device__ __forceinline__ static Row row_of(const TileJob& j, const f32x4& r) {
     const int t = __builtin_bit_cast(int, (float)r[3]);
     const int64_t at = (int64_t)t - j.x.col0;
     return {r[0], r[1], r[2], t >= 0 && at >= 0 && at < 256 ? (int)at : -1};
@@ -272,12 +299,23 @@ struct XentGrad {
 
   // A lane's rows, loaded before the mainloop.
   struct Rows16 {
-    Row row[8];
+    f32x4 row[8];
   };
   __device__ __forceinline__ static Rows16 fetch16(const TileJob& j, int lane, int g) {
     Rows16 r;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r.row[i] = row_of(j, 128 * g + 16 * i + (lane & 15));
+    for (int i = 0; i < 8; ++i) r.row[i] = fetch(j, 128 * g + 16 * i + (lane & 15));
+    return r;
+  }
+  template <int FM>
+  struct Rows32 {
+    f32x4 row[FM];
+  };
+  template <int FM, int WM>
+  __device__ __forceinline__ static Rows32<FM> fetch32(const TileJob& j, int lane, int wm) {
+    Rows32<FM> r;
+#pragma unroll
+    for (int fm = 0; fm < FM; ++fm) r.row[fm] = fetch(j, WM * wm + 32 * fm + (lane & 31));
     return r;
   }
 
@@ -289,20 +327,20 @@ struct XentGrad {
     if (j.m_valid <= 128 * g) return;
     const int c0 = 64 * w4 + 4 * (lane >> 4);
     const float k = j.alpha * kLog2e;
-    const Row (&r)[8] = rows.row;
 #pragma unroll
     for (int i = 0; i < Tile::kI; ++i) {
+      const Row r = row_of(j, rows.row[i]);
 #pragma unroll
       for (int jn = 0; jn < Tile::kJ; ++jn)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][jn][e] = value(acc[i][jn][e], k, r[i]);
-      const int at = r[i].at - c0;
+        for (int e = 0; e < 4; ++e) acc[i][jn][e] = value(acc[i][jn][e], k, r);
+      const int at = r.at - c0;
       if (at >= 0 && at < 64 && (at & 12) == 0) {
 #pragma unroll
         for (int jn = 0; jn < Tile::kJ; ++jn)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (at == 16 * jn + e) acc[i][jn][e] -= r[i].t;
+            if (at == 16 * jn + e) acc[i][jn][e] -= r.t;
       }
       if (j.n_valid < 256) {
 #pragma unroll
@@ -335,9 +373,9 @@ struct XentGrad {
   }
 
   template <int FM, int FN, int WM, int WN, int WavesN>
-  __device__ __forceinline__ static void finish32(f32x16 (&acc)[FM][FN], const TileJob& j, char*,
-                                                  void* D, int64_t ldd, int lane, int wm,
-                                                  int wn) {
+  __device__ __forceinline__ static void finish32(f32x16 (&acc)[FM][FN], const TileJob& j,
+                                                  const Rows32<FM>& rows, char*, void* D,
+                                                  int64_t ldd, int lane, int wm, int wn) {
     const int c0 = WN * wn + 4 * (lane >> 5);
     const float k = j.alpha * kLog2e;
     const u32x2 none{};
@@ -345,7 +383,7 @@ struct XentGrad {
     for (int fm = 0; fm < FM; ++fm) {
       const int ml = WM * wm + 32 * fm + (lane & 31);
       if (ml >= j.m_valid) continue;
-      const Row r = row_of(j, ml);
+      const Row r = row_of(j, rows.row[fm]);
 #pragma unroll
       for (int fn = 0; fn < FN; ++fn)
 #pragma unroll
@@ -366,11 +404,22 @@ struct XentGrad {
 template <int DD>
 struct XentGradFew {
   using Grad = XentGrad<DD>;
-  __device__ __forceinline__ static typename Grad::Row row_of(const TileJob& j, int lane, int ml) {
+  template <int FM>
+  struct Rows32 {
+    TargetWords t;
+    float dloss, dlse, lse;
+  };
+  template <int FM, int WM>
+  __device__ __forceinline__ static Rows32<FM> fetch32(const TileJob& j, int lane, int) {
     const int m = min(lane, j.m_valid - 1);
-    const int t = target_of(j.x.targets, j.x.wide, m, j.x.words);
-    const float given = j.x.dloss[m], dl = t >= 0 ? given : 0.0f;
-    const float whole = j.x.dlse ? dl + j.x.dlse[m] : dl;
+    return {load_target(j.x.targets, j.x.wide, m), j.x.dloss[m],
+            (j.x.dlse ? j.x.dlse : j.x.dloss)[m], j.x.lse[m]};
+  }
+  __device__ __forceinline__ static typename Grad::Row row_of(const TileJob& j,
+                                                              const Rows32<1>& own, int ml) {
+    const int t = target_of(own.t, j.x.wide, j.x.words);
+    const float dl = t >= 0 ? own.dloss : 0.0f;
+    const float whole = j.x.dlse ? dl + own.dlse : dl;
     const float most = lane_reduce<64>(__builtin_fabsf(dl), OpMax{});
     const float top =
         lane_reduce<64>(__builtin_fabsf(dl) + __builtin_fabsf(whole), OpMax{});
@@ -378,19 +427,18 @@ struct XentGradFew {
     if (j.x.col0 == 0 && threadIdx.x == 0) j.x.scale[0] = f.down;
     const int64_t at = (int64_t)t - j.x.col0;
     const int in = t >= 0 && at >= 0 && at < 256 ? (int)at : -1;
-    const float lse = j.x.lse[m];
-    return {__shfl(base_of(lse), ml), __shfl(softmax_factor(dl, whole, f.up, lse), ml),
+    return {__shfl(base_of(own.lse), ml), __shfl(softmax_factor(dl, whole, f.up, own.lse), ml),
             __shfl(dl * f.up, ml), __shfl(in, ml)};
   }
 
   template <int FM, int FN, int WM, int WN, int WavesN>
-  __device__ __forceinline__ static void finish32(f32x16 (&acc)[FM][FN], const TileJob& j, char*,
-                                                  void* D, int64_t ldd, int lane, int wm,
-                                                  int wn) {
+  __device__ __forceinline__ static void finish32(f32x16 (&acc)[FM][FN], const TileJob& j,
+                                                  const Rows32<FM>& own, char*, void* D,
+                                                  int64_t ldd, int lane, int wm, int wn) {
     static_assert(FM == 1 && FN == 1 && 2 * WM == kWaveSize, "a row for each lane");
     const int ml = WM * wm + (lane & 31), c0 = WN * wn + 4 * (lane >> 5);
     const float k = j.alpha * kLog2e;
-    const typename Grad::Row r = row_of(j, lane, ml);
+    const typename Grad::Row r = row_of(j, own, ml);
     if (ml >= j.m_valid) return;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
