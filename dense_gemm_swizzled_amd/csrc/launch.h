@@ -22,9 +22,8 @@ constexpr int kCUs = 256;  // MI355X compute units
 // run on the ping-pong (`pingpong`: K-major operands, or a K that its loaders
 // of MN-major operands take) and the 128x128 tiles would need three or more
 // rounds of the CUs, one partial round of the ping-pong is faster (bf16 on
-// MI355X, TFLOP/s 256 vs 128 tiles: 3072^3 1056 vs 694, 3584^3 1337 vs 911,
-// 3072x3072x1024 846 vs 585), though not against one or two rounds of 128x128
-// tiles (2560^3 753 vs 847, 2048x4096x4096 934 vs 1041).
+// MI355X, TFLOP/s 256 vs 128 tiles: 3584^3 1337 vs 911), though not against one
+// or two rounds of 128x128 tiles (2560^3 753 vs 847, 2048x4096x4096 934 vs 1041).
 // `fits256`: 256-row panels stay within 32-bit buffer offsets.
 inline TileShape pick_dense_tile(int64_t M, int64_t N, bool pingpong, bool fits256) {
   auto tiles = [&](int64_t side) { return ((M + side - 1) / side) * ((N + side - 1) / side); };
