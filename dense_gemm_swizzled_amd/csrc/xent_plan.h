@@ -105,10 +105,11 @@ inline bool xent_joins(int64_t tiles, int64_t threads, int64_t values) {
 }
 
 // Backward: the words go in runs of `words`, for which the gradient of the
-// logits, 16 bits each (twice for few tokens), takes up to 512 MB and an operand
-// of a product stays below 2^31 bytes.  Workspace: the tokens' terms, the scale,
-// the gradient of one run, A twice for few tokens, and the sums of dA: one for
-// each split, and with several runs one more.
+// logits, 16 bits each (twice for few tokens), takes up to 512 MB, a row of it
+// fewer than 2^22 values (dB's tiles look up to 96 rows past the last by 32-bit
+// offsets) and an operand of a product stays below 2^31 bytes.  Workspace: the
+// tokens' terms, the scale, the gradient of one run, A twice for few tokens, and
+// the sums of dA: one for each split, and with several runs one more.
 constexpr int kXentMostParts = 256;  // workgroups that look for the largest |dloss|
 constexpr int64_t kXentMostSplits = 32;
 struct XentPlan {
@@ -125,6 +126,7 @@ inline XentPlan xent_plan(int64_t M, int64_t N, int64_t K, int64_t ldb) {
   p.rows = few ? 2 * M : M;
   int64_t most = std::max<int64_t>((int64_t{1} << 28) / p.rows, 256);
   most = std::min(most, ((int64_t{1} << 30) - 1) / ldb);
+  most = std::min(most, kXentMaxLd - 256);  // (the pitch of g as that of A and B)
   most = std::max<int64_t>(most / 256 * 256, 256);
   p.words = cdiv(cdiv(N, cdiv(N, most)), 256) * 256;
   const int64_t run = std::min(p.words, N);
