@@ -108,10 +108,11 @@ struct XentScale {
 __device__ __forceinline__ XentScale scale_of(float alpha, float most, float top) {
   if (!(most > 0x1p-20f * top)) most = top;  // (dlse alone)
   const float a = __builtin_fabsf(alpha) * most;
-  if (!(a > 0x1p-100f && a < 0x1p100f)) return {alpha, 1.0f};
-  int e;
+  if (!(a >= FLT_MIN && a < 0x1p100f)) return {alpha, 1.0f};
+  int e, em;
   frexpf(top / most, &e);  // top / most in [2^(e-1), 2^e)
-  const float size = ldexpf(1.0f, 14 - e);
+  frexpf(most, &em);       // (`up` stays below 2^120, however small `most` is)
+  const float size = ldexpf(1.0f, min(14 - e, em + 119));
   return {(alpha < 0 ? -size : size) / most, a / size};
 }
 
