@@ -116,6 +116,14 @@ __device__ __forceinline__ XentScale scale_of(float alpha, float most, float top
   return {(alpha < 0 ? -size : size) / most, a / size};
 }
 
+// What a token's weights count for the scale: |dloss| and |dloss| + |dloss + dlse|,
+// or nothing where one is no number, which only its own terms become then.
+__device__ __forceinline__ float2 weight_of(float dl, float whole) {
+  const float a = __builtin_fabsf(dl), b = __builtin_fabsf(whole);
+  const bool on = a < __builtin_inff() && b < __builtin_inff();
+  return make_float2(on ? a : 0.0f, on ? a + b : 0.0f);
+}
+
 // log2(e) lse, or +inf where that is no number: exp(z - lse) is then 0 for every
 // logit, so that a factor of 0 stays 0 (lse is -inf where all logits are).
 __device__ __forceinline__ float base_of(float lse) {
@@ -421,10 +429,9 @@ struct XentGradFew {
     const int t = target_of(own.t, j.x.wide, j.x.words);
     const float dl = t >= 0 ? own.dloss : 0.0f;
     const float whole = j.x.dlse ? dl + own.dlse : dl;
-    const float most = lane_reduce<64>(__builtin_fabsf(dl), OpMax{});
-    const float top =
-        lane_reduce<64>(__builtin_fabsf(dl) + __builtin_fabsf(whole), OpMax{});
-    const XentScale f = scale_of(j.alpha, most, top);
+    const float2 size = weight_of(dl, whole);
+    const XentScale f = scale_of(j.alpha, lane_reduce<64>(size.x, OpMax{}),
+                                 lane_reduce<64>(size.y, OpMax{}));
     if (j.x.col0 == 0 && threadIdx.x == 0) j.x.scale[0] = f.down;
     const int64_t at = (int64_t)t - j.x.col0;
     const int in = t >= 0 && at >= 0 && at < 256 ? (int)at : -1;

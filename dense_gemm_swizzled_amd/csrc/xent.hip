@@ -91,8 +91,9 @@ __device__ __forceinline__ float2 largest(const XentRows& p, int64_t first, int6
 #pragma unroll 4
   for (int64_t m = first; m < p.M; m += step) {
     const float2 f = factors_of(p, m, target_of(p.targets, p.wide, m, p.N));
-    most = __builtin_fmaxf(most, __builtin_fabsf(f.x));
-    top = __builtin_fmaxf(top, __builtin_fabsf(f.x) + __builtin_fabsf(f.y));
+    const float2 size = weight_of(f.x, f.y);
+    most = __builtin_fmaxf(most, size.x);
+    top = __builtin_fmaxf(top, size.y);
   }
   return over_workgroup(most, top, area);
 }

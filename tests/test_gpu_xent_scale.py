@@ -34,3 +34,23 @@ def test_weights_and_factors_far_from_one(M, w, alpha, only):
     wA, wB, bA, bB = ref.backward(d, A, B, t, alpha, dlse)
     close(dA, wA, bA, "dA")
     close(dB, wB, bB, "dB")
+
+
+@pytest.mark.parametrize("M", [40, 300, 9000])
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("where", ["dloss", "dlse"])
+def test_a_weight_that_is_no_number(M, dtype, bad, where):
+    """One token's weight is infinite or NaN: its own row of dA is no number, and
+    the other rows are what they are without it."""
+    A, B, t = ref.inputs(M, 900, 64, dtype, 3, ignored=0.0)
+    _, lse = sg.gemm_xent(A, B, t)
+    d = torch.full((M,), 1e-4, device="cuda")
+    z = torch.full((M,), 1e-5, device="cuda")
+    want, _, bound, _ = ref.backward(d, A, B, t, 1.0, z)
+    (d if where == "dloss" else z)[3] = bad
+    keep = torch.ones(M, dtype=torch.bool, device="cuda")
+    keep[3] = False
+    dA, _ = sg.gemm_xent_backward(d, A, B, t, lse, dlse=z, need=(True, False))
+    close(dA[keep], want[keep], bound[keep], "dA")
+    assert not bool(torch.isfinite(dA[3]).any())
