@@ -1323,8 +1323,8 @@ def gemm_xent(A, B, targets, *, alpha: float = 1.0, out=None, workspace=None):
     target lies outside [0, N).
 
     Where A or B requires a gradient, loss and lse carry it.  out: (loss, lse)
-    to write, which carry no history: their gradient is a call of
-    gemm_xent_backward.  workspace: a uint8 tensor of at least
+    to write, which overlap nothing and carry no history: their gradient is a
+    call of gemm_xent_backward.  workspace: a uint8 tensor of at least
     gemm_xent_workspace_bytes(M, N, K) bytes; by default one is allocated for
     the call.
 
@@ -1361,7 +1361,8 @@ def gemm_xent_backward(dloss, A, B, targets, lse, *, alpha: float = 1.0, dlse=No
     its lse (None: zero).  lse is gemm_xent's.
 
     need: which of the two are computed; the other is None.  out: (dA, dB) to
-    write (None: a new tensor), rows padded or not.  workspace: a uint8 tensor of
+    write (None: a new tensor), rows padded or not, that overlap no input and not
+    each other.  workspace: a uint8 tensor of
     at least gemm_xent_backward_workspace_bytes(M, N, K, B.stride(0)) bytes."""
     lib, T = _lib_torch()
     M, N, K, lda, ldb, dt, tt = _xent_args(A, B, targets)

@@ -711,6 +711,36 @@ int workspace_check(const char* who, const void* workspace, int64_t bytes, int64
   return SG_OK;
 }
 
+// Rows of a call's argument in memory, in bytes (a vector: one row).
+struct Area {
+  const char* name;
+  const void* at;
+  int64_t rows, pitch, width;
+};
+
+// Whether two areas have a byte in common.  Rows of one pitch may lie side by
+// side; of two pitches only areas one behind the other are known to be apart.
+bool overlap(const Area& a, const Area& b) {
+  if (!a.at || !b.at || a.rows <= 0 || b.rows <= 0 || a.width <= 0 || b.width <= 0) return false;
+  const uintptr_t pa = reinterpret_cast<uintptr_t>(a.at), pb = reinterpret_cast<uintptr_t>(b.at);
+  if (pa > pb) return overlap(b, a);
+  const uintptr_t from = pb - pa;
+  if (from >= (uintptr_t)(a.rows - 1) * a.pitch + a.width) return false;
+  const int64_t pitch = a.rows > 1 ? a.pitch : b.pitch;
+  if (a.rows > 1 && b.rows > 1 && a.pitch != b.pitch) return true;
+  const int64_t column = (int64_t)(from % (uintptr_t)pitch);
+  return column < a.width || column + b.width > pitch;
+}
+
+// No output (the first `outputs` areas) overlaps another area.
+int overlap_check(const char* who, const Area* areas, int outputs, int all) {
+  for (int i = 0; i < outputs; ++i)
+    for (int k = i + 1; k < all; ++k)
+      if (overlap(areas[i], areas[k]))
+        return fail(SG_ERR_ALIGN, "%s: %s overlaps %s", who, areas[i].name, areas[k].name);
+  return SG_OK;
+}
+
 // The checks that the forward and backward routing share.
 int route_check(const char* who, int64_t T, int E, int top_k, const void* logits, int64_t ldl,
                 int dtype, int score) {
@@ -838,6 +868,14 @@ int gemm_xent_run(int64_t M, int64_t N, int64_t K, float alpha, const void* A, i
   if (const int rc = workspace_check(who, workspace, workspace_bytes,
                                      sg::xent_workspace(M, N)))
     return rc;
+  const int64_t of_targets = M * (target_dtype == SG_I64 ? 8 : 4);
+  const Area areas[] = {{"loss", loss, 1, 4 * M, 4 * M},
+                        {"lse", lse, 1, 4 * M, 4 * M},
+                        {"workspace", workspace, 1, workspace_bytes, sg::xent_workspace(M, N)},
+                        {"A", A, M, 2 * lda, 2 * K},
+                        {"B", B, N, 2 * ldb, 2 * K},
+                        {"targets", targets, 1, of_targets, of_targets}};
+  if (const int rc = overlap_check(who, areas, 3, 6)) return rc;
   sg::XentCall c = xent_call(M, N, K, alpha, A, lda, B, ldb, ab_dtype, targets, target_dtype,
                              workspace);
   c.loss = loss;
@@ -876,6 +914,17 @@ int gemm_xent_backward_run(int64_t M, int64_t N, int64_t K, float alpha, const f
       return fail(SG_ERR_SHAPE, "%s: a gradient of 2^23 or more tiles of 256 x 256", who);
   }
   if (const int rc = workspace_check(who, workspace, workspace_bytes, plan.bytes)) return rc;
+  const int64_t of_targets = M * (target_dtype == SG_I64 ? 8 : 4);
+  const Area areas[] = {{"dA", dA, M, 2 * ldda, 2 * K},
+                        {"dB", dB, N, 2 * lddb, 2 * K},
+                        {"workspace", workspace, 1, plan.bytes, plan.bytes},
+                        {"A", A, M, 2 * lda, 2 * K},
+                        {"B", B, N, 2 * ldb, 2 * K},
+                        {"targets", targets, 1, of_targets, of_targets},
+                        {"dloss", dloss, 1, 4 * M, 4 * M},
+                        {"dlse", dlse, 1, 4 * M, 4 * M},
+                        {"lse", lse, 1, 4 * M, 4 * M}};
+  if (const int rc = overlap_check(who, areas, 3, 9)) return rc;
   sg::XentCall c = xent_call(M, N, K, alpha, A, lda, B, ldb, ab_dtype, targets, target_dtype,
                              workspace);
   c.lse = const_cast<float*>(lse);

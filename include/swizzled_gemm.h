@@ -514,8 +514,9 @@ int moe_balance_backward_run(int64_t T, int E, const float* dloss, const void* l
  *            nothing between calls; calls that may run at the same time need
  *            their own.
  * The result depends on nothing but the arguments (no atomics).  Errors:
- * SG_ERR_NULL, SG_ERR_ALIGN, SG_ERR_SHAPE (also 2^23 tiles or more),
- * SG_ERR_DTYPE, SG_ERR_HIP.
+ * SG_ERR_NULL, SG_ERR_ALIGN (also an output or the workspace that overlaps
+ * another argument), SG_ERR_SHAPE (also 2^23 tiles or more), SG_ERR_DTYPE,
+ * SG_ERR_HIP.
  */
 int gemm_xent_run(int64_t M, int64_t N, int64_t K, float alpha, const void* A, int64_t lda,
                   const void* B, int64_t ldb, int ab_dtype, const void* targets, int target_dtype,
@@ -540,7 +541,9 @@ int64_t gemm_xent_workspace_bytes(int64_t M, int64_t N, int64_t K);
  *   lse      fp32 [M] as gemm_xent_run wrote it for the same A, B and alpha.
  *   dA       ab_dtype [M][ldda], or NULL: not wanted;  dB  ab_dtype [N][lddb],
  *            or NULL.  16-byte aligned, row pitches too.  Both are overwritten
- *            whole (zeros where M or N is 0).
+ *            whole (zeros where M or N is 0).  Neither may overlap an input, so
+ *            neither gradient replaces its operand (SG_ERR_ALIGN); rows of one
+ *            pitch may lie side by side.
  *   workspace  DEVICE, gemm_xent_backward_workspace_bytes(M, N, K, ldb) bytes,
  *            16-byte aligned; as above.  It is 2 * M bytes a word of a run (at
  *            most 512 MB or 256 words; twice that for up to 64 tokens, whose g
