@@ -828,6 +828,16 @@ def _on_one_device(first, *others) -> None:
             _fail(-1, f"tensors are on {t.device} and {device}")
 
 
+def _no_tangent(**tensors) -> None:
+    """No tensor carries a forward-mode gradient, which the kernels would drop."""
+    forward_ad = _torch.autograd.forward_ad
+    if getattr(forward_ad, "_current_level", 0) < 0:
+        return
+    for name, t in tensors.items():
+        if forward_ad.unpack_dual(t).tangent is not None:
+            _fail(-4, f"{name} has a forward-mode tangent; only reverse mode is supported")
+
+
 def _vector(name: str, t, n: int, dtype) -> None:
     """t is a packed vector of n elements of dtype."""
     if t.shape != (n,):
@@ -1032,9 +1042,10 @@ def moe_route(logits, top_k: int, *, score: str = "softmax", bias=None, n_groups
     ids -1 and weights 0.
 
     Where the logits require a gradient, the weights carry it (the choice held
-    fixed; bias gets none).  out: (weights, ids) to write, which carry no
+    fixed; bias gets none; a forward-mode tangent is refused).  out: (weights, ids) to write, which carry no
     history: their gradient is a call of moe_route_backward."""
     lib, T = _lib_torch()
+    _no_tangent(logits=logits)
     if out is None and logits.requires_grad and T.is_grad_enabled():
         return _routed(logits, top_k, score, renorm, scale, {
             "bias": bias, "n_groups": n_groups, "top_groups": top_groups,
@@ -1184,11 +1195,12 @@ def moe_balance(logits, ids, *, score: str = "softmax", out=None, workspace=None
     do not count.
 
     Where the logits require a gradient, the loss carries it (the counts held
-    fixed).  out: (loss, counts, tokens) to write, which carry no history: their
+    fixed; a forward-mode tangent is refused).  out: (loss, counts, tokens) to write, which carry no history: their
     gradient is a call of moe_balance_backward.  workspace: a uint8 tensor of at
     least moe_balance_workspace_bytes(T, E) bytes; by default one is allocated
     for the call.  (A captured step with its backward: as for gemm_xent.)"""
     lib, T = _lib_torch()
+    _no_tangent(logits=logits)
     if out is None and logits.requires_grad and T.is_grad_enabled():
         return _balanced(logits, ids, score, workspace)
     ldl = _pitch("logits", logits)
@@ -1322,9 +1334,9 @@ def gemm_xent(A, B, targets, *, alpha: float = 1.0, out=None, workspace=None):
     softmax's divisor, loss = lse - the target's logit, or 0 for a token whose
     target lies outside [0, N).
 
-    Where A or B requires a gradient, loss and lse carry it.  out: (loss, lse)
-    to write, which overlap nothing and carry no history: their gradient is a
-    call of gemm_xent_backward.  workspace: a uint8 tensor of at least
+    Where A or B requires a gradient, loss and lse carry it (reverse mode: a
+    forward-mode tangent is refused).  out: (loss, lse) to write, which overlap
+    nothing and carry no history: their gradient is a call of gemm_xent_backward.  workspace: a uint8 tensor of at least
     gemm_xent_workspace_bytes(M, N, K) bytes; by default one is allocated for
     the call.
 
@@ -1333,6 +1345,7 @@ def gemm_xent(A, B, targets, *, alpha: float = 1.0, out=None, workspace=None):
     the stream of that one."""
     lib, T = _lib_torch()
     alpha = float(alpha)
+    _no_tangent(A=A, B=B)
     if out is None and (A.requires_grad or B.requires_grad) and T.is_grad_enabled():
         return _xent(A, B, targets, alpha, workspace)
     M, N, K, lda, ldb, dt, tt = _xent_args(A, B, targets)
