@@ -1371,7 +1371,9 @@ def gemm_xent_backward(dloss, A, B, targets, lse, *, alpha: float = 1.0, dlse=No
                        need=(True, True), out=None, workspace=None):
     """The gradients (dA [M][K], dB [N][K]), of A's and B's type, from dloss
     float32 [M], the gradient of gemm_xent's loss, and dlse float32 [M], that of
-    its lse (None: zero).  lse is gemm_xent's.
+    its lse (None: zero).  lse is gemm_xent's.  The gradient of the logits is
+    rounded to A's type on the way, up to 64 tokens to twice as many bits.  M is
+    below 2^22, and with dB the rows of A span less than 2^31 bytes.
 
     need: which of the two are computed; the other is None.  out: (dA, dB) to
     write (None: a new tensor), rows padded or not, that overlap no input and not

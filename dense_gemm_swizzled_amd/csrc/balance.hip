@@ -23,10 +23,12 @@ constexpr int kGradThreads = 256;
 // A token's scores over Lanes lanes with Quads quads of experts each (quad q of
 // the lane: experts from 4 * (q * Lanes + lane)), their sum, and for a sigmoid
 // 1 - s.  A masked logit scores zero; a token with all masked has the sum zero.
-// Nine instructions a logit for the loss, which with many tokens bounds it as
-// much as memory does (expf, a division and the masks of moe_rows.h made 16384 x
-// 256 fp32 take 1 us more): the exponentials are off by |x - top|, or |x| for a
-// sigmoid, units of 2^-24 of themselves, the rounding of their arguments.
+// With many tokens the pass waits for chains of these instructions as much as for
+// memory (its waves stand two thirds of their time, 27 to 29% of the vector issue
+// of 65521 x 128 is used), so they are few: expf, a division and the masks of
+// moe_rows.h made 16384 x 256 fp32 take 1 us more.  The exponentials are off by
+// |x - top|, or |x| for a sigmoid, units of 2^-24 of themselves, the rounding of
+// their arguments; the reciprocals, here and of the sums, by one unit.
 template <int Lanes, int Quads, bool Rest>
 __device__ __forceinline__ float scores(float (&x)[Quads][kHeld], float (&rest)[Quads][kHeld],
                                         bool soft) {

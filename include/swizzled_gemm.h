@@ -534,9 +534,15 @@ int64_t gemm_xent_workspace_bytes(int64_t M, int64_t N, int64_t K);
  *   dA = g*B,  dB = g^T*A,
  * dl = dloss, or 0 for a token without a target; g is 0 for a token whose dl and
  * dlse are 0, whatever its A holds (its row of dA is 0; dB adds 0 * A, so that A
- * has to be finite there).  The logits are computed again,
- * a run of words at a time; g is rounded to ab_dtype (fp16: scaled into its
- * range first, exactly), the sums are fp32, the results are rounded once.
+ * has to be finite there).  The logits are computed again, a run of words at a
+ * time.  g is rounded to ab_dtype, up to 64 tokens to twice as many bits; the sums
+ * are fp32, the results are rounded once.  For that the terms of both types are
+ * scaled by a power of two over the largest |dl| (of those that, with dlse, are
+ * numbers): that weight and its equals become the power of two, the others take
+ * one rounding of fp32 each, and in fp16 what is below 2^-38 of the largest is
+ * lost.  Error over the norm of dA and dB, beyond 64 tokens: 0.0017 to 0.0019 in
+ * bf16 with equal weights, 0.0023 with random ones (0.00166 is the rounding of
+ * the results), 0.00025 and 0.00029 in fp16 (0.00021).
  *   dloss    fp32 [M];  dlse  fp32 [M] or NULL (zero).
  *   lse      fp32 [M] as gemm_xent_run wrote it for the same A, B and alpha.
  *   dA       ab_dtype [M][ldda], or NULL: not wanted;  dB  ab_dtype [N][lddb],
@@ -545,11 +551,12 @@ int64_t gemm_xent_workspace_bytes(int64_t M, int64_t N, int64_t K);
  *            neither gradient replaces its operand (SG_ERR_ALIGN); rows of one
  *            pitch may lie side by side.
  *   workspace  DEVICE, gemm_xent_backward_workspace_bytes(M, N, K, ldb) bytes,
- *            16-byte aligned; as above.  It is 2 * M bytes a word of a run (at
- *            most 512 MB or 256 words; twice that for up to 64 tokens, whose g
- *            is kept to twice as many bits), 4 * M * K with several runs, and
- *            where dA has few tiles 4 * M * K for each of up to 32 shares of the
- *            words, so many that they fill the CUs.
+ *            16-byte aligned; as above.  Beside 16 bytes a token it holds g of
+ *            one run, 2 * M bytes a word (4 * M up to 64 tokens), at most 512 MB
+ *            or 256 words; with several runs 4 * M * K bytes; where dA has few
+ *            tiles 4 * M * K for each of up to 32 shares of the words, so many
+ *            that they fill the CUs.  Up to 64 tokens there is always a share,
+ *            each is 8 * M * K, and a second copy of A takes 4 * M * K.
  * M is below 2^22, and with dB the rows of A span less than 2^31 bytes.  The
  * other arguments and the errors are gemm_xent_run's.
  */
