@@ -101,3 +101,50 @@ def test_more_words_than_a_run_may_have(dtype):
     A, B, t = ref.inputs(M, N, K, dtype, 1, ignored=0.0)
     t[0], t[1], t[2] = 0, N - 1, 1 << 22
     check_back(torch.tensor([1.0, -2.0, 0.5], device="cuda"), A, B, t)
+
+
+@pytest.mark.parametrize("alpha", [-1.0, 0.5, 0.0])
+@pytest.mark.parametrize("M,N,K", [(40, 3001, 72), (4100, 4099, 64)])
+def test_scaled_logits_of_few_and_of_many_tokens(alpha, M, N, K):
+    """64x64 tiles with the gradient in two parts, and 256x256 tiles."""
+    A, B, t = ref.inputs(M, N, K, BF, 5, alpha=alpha)
+    loss, lse = sg.gemm_xent(A, B, t.to(torch.int32), alpha=alpha)
+    want = ref.forward(A, B, t, alpha)
+    close(loss, want[0], want[2], "loss")
+    close(lse, want[1], want[3], "lse")
+    gen = torch.Generator().manual_seed(1)
+    d, dlse = (torch.randn(M, generator=gen).cuda() for _ in range(2))
+    dA, dB = sg.gemm_xent_backward(d, A, B, t.to(torch.int32), lse, alpha=alpha, dlse=dlse)
+    wA, wB, bA, bB = ref.backward(d, A, B, t, alpha, dlse)
+    close(dA, wA, bA, "dA")
+    close(dB, wB, bB, "dB")
+
+
+def pitched(x, pitch, fill):
+    wide = torch.full((x.shape[0], pitch), fill, dtype=x.dtype, device="cuda")
+    wide[:, :x.shape[1]] = x
+    return wide[:, :x.shape[1]]
+
+
+@pytest.mark.parametrize("M,N,K", [(40, 600, 72), (200, 600, 72), (250, 70000, 64)])
+def test_the_widest_pitches(M, N, K):
+    """A's rows eight mebibytes apart (a panel of 256 of them just below 2^31 bytes),
+    B's too where they are few; gradients whose places need more than 32 bits."""
+    A, B, t = ref.inputs(M, N, K, BF, 6)
+    a = pitched(A, (1 << 22) - 8, math.nan)
+    b = pitched(B, (1 << 22) - 8, math.nan) if N < 1000 else B
+    loss, lse = sg.gemm_xent(a, b, t)
+    want = ref.forward(A, B, t, 1.0)
+    close(loss, want[0], want[2], "loss")
+    close(lse, want[1], want[3], "lse")
+    d = torch.rand(M, generator=torch.Generator().manual_seed(2)).cuda() / M
+    zero_A, zero_B = torch.zeros_like(A), torch.zeros_like(B)
+    out = pitched(zero_A, 1 << 24, 7.0) if M > 200 else zero_A, \
+        pitched(zero_B, 1 << 22, 7.0) if N < 1000 else zero_B
+    dA, dB = sg.gemm_xent_backward(d, a, b, t, lse, out=out)
+    wA, wB, bA, bB = ref.backward(d, A, B, t, 1.0)
+    close(dA, wA, bA, "dA")
+    close(dB, wB, bB, "dB")
+    # (what lies between the rows is left as it was)
+    base = dA._base if M > 200 else None
+    assert base is None or bool((base[:, K:K + 64] == 7).all())
