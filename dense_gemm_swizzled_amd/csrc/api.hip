@@ -725,7 +725,7 @@ bool overlap(const Area& a, const Area& b) {
   const uintptr_t pa = reinterpret_cast<uintptr_t>(a.at), pb = reinterpret_cast<uintptr_t>(b.at);
   if (pa > pb) return overlap(b, a);
   const uintptr_t from = pb - pa;
-  if (from >= (uintptr_t)(a.rows - 1) * a.pitch + a.width) return false;
+  if (from >= (uintptr_t)(a.rows - 1) * (uintptr_t)a.pitch + (uintptr_t)a.width) return false;
   const int64_t pitch = a.rows > 1 ? a.pitch : b.pitch;
   if (a.rows > 1 && b.rows > 1 && a.pitch != b.pitch) return true;
   const int64_t column = (int64_t)(from % (uintptr_t)pitch);
@@ -915,8 +915,11 @@ int gemm_xent_backward_run(int64_t M, int64_t N, int64_t K, float alpha, const f
   }
   if (const int rc = workspace_check(who, workspace, workspace_bytes, plan.bytes)) return rc;
   const int64_t of_targets = M * (target_dtype == SG_I64 ? 8 : 4);
-  const Area areas[] = {{"dA", dA, M, 2 * ldda, 2 * K},
-                        {"dB", dB, N, 2 * lddb, 2 * K},
+  auto pitch = [&](int64_t rows, int64_t ld) {  // (of a single row: any, not looked at)
+    return rows > 1 ? (int64_t)(2 * (uint64_t)ld) : 2 * K;
+  };
+  const Area areas[] = {{"dA", dA, M, pitch(M, ldda), 2 * K},
+                        {"dB", dB, N, pitch(N, lddb), 2 * K},
                         {"workspace", workspace, 1, plan.bytes, plan.bytes},
                         {"A", A, M, 2 * lda, 2 * K},
                         {"B", B, N, 2 * ldb, 2 * K},

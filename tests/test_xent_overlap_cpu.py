@@ -77,3 +77,15 @@ def test_rows_that_lie_in_each_other():
     refused(back(lda=wide, ldda=wide + 8, dA=AT["A"] + 2 * K), "gemm_xent_backward_run", "dA", "A")
 
 
+
+
+def test_pitches_that_no_memory_has():
+    """(A single row has none; a vocabulary of one word, then one token.)"""
+    huge = (1 << 62) + 64
+    for m, n in ((M, 1), (1, N)):
+        need = sg.gemm_xent_backward_workspace_bytes(m, n, K, K)
+        rc = sg.gemm_xent_backward_run(
+            m, n, K, 1.0, AT["dloss"], None, AT["A"], K, AT["B"], K, sg.SG_BF16, AT["targets"],
+            sg.SG_I64, AT["lse"], AT["A"] if m == 1 else None, huge,
+            AT["B"] if n == 1 else None, huge, AT["work"], need, None)
+        refused(rc, "gemm_xent_backward_run", "dA" if m == 1 else "dB")
